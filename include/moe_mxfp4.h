@@ -72,13 +72,18 @@ typedef enum {
   MOE_ERR_HIP = -4                  /* a HIP runtime call or launch failed     */
 } moe_status;
 
-typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype;
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_I8 = 3 } moe_dtype;
 
-/* Largest batch (activation rows) any entry point accepts. */
+/* Largest batch (activation rows) of the decode-layer, router_topk, MXFP4,
+ * norm and bf16 entry points.  moe_route and the 8-bit entry points below
+ * take prompts too: their limits stand with them. */
 #define MOE_MAX_BATCH 64
 /* Largest top_k and number of experts the router/top-k kernels accept. */
 #define MOE_MAX_TOPK 64
 #define MOE_MAX_EXPERTS 4096
+/* Largest number of rows (tokens) moe_route, quant_rows_i8, gemm_i8 and
+ * moe_combine accept: 2^24 - 1. */
+#define MOE_MAX_ROWS 0xFFFFFF
 
 /* Layout of the experts buffer (moe_layer_weights.expert_layout). */
 #define MOE_EXPERTS_CANONICAL 0 /* the blob layout described above             */
@@ -320,6 +325,145 @@ moe_status dense_gemv_bf16(const uint16_t* w, int n, int k, const uint16_t* x, i
 moe_status residual_add_bf16(float* h, const uint16_t* t, int batch, int hidden, void* stream);
 moe_status residual_add_rmsnorm_bf16(float* h, const uint16_t* t, int batch, int hidden, float eps, uint16_t* out,
                                      void* stream);
+
+/*
+ * moe_route -- scores of caller-computed router logits to experts and gates,
+ * for any number of rows (one decoding token to a long prompt).
+ *   logits      [rows][num_experts], bf16, fp16 or fp32 (`dtype`), row r at
+ *               logits + r * row_stride elements (row_stride >= num_experts)
+ *   bias        fp32 [num_experts] or NULL: added to the scores for the
+ *               selection only, never to the gates (a balance bias)
+ *   topk_idx    out int32 [rows][top_k]; topk_gate out fp32 [rows][top_k]
+ * For row r with logits l, over the candidates: the experts whose logit (and
+ * bias) is neither NaN nor -inf (a logit of +inf counts as the largest fp32):
+ *   s[e]    = exp(l[e]) / sum_i exp(l[i])  (MOE_SCORE_SOFTMAX)  or
+ *             1 / (1 + exp(-l[e]))         (MOE_SCORE_SIGMOID)
+ *   c[e]    = s[e] + bias[e]
+ *   groups  > 1: group g holds the num_experts / groups experts from
+ *           g * num_experts / groups on; its worth is the sum of the
+ *           group_top (1 or 2; fewer if it has fewer) largest c of its
+ *           candidates; the top_groups groups of the largest worth stay
+ *           (ties: the lower group; a group without candidates never stays)
+ *   S       = the top_k candidates of the remaining groups by (c descending,
+ *             index ascending); without a bias by (l descending, index
+ *             ascending), the same order where the scores are told apart
+ *   gate[j] = scale * s[S_j] / (renorm ? sum_i s[S_i] : 1); 0 if that sum is 0
+ * A row with fewer than top_k such candidates (a padded row has none) ends in
+ * index -1, gate 0.  Scores, sums and c are compared in fp64 (or so that the
+ * comparison has the same result), so two experts are in the order of the
+ * formula also where their fp32 scores would tie; gates are rounded once.
+ * 1 <= rows <= MOE_MAX_ROWS, 1 <= top_k <= min(64, top_groups * num_experts / groups),
+ * num_experts <= 4096 and a multiple of groups, 1 <= top_groups <= groups <=
+ * 64, group_top 1 or 2; groups == 1 needs top_groups == 1.  bias 4-byte
+ * aligned, logits aligned to their element.
+ */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+typedef struct {
+  int32_t num_experts, top_k;
+  int32_t score;                         /* MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID */
+  int32_t groups, top_groups, group_top; /* 1, 1, 1: no groups                     */
+  int32_t renorm;                        /* 0 or 1                                 */
+  float scale;
+} moe_route_params;
+moe_status moe_route(const void* logits, moe_dtype dtype, size_t row_stride, int rows, const float* bias,
+                     const moe_route_params* params, int32_t* topk_idx, float* topk_gate, void* stream);
+
+/*
+ * 8-bit integer products.  Activations are quantised per row (token), weights
+ * per output channel, both symmetrically; the products are summed exactly in
+ * int32 and scaled once.
+ *
+ * quant_rows_i8 -- rows to 8-bit codes with one scale each:
+ *   scale[m] = fp32( max_k |x[m][k]| / 127 )
+ *   q[m][k]  = the integer nearest to x[m][k] / scale[m] (the exact quotient,
+ *              ties to even), within +-127
+ *   x        [rows][k] bf16, fp16 or fp32, row m at x + m * x_stride elements
+ *   q        out int8 [rows][k]; scale out fp32 [rows]
+ * A row of zeros (or so small that its scale rounds to 0) has scale 0 and
+ * codes 0.  A row that holds a NaN or an infinity has scale NaN and codes 0,
+ * so every product of it is NaN.  1 <= rows <= MOE_MAX_ROWS, 1 <= k <= 65536.
+ */
+moe_status quant_rows_i8(const void* x, moe_dtype dtype, size_t x_stride, int rows, int k, int8_t* q, float* scale,
+                         void* stream);
+
+/*
+ * gemm_i8 -- y[m][n] = x_scale[m] * w_scale[n] * sum_k xq[m][k] * w[n][k]
+ *   x         x_dtype MOE_DTYPE_I8: the codes xq, with x_scale fp32 [m];
+ *             bf16, fp16 or fp32: rows that the call quantises as
+ *             quant_rows_i8 does, x_scale NULL
+ *             row i at x + i * x_stride elements, x_stride >= k
+ *   w         int8 [n][k] codes, w_scale fp32 [n]
+ *   swiglu    0, or 1: w is [2][n][k], gate then up, w_scale [2][n], and
+ *             y[m][i] = silu(g) * u of the two products g and u
+ *   y         out [m][n], bf16, fp16 or fp32 (y_dtype); must not alias x
+ *   ws        workspace of >= gemm_i8_workspace_size(...) bytes, 256-byte
+ *             aligned (may be NULL where that is 0).  It needs no
+ *             initialisation and holds nothing between calls.
+ * The sum is exact; it is rounded to fp32, multiplied by the two scales and
+ * rounded to y_dtype; SwiGLU runs in fp32 on the scaled sums.
+ * 1 <= m <= MOE_MAX_ROWS, 1 <= n <= 2^20, k a multiple of 16 in 16 .. 65536; 16-byte aligned x
+ * (x_stride a multiple of 16) if it is int8, else aligned to its element; w
+ * and y 16-byte aligned.
+ */
+size_t gemm_i8_workspace_size(int m, int n, int k, int swiglu, moe_dtype x_dtype);
+moe_status gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int m, int k,
+                   const int8_t* w, const float* w_scale, int n, int swiglu, void* y, moe_dtype y_dtype, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * moe_group_slots -- sort the slots s = t * top_k + j of a routing by expert.
+ *   idx      int32 [tokens][top_k], as moe_route or router_topk leave it; a
+ *            value outside 0 .. num_experts - 1 is a slot without an expert
+ *   groups   out, device buffer of >= moe_slot_groups_size(...) bytes,
+ *            256-byte aligned, holding
+ *              int32 order[tokens * top_k] at byte 0: the slots by expert,
+ *                ascending within one; slots without an expert come last
+ *              int32 offsets[num_experts + 2] at byte
+ *                MOE_GROUPS_OFFSETS(tokens, top_k): expert e has order[
+ *                offsets[e]] up to order[offsets[e + 1]] exclusive, and
+ *                num_experts names the slots without an expert
+ *            and lists that experts_gemm_i8 works through.
+ * 1 <= tokens, 1 <= top_k <= 64, num_experts <= 4096, tokens * top_k < 2^27.
+ * moe_slot_groups_size is 0 outside these limits.
+ */
+#define MOE_GROUPS_OFFSETS(tokens, top_k) ((((size_t)(tokens) * (size_t)(top_k) * 4 + 255) / 256) * 256)
+size_t moe_slot_groups_size(int tokens, int top_k, int num_experts);
+moe_status moe_group_slots(const int32_t* idx, int tokens, int top_k, int num_experts, void* groups,
+                           size_t groups_bytes, void* stream);
+
+/*
+ * experts_gemm_i8 -- gemm_i8 of every slot with its own expert's matrix:
+ *   y[s] = product of x[r] with w[expert of slot s];  zeros for a slot
+ *   without an expert
+ *   x_rows   tokens (row r = s / top_k: FC1) or tokens * top_k (row r = s:
+ *            FC2); with top_k 1 the two are the same
+ *   groups   as moe_group_slots left it for the same tokens, top_k and
+ *            num_experts
+ *   w        int8 [num_experts][n][k], w_scale fp32 [num_experts][n]; with
+ *            swiglu int8 [num_experts][2][n][k], w_scale [num_experts][2][n]
+ *   y        out [tokens * top_k][n]
+ * Types, alignments, limits, sums and workspace as gemm_i8;
+ * tokens, top_k and num_experts as moe_group_slots.
+ */
+size_t experts_gemm_i8_workspace_size(int tokens, int top_k, int num_experts, int x_rows, int n, int k, int swiglu,
+                                      moe_dtype x_dtype);
+moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int x_rows, int k,
+                           const void* groups, size_t groups_bytes, int tokens, int top_k, int num_experts,
+                           const int8_t* w, const float* w_scale, int n, int swiglu, void* y, moe_dtype y_dtype,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_combine -- out[t][h] = residual[t][h] + sum_j gate[t][j] * y[t*top_k + j][h]
+ *   y         [tokens * top_k][hidden], bf16, fp16 or fp32 (`dtype`)
+ *   gate      fp32 [tokens][top_k]
+ *   residual  fp32 [tokens][hidden], or NULL for zeros; may be out itself
+ *   out       fp32 [tokens][hidden]
+ * Summed in fp32, j ascending, then the residual.  1 <= tokens <=
+ * MOE_MAX_ROWS, 1 <= top_k <= 64, 1 <= hidden <= 2^20.  Pointers aligned to their element.
+ */
+moe_status moe_combine(const void* y, moe_dtype dtype, const float* gate, int tokens, int top_k, int hidden,
+                       const float* residual, float* out, void* stream);
 
 /*
  * moe_set_max_workgroups -- test and diagnostic knob, not needed for decoding:

@@ -17,7 +17,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_mxfp4.so")
 
 MOE_OK, MOE_ERR_INVALID_ARGUMENT, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_HIP = 0, -1, -2, -3, -4
-MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1
+MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_DTYPE_F16, MOE_DTYPE_I8 = 0, 1, 2, 3
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_EXPERTS_CANONICAL, MOE_EXPERTS_PACKED = 0, 1
 MAX_BATCH = 64
 
@@ -27,7 +28,9 @@ EXPORTS = ("moe_expert_bytes", "moe_workspace_size", "moe_router_workspace_size"
            "moe_decode_layer_kernel_name", "moe_decode_layer_timed", "moe_workspace_init", "moe_pack_experts",
            "moe_unpack_experts", "rmsnorm_bf16", "dense_gemv_bf16", "residual_add_bf16", "residual_add_rmsnorm_bf16",
            "moe_workspace_status", "moe_stream_read_probe", "moe_decode_layer_noalloc", "moe_decode_layer_mxfp8",
-           "moe_prefetch", "moe_set_max_workgroups", "moe_status_string")
+           "moe_prefetch", "moe_set_max_workgroups", "moe_status_string", "moe_route", "quant_rows_i8",
+           "gemm_i8_workspace_size", "gemm_i8", "moe_slot_groups_size", "moe_group_slots",
+           "experts_gemm_i8_workspace_size", "experts_gemm_i8", "moe_combine")
 
 
 class MoeError(RuntimeError):
@@ -81,6 +84,15 @@ def load():
         "moe_set_max_workgroups": (I, [I]),
         "moe_stream_read_probe": (I, [P, Z, I, P, P]),
         "moe_status_string": (ctypes.c_char_p, [I]),
+        "moe_route": (I, [P, I, Z, I, P, P, P, P, P]),
+        "quant_rows_i8": (I, [P, I, Z, I, I, P, P, P]),
+        "gemm_i8_workspace_size": (Z, [I, I, I, I, I]),
+        "gemm_i8": (I, [P, I, Z, P, I, I, P, P, I, I, P, I, P, Z, P]),
+        "moe_slot_groups_size": (Z, [I, I, I]),
+        "moe_group_slots": (I, [P, I, I, I, P, Z, P]),
+        "experts_gemm_i8_workspace_size": (Z, [I, I, I, I, I, I, I, I]),
+        "experts_gemm_i8": (I, [P, I, Z, P, I, I, P, Z, I, I, I, P, P, I, I, P, I, P, Z, P]),
+        "moe_combine": (I, [P, I, P, I, I, I, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -354,4 +366,234 @@ def residual_add_rmsnorm_bf16(h, t, eps: float = 1e-6, out=None, stream=None):
     out = torch.empty((B, H), dtype=torch.bfloat16, device=h.device) if out is None else out
     _check(load().residual_add_rmsnorm_bf16(_ptr(h), _ptr(t), B, H, float(eps), _ptr(out), _stream(stream)),
            "residual_add_rmsnorm_bf16")
+    return out
+
+
+# ---- routing, slots by expert, 8-bit products ---------------------------------------------------------------
+
+
+class RouteParamsC(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+_dtypes = None
+
+
+def _dtype_code(dtype, what: str, int8: bool = False) -> int:
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16,
+                   torch.int8: MOE_DTYPE_I8}
+    code = _dtypes.get(dtype)
+    if code is None or (code == MOE_DTYPE_I8 and not int8):
+        raise ValueError(f"{what} must be bfloat16, float16 or float32{' or int8' if int8 else ''}, not {dtype}")
+    return code
+
+
+def _want(t, shape, dtype, device, what: str):
+    """Checks a tensor that a kernel takes by address: shape, type, device, dense rows one after another."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, not "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _rows(t, what: str):
+    """Checks a matrix whose rows may lie apart; returns rows, columns and the row stride."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a matrix with consecutive elements in a row")
+    rows, cols = t.shape
+    stride = t.stride(0) if rows > 1 else cols
+    if stride < cols:
+        raise ValueError(f"{what} must not have overlapping rows")
+    return rows, cols, stride
+
+
+def _launch(what: str, device, stream, *args):
+    """Calls an entry point with `device` current, on the given stream or on that device's current one."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"{what} takes tensors on the GPU, not on {device}")
+    f = getattr(load(), what)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    s = ctypes.c_void_p(stream if isinstance(stream, int) else stream.cuda_stream)
+    if device.index == torch.cuda.current_device():
+        _check(f(*args, s), what)
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, s), what)
+
+
+def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int = 1, top_groups: int = 1,
+              group_top: int = 1, renorm: bool = True, scale: float = 1.0, idx=None, gate=None, stream=None):
+    """Router logits [rows][E] to experts and gates (moe_route): softmax or sigmoid scores, a bias for the
+    selection, groups of experts, renormalised gates. Returns (idx int32 [rows][k], gate fp32 [rows][k])."""
+    import torch
+    rows, E, stride = _rows(logits, "logits")
+    dev = logits.device
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, not {score!r}")
+    code = _dtype_code(logits.dtype, "logits")
+    if bias is not None:
+        _want(bias, (E,), torch.float32, dev, "bias")
+    p = RouteParamsC(E, top_k, _SCORES[score], groups, top_groups, group_top, int(renorm), scale)
+    shape = (rows, top_k)
+    idx = torch.empty(shape, dtype=torch.int32, device=dev) if idx is None else _want(idx, shape, torch.int32, dev, "idx")
+    gate = torch.empty(shape, dtype=torch.float32, device=dev) if gate is None else \
+        _want(gate, shape, torch.float32, dev, "gate")
+    _launch("moe_route", dev, stream, _ptr(logits), code, stride, rows, _ptr(bias), ctypes.byref(p), _ptr(idx), _ptr(gate))
+    return idx, gate
+
+
+def quant_rows_i8(x, q=None, scale=None, stream=None):
+    """Rows of x [rows][k] to 8-bit codes with one scale each (quant_rows_i8). Returns (q int8, scale fp32 [rows])."""
+    import torch
+    rows, k, stride = _rows(x, "x")
+    dev = x.device
+    code = _dtype_code(x.dtype, "x")
+    q = torch.empty((rows, k), dtype=torch.int8, device=dev) if q is None else _want(q, (rows, k), torch.int8, dev, "q")
+    scale = torch.empty((rows,), dtype=torch.float32, device=dev) if scale is None else \
+        _want(scale, (rows,), torch.float32, dev, "scale")
+    _launch("quant_rows_i8", dev, stream, _ptr(x), code, stride, rows, k, _ptr(q), _ptr(scale))
+    return q, scale
+
+
+def gemm_i8_workspace_size(m: int, n: int, k: int, swiglu: bool, x_dtype) -> int:
+    return int(load().gemm_i8_workspace_size(m, n, k, int(swiglu), _dtype_code(x_dtype, "x", int8=True)))
+
+
+def _i8_operands(x, x_scale, w, w_scale, swiglu: bool, lead: tuple):
+    """Shape checks shared by the two products; w is lead + [2][n][k] with swiglu, else lead + [n][k]."""
+    import torch
+    rows, k, stride = _rows(x, "x")
+    dev = x.device
+    parts = (2,) if swiglu else ()
+    if w.dim() != len(lead) + len(parts) + 2:
+        raise ValueError(f"w has {w.dim()} dimensions, not {len(lead) + len(parts) + 2}")
+    n = w.shape[-2]
+    _want(w, lead + parts + (n, k), torch.int8, dev, "w")
+    _want(w_scale, lead + parts + (n,), torch.float32, dev, "w_scale")
+    if (x_scale is not None) != (x.dtype == torch.int8):
+        raise ValueError("x_scale goes with int8 rows, and only with them")
+    if x_scale is not None:
+        _want(x_scale, (rows,), torch.float32, dev, "x_scale")
+    return rows, k, stride, n, _dtype_code(x.dtype, "x", int8=True)
+
+
+def _out(out, shape, out_dtype, device):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=device)
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out is {out.dtype}, not {out_dtype}")
+    return _want(out, shape, out.dtype, device, "out")
+
+
+def _workspace(ws, need: int, device):
+    import torch
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    return _want(ws, ws.shape, torch.uint8, device, "ws")
+
+
+def gemm_i8(x, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dtype=None, ws=None, stream=None):
+    """y = x w^T in 8-bit integers (gemm_i8): x [m][k] float rows, quantised on the way, or int8 codes with
+    x_scale [m]; w int8 [n][k] with w_scale [n], or [2][n][k] and [2][n] with swiglu. Returns y [m][n] in out's
+    type, out_dtype or bfloat16."""
+    m, k, stride, n, code = _i8_operands(x, x_scale, w, w_scale, swiglu, ())
+    dev = x.device
+    y = _out(out, (m, n), out_dtype, dev)
+    ws = _workspace(ws, 0 if ws is not None else load().gemm_i8_workspace_size(m, n, k, int(swiglu), code), dev)
+    _launch("gemm_i8", dev, stream, _ptr(x), code, stride, _ptr(x_scale), m, k, _ptr(w), _ptr(w_scale), n, int(swiglu),
+            _ptr(y), _dtype_code(y.dtype, "out"), _ptr(ws), 0 if ws is None else ws.numel())
+    return y
+
+
+@dataclass
+class SlotGroups:
+    """The slots of a routing by expert (moe_group_slots): `order` int32 [tokens * top_k] and `offsets` int32
+    [num_experts + 2] are views of `buffer`, which also holds what experts_gemm_i8 works through."""
+    tokens: int
+    top_k: int
+    num_experts: int
+    buffer: object
+    order: object
+    offsets: object
+
+
+def alloc_slot_groups(tokens: int, top_k: int, num_experts: int, device=None) -> SlotGroups:
+    import torch
+    size = int(load().moe_slot_groups_size(tokens, top_k, num_experts))
+    if not size:
+        raise ValueError(f"slot groups of {tokens} tokens, {top_k} slots each and {num_experts} experts are out of range")
+    buf = torch.empty(size, dtype=torch.uint8, device="cuda" if device is None else device)
+    slots = tokens * top_k
+    at = (4 * slots + 255) // 256 * 256
+    return SlotGroups(tokens, top_k, num_experts, buf, buf[:4 * slots].view(torch.int32),
+                      buf[at:at + 4 * (num_experts + 2)].view(torch.int32))
+
+
+def moe_group_slots(idx, num_experts: int, groups: Optional[SlotGroups] = None, stream=None) -> SlotGroups:
+    """Sort the slots of idx (int32 [tokens][k]) by expert (moe_group_slots)."""
+    import torch
+    if idx.dim() != 2:
+        raise ValueError("idx must be a matrix")
+    tokens, top_k = idx.shape
+    _want(idx, (tokens, top_k), torch.int32, idx.device, "idx")
+    if groups is None:
+        groups = alloc_slot_groups(tokens, top_k, num_experts, idx.device)
+    elif (groups.tokens, groups.top_k, groups.num_experts) != (tokens, top_k, num_experts) or \
+            groups.buffer.device != idx.device:
+        raise ValueError("groups were allocated for another shape or device")
+    _launch("moe_group_slots", idx.device, stream, _ptr(idx), tokens, top_k, num_experts, _ptr(groups.buffer),
+            groups.buffer.numel())
+    return groups
+
+
+def experts_gemm_i8_workspace_size(groups: SlotGroups, x_rows: int, n: int, k: int, swiglu: bool, x_dtype) -> int:
+    return int(load().experts_gemm_i8_workspace_size(groups.tokens, groups.top_k, groups.num_experts, x_rows, n, k,
+                                                     int(swiglu), _dtype_code(x_dtype, "x", int8=True)))
+
+
+def experts_gemm_i8(x, groups: SlotGroups, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dtype=None,
+                    ws=None, stream=None):
+    """gemm_i8 of every slot with its expert's matrix (experts_gemm_i8): x has a row per token or per slot, w is
+    int8 [num_experts][n][k] (or [num_experts][2][n][k] with swiglu). Returns y [tokens * top_k][n]."""
+    E = groups.num_experts
+    rows, k, stride, n, code = _i8_operands(x, x_scale, w, w_scale, swiglu, (E,))
+    dev = x.device
+    if rows != groups.tokens and rows != groups.tokens * groups.top_k:
+        raise ValueError(f"x has {rows} rows, neither the tokens nor the slots of the groups")
+    if groups.buffer.device != dev:
+        raise ValueError("groups are on another device")
+    y = _out(out, (groups.tokens * groups.top_k, n), out_dtype, dev)
+    need = 0 if ws is not None else load().experts_gemm_i8_workspace_size(groups.tokens, groups.top_k, E, rows, n, k,
+                                                                          int(swiglu), code)
+    ws = _workspace(ws, need, dev)
+    _launch("experts_gemm_i8", dev, stream, _ptr(x), code, stride, _ptr(x_scale), rows, k, _ptr(groups.buffer),
+            groups.buffer.numel(), groups.tokens, groups.top_k, E, _ptr(w), _ptr(w_scale), n, int(swiglu), _ptr(y),
+            _dtype_code(y.dtype, "out"), _ptr(ws), 0 if ws is None else ws.numel())
+    return y
+
+
+def moe_combine(y, gate, residual=None, out=None, stream=None):
+    """out[t] = residual[t] + sum_j gate[t][j] * y[t * k + j] (moe_combine), fp32 [tokens][hidden]; out may be
+    residual itself. Returns out."""
+    import torch
+    tokens, top_k = gate.shape
+    hidden = y.shape[-1]
+    dev = y.device
+    _want(gate, (tokens, top_k), torch.float32, dev, "gate")
+    _want(y, (tokens * top_k, hidden), y.dtype, dev, "y")
+    shape = (tokens, hidden)
+    if residual is not None:
+        _want(residual, shape, torch.float32, dev, "residual")
+    out = torch.empty(shape, dtype=torch.float32, device=dev) if out is None else _want(out, shape, torch.float32, dev, "out")
+    _launch("moe_combine", dev, stream, _ptr(y), _dtype_code(y.dtype, "y"), _ptr(gate), tokens, top_k, hidden,
+            _ptr(residual), _ptr(out))
     return out

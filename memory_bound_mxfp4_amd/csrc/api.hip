@@ -373,6 +373,195 @@ moe_status residual_add_rmsnorm_bf16(float* h, const uint16_t* t, int batch, int
   return MOE_OK;
 }
 
+// ---- routing, slots by expert, 8-bit products -------------------------------
+
+static bool float_dtype(moe_dtype t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32 || t == MOE_DTYPE_F16; }
+static size_t dtype_bytes(moe_dtype t) { return t == MOE_DTYPE_F32 ? 4 : t == MOE_DTYPE_I8 ? 1 : 2; }
+static constexpr int kMaxI8K = 65536;  // 127 * 128 * k stays inside int32
+static constexpr int kMaxCols = 1 << 20;
+
+moe_status moe_route(const void* logits, moe_dtype dtype, size_t row_stride, int rows, const float* bias,
+                     const moe_route_params* params, int32_t* topk_idx, float* topk_gate, void* stream) {
+  if (!logits || !params || !topk_idx || !topk_gate || !float_dtype(dtype) || rows < 1) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_route_params p = *params;
+  if (p.num_experts < 1 || p.top_k < 1 || p.groups < 1 || p.top_groups < 1 || p.top_groups > p.groups ||
+      p.num_experts % p.groups || (p.group_top != 1 && p.group_top != 2) || (p.renorm != 0 && p.renorm != 1) ||
+      (p.score != MOE_SCORE_SOFTMAX && p.score != MOE_SCORE_SIGMOID))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (p.top_k > p.top_groups * (p.num_experts / p.groups) || p.top_k > MOE_MAX_TOPK ||
+      row_stride < (size_t)p.num_experts)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(bias, 4) || !aligned(topk_idx, 4) || !aligned(topk_gate, 4))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (p.num_experts > MOE_MAX_EXPERTS || p.groups > 64 || rows > MOE_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+  if (launch_route(logits, dtype, row_stride, rows, bias, p, topk_idx, topk_gate, static_cast<hipStream_t>(stream)) !=
+      hipSuccess)
+    return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+moe_status quant_rows_i8(const void* x, moe_dtype dtype, size_t x_stride, int rows, int k, int8_t* q, float* scale,
+                         void* stream) {
+  if (!x || !q || !scale || !float_dtype(dtype) || rows < 1 || k < 1 || x_stride < (size_t)k)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(x, dtype_bytes(dtype)) || !aligned(scale, 4)) return MOE_ERR_INVALID_ARGUMENT;
+  if (k > kMaxI8K || rows > MOE_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+  if (launch_quant_rows(x, dtype, x_stride, rows, k, q, scale, static_cast<hipStream_t>(stream)) != hipSuccess)
+    return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+// The codes and scales of rows that a product quantises itself.
+struct QuantWs {
+  int8_t* q;
+  float* scale;
+  size_t bytes;
+};
+static QuantWs quant_ws(void* ws, int rows, int k) {
+  QuantWs w;
+  const size_t codes = align256((size_t)rows * k);
+  w.q = static_cast<int8_t*>(ws);
+  w.scale = reinterpret_cast<float*>(static_cast<char*>(ws) + codes);
+  w.bytes = codes + align256(4 * (size_t)rows);
+  return w;
+}
+
+static moe_status check_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int x_rows, int k,
+                           const int8_t* w, const float* w_scale, int n, int swiglu, const void* y, moe_dtype y_dtype) {
+  if (!x || !w || !w_scale || !y || x_rows < 1 || n < 1 || k < 16 || k % 16 || (swiglu != 0 && swiglu != 1))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!float_dtype(y_dtype) || !(float_dtype(x_dtype) || x_dtype == MOE_DTYPE_I8)) return MOE_ERR_INVALID_ARGUMENT;
+  if ((x_dtype == MOE_DTYPE_I8) != (x_scale != nullptr) || x_stride < (size_t)k) return MOE_ERR_INVALID_ARGUMENT;
+  if (x_dtype == MOE_DTYPE_I8 ? (!aligned(x, 16) || x_stride % 16) : !aligned(x, dtype_bytes(x_dtype)))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(w, 16) || !aligned(y, 16) || !aligned(w_scale, 4) || !aligned(x_scale, 4)) return MOE_ERR_INVALID_ARGUMENT;
+  if (k > kMaxI8K || n > kMaxCols || x_rows > MOE_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Quantises rows into the workspace if they are not codes already.
+static moe_status rows_to_i8(I8Args& a, const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale,
+                             int x_rows, int k, void* ws, size_t ws_bytes, hipStream_t s) {
+  a.x = static_cast<const int8_t*>(x);
+  a.x_stride = x_stride;
+  a.x_scale = x_scale;
+  if (x_dtype == MOE_DTYPE_I8) return MOE_OK;
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  const QuantWs w = quant_ws(ws, x_rows, k);
+  if (ws_bytes < w.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (launch_quant_rows(x, x_dtype, x_stride, x_rows, k, w.q, w.scale, s) != hipSuccess) return MOE_ERR_HIP;
+  a.x = w.q;
+  a.x_stride = (size_t)k;
+  a.x_scale = w.scale;
+  return MOE_OK;
+}
+
+size_t gemm_i8_workspace_size(int m, int n, int k, int swiglu, moe_dtype x_dtype) {
+  if (m < 1 || n < 1 || k < 1 || x_dtype == MOE_DTYPE_I8) return 0;
+  (void)swiglu;
+  return quant_ws(nullptr, m, k).bytes;
+}
+
+moe_status gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int m, int k,
+                   const int8_t* w, const float* w_scale, int n, int swiglu, void* y, moe_dtype y_dtype, void* ws,
+                   size_t ws_bytes, void* stream) {
+  moe_status st = check_i8(x, x_dtype, x_stride, x_scale, m, k, w, w_scale, n, swiglu, y, y_dtype);
+  if (st != MOE_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  I8Args a{};
+  st = rows_to_i8(a, x, x_dtype, x_stride, x_scale, m, k, ws, ws_bytes, s);
+  if (st != MOE_OK) return st;
+  a.rows = m;
+  a.k = k;
+  a.n = n;
+  a.w = w;
+  a.w_scale = w_scale;
+  a.swiglu = swiglu != 0;
+  a.y = y;
+  a.y_dtype = y_dtype;
+  a.num_experts = 1;
+  a.x_div = 1;
+  const int bm = i8_tile_rows(a);
+  if (launch_gemm_i8(a, bm, (int)(((size_t)m + bm - 1) / bm), s) != hipSuccess) return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+static bool slots_ok(int tokens, int top_k, int num_experts) {
+  return tokens >= 1 && top_k >= 1 && top_k <= MOE_MAX_TOPK && num_experts >= 1 && num_experts <= MOE_MAX_EXPERTS &&
+         (size_t)tokens * top_k < ((size_t)1 << 27);
+}
+
+size_t moe_slot_groups_size(int tokens, int top_k, int num_experts) {
+  return slots_ok(tokens, top_k, num_experts) ? groups_layout(tokens, top_k, num_experts).bytes : 0;
+}
+
+moe_status moe_group_slots(const int32_t* idx, int tokens, int top_k, int num_experts, void* groups,
+                           size_t groups_bytes, void* stream) {
+  if (!idx || !groups || !aligned(idx, 4) || !aligned(groups, 256) || !slots_ok(tokens, top_k, num_experts))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (groups_bytes < groups_layout(tokens, top_k, num_experts).bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (launch_group_slots(idx, tokens, top_k, num_experts, groups, static_cast<hipStream_t>(stream)) != hipSuccess)
+    return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+size_t experts_gemm_i8_workspace_size(int tokens, int top_k, int num_experts, int x_rows, int n, int k, int swiglu,
+                                      moe_dtype x_dtype) {
+  if (!slots_ok(tokens, top_k, num_experts) || x_rows < 1 || n < 1 || k < 1 || x_dtype == MOE_DTYPE_I8) return 0;
+  (void)swiglu;
+  return quant_ws(nullptr, x_rows, k).bytes;
+}
+
+moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int x_rows, int k,
+                           const void* groups, size_t groups_bytes, int tokens, int top_k, int num_experts,
+                           const int8_t* w, const float* w_scale, int n, int swiglu, void* y, moe_dtype y_dtype,
+                           void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_i8(x, x_dtype, x_stride, x_scale, x_rows, k, w, w_scale, n, swiglu, y, y_dtype);
+  if (st != MOE_OK) return st;
+  if (!groups || !aligned(groups, 256) || !slots_ok(tokens, top_k, num_experts)) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t slots = (size_t)tokens * top_k;
+  if (x_rows != tokens && (size_t)x_rows != slots) return MOE_ERR_INVALID_ARGUMENT;
+  const GroupsLayout g = groups_layout(tokens, top_k, num_experts);
+  if (groups_bytes < g.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  I8Args a{};
+  st = rows_to_i8(a, x, x_dtype, x_stride, x_scale, x_rows, k, ws, ws_bytes, s);
+  if (st != MOE_OK) return st;
+  const char* gp = static_cast<const char*>(groups);
+  a.rows = (int)slots;
+  a.k = k;
+  a.n = n;
+  a.w = w;
+  a.w_scale = w_scale;
+  a.swiglu = swiglu != 0;
+  a.y = y;
+  a.y_dtype = y_dtype;
+  a.num_experts = num_experts;
+  a.x_div = (size_t)x_rows == slots ? 1 : top_k;
+  a.order = reinterpret_cast<const int32_t*>(gp);
+  a.offsets = reinterpret_cast<const int32_t*>(gp + g.offsets);
+  const int bm = i8_tile_rows(a);
+  int map = 0;
+  while (map + 1 < kTileMaps && kTileRows[map] != bm) ++map;
+  a.num_tiles = reinterpret_cast<const int32_t*>(gp + g.counts) + map;
+  a.tiles = reinterpret_cast<const int2*>(gp + g.tiles[map]);
+  if (launch_gemm_i8(a, bm, g.max_tiles[map], s) != hipSuccess) return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+moe_status moe_combine(const void* y, moe_dtype dtype, const float* gate, int tokens, int top_k, int hidden,
+                       const float* residual, float* out, void* stream) {
+  if (!y || !gate || !out || !float_dtype(dtype) || tokens < 1 || top_k < 1 || top_k > MOE_MAX_TOPK || hidden < 1)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned(y, dtype_bytes(dtype)) || !aligned(gate, 4) || !aligned(residual, 4) || !aligned(out, 4))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (tokens > MOE_MAX_ROWS || hidden > kMaxCols) return MOE_ERR_UNSUPPORTED;
+  if (launch_combine(y, dtype, gate, tokens, top_k, hidden, residual, out, static_cast<hipStream_t>(stream)) !=
+      hipSuccess)
+    return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
 const char* moe_status_string(moe_status s) {
   switch (s) {
     case MOE_OK: return "MOE_OK";

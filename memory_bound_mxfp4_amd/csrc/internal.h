@@ -107,6 +107,50 @@ hipError_t launch_residual_add_rmsnorm(float* h, const uint16_t* t, int B, int H
 hipError_t launch_stream_read(const void* buf, size_t bytes, int blocks_per_cu, uint32_t* sink, hipStream_t s);
 hipError_t launch_prefetch(const moe_range* ranges, int n, int blocks, hipStream_t s);
 
+// ---- routing, slots by expert, 8-bit products ----
+hipError_t launch_route(const void* logits, int dtype, size_t row_stride, int rows, const float* bias,
+                        const moe_route_params& p, int32_t* idx, float* gate, hipStream_t s);
+
+// A slot-groups buffer: order at byte 0, then offsets, the number of tiles of
+// each map, and the maps.  Map i lists, for every expert that has slots (and
+// for the slots without one, as expert num_experts), the tiles of kTileRows[i]
+// of its positions: {expert, first position}.
+constexpr int kTileMaps = 2;
+constexpr int kTileRows[kTileMaps] = {16, 64};
+struct TileMaps {
+  int2* t[kTileMaps];
+};
+struct GroupsLayout {
+  size_t offsets, counts, tiles[kTileMaps];
+  int max_tiles[kTileMaps];
+  size_t bytes;
+};
+GroupsLayout groups_layout(int tokens, int top_k, int E);
+hipError_t launch_group_slots(const int32_t* idx, int tokens, int top_k, int E, void* groups, hipStream_t s);
+hipError_t launch_combine(const void* y, int dtype, const float* gate, int tokens, int top_k, int H,
+                          const float* residual, float* out, hipStream_t s);
+
+hipError_t launch_quant_rows(const void* x, int dtype, size_t x_stride, int rows, int K, int8_t* q, float* scale,
+                             hipStream_t s);
+
+struct I8Args {
+  const int8_t* x;
+  size_t x_stride;
+  const float* x_scale;
+  int rows, k, n;  // rows: positions of the product (dense rows, or slots)
+  const int8_t* w;
+  const float* w_scale;
+  bool swiglu;
+  void* y;
+  int y_dtype;
+  // grouped products; order NULL: dense
+  const int32_t *order, *offsets, *num_tiles;
+  const int2* tiles;
+  int num_experts, x_div;
+};
+int i8_tile_rows(const I8Args& a);
+hipError_t launch_gemm_i8(const I8Args& a, int tile_rows, int max_tiles, hipStream_t s);
+
 int num_cus();
 
 }  // namespace moe

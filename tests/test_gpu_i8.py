@@ -1,0 +1,447 @@
+"""GPU parity of the 8-bit integer operators (row quantiser, product, slots by
+expert, the experts' products, the gated sum) against plain 64-bit references,
+and a run of them together as a layer."""
+import numpy as np
+import pytest
+
+import i8_reference as ref
+import memory_bound_mxfp4_amd as moe
+
+pytestmark = pytest.mark.gpu
+
+
+def _dev(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _x(rows, k, dtype, seed, sigma=1.0):
+    """Random rows as a GPU tensor of the type, and their values in fp64."""
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    t = (torch.randn(rows, k, generator=g) * sigma).to(ref.torch_dtype(dtype))
+    return t.cuda(), t.double().numpy()
+
+
+def _w(shape, seed):
+    rng = np.random.default_rng(seed)
+    w = np.clip(np.rint(rng.standard_normal(shape) * 40), -128, 127).astype(np.int8)
+    return w, (rng.uniform(0.5, 1.5, shape[:-1]) * 1e-3).astype(np.float32)
+
+
+def _close(y, want, bound, what=""):
+    y = y.double().cpu().numpy()
+    bad = ~(np.abs(y - want) <= bound)
+    bad &= ~(np.isnan(y) & np.isnan(want))
+    assert not bad.any(), (what, np.argwhere(bad)[:4], y[bad][:4], want[bad][:4])
+
+
+# ---- rows to codes ----------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,k", [(1, 1), (1, 7168), (3, 5), (7, 16), (5, 130), (2, 1000), (300, 257), (9, 2048),
+                                    (4, 16384), (3, 20001), (2, 65536)])
+def test_quant_rows(dtype, rows, k):
+    x, v = _x(rows, k, dtype, rows * 7 + k, sigma=3.0)
+    q, s = moe.quant_rows_i8(x)
+    codes, scales = ref.quant(v)
+    assert np.array_equal(s.cpu().numpy().astype(np.float64), scales)
+    assert np.array_equal(q.cpu().numpy(), codes)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_quant_rows_borders(dtype):
+    """Quotients on and next to the middle between two codes, rows of zeros, the smallest and largest magnitudes."""
+    import torch
+    k = 512
+    t = torch.zeros(12, k, dtype=torch.float64)
+    t[0] = torch.arange(k) / 2.0 - 127.0            # scale 1: every half
+    t[0, -1] = 127.0
+    t[0] = t[0].clamp(-127, 127)
+    t[1] = t[0] * 0.5
+    t[2] = t[0] * 3.0 / 7.0
+    t[3] = 0.0
+    t[4, 5] = 2.0 ** -149                           # a scale that rounds to 0
+    t[5] = torch.arange(k) * 2.0 ** -149            # subnormals: codes past 127 are cut
+    t[6] = (torch.arange(k) - 200) * 2.0 ** -126
+    t[7] = torch.linspace(-1, 1, k) * 6e4
+    t[8] = torch.linspace(-1, 1, k) * 1e38
+    t[9, 0] = 3.0
+    t[10] = -0.0
+    t[11] = (torch.arange(k) % 255 - 127 + 0.5) * (1 + 2.0 ** -12)
+    x = t.to(ref.torch_dtype(dtype))
+    x = torch.where(torch.isinf(x), torch.zeros_like(x), x)
+    q, s = moe.quant_rows_i8(x.cuda())
+    codes, scales = ref.quant(x.double().numpy())
+    assert np.array_equal(s.cpu().numpy().astype(np.float64), scales)
+    assert np.array_equal(q.cpu().numpy(), codes), np.argwhere(q.cpu().numpy() != codes)[:5]
+
+
+def test_quant_rows_of_nan_and_infinity():
+    import torch
+    x = torch.randn(5, 300)
+    x[1, 299], x[2, 0], x[3, 17] = float("nan"), float("inf"), float("-inf")
+    for dtype in ("bf16", "f16", "f32"):
+        q, s = moe.quant_rows_i8(x.to(ref.torch_dtype(dtype)).cuda())
+        assert torch.isnan(s).tolist() == [False, True, True, True, False]
+        assert not q[1:4].any() and q[0].any() and q[4].any()
+
+
+def test_quant_rows_strides():
+    import torch
+    for dtype in ("bf16", "f32"):
+        wide, v = _x(6, 700, dtype, 3)
+        for part, pv in ((wide[:, 1:302], v[:, 1:302]), (wide[::2, 8:520], v[::2, 8:520]), (wide[:, 3:4], v[:, 3:4])):
+            q, s = moe.quant_rows_i8(part)
+            codes, scales = ref.quant(pv)
+            assert np.array_equal(q.cpu().numpy(), codes) and np.array_equal(s.cpu().numpy().astype(np.float64), scales)
+    q = torch.full((4, 64), 9, dtype=torch.int8, device="cuda")
+    s = torch.full((4,), 9.0, device="cuda")
+    x, v = _x(2, 64, "bf16", 1)
+    moe.quant_rows_i8(x, q=q[:2], scale=s[:2])
+    assert (q[2:] == 9).all() and (s[2:] == 9).all()
+
+
+# ---- the dense product --------------------------------------------------------------------------------------------
+
+SHAPES = [(1, 1, 16), (1, 16, 64), (1, 640, 7168), (2, 33, 48), (3, 17, 80), (5, 100, 1040), (16, 33, 256), (17, 100, 272),
+          (31, 64, 4096), (64, 96, 528), (65, 130, 1040), (100, 515, 336), (129, 257, 528), (256, 256, 128), (300, 512, 64),
+          (257, 1030, 400), (513, 770, 144), (1000, 1111, 272)]
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_gemm(m, n, k, swiglu):
+    kinds = ["bf16", "f16", "f32"]
+    dtype, out = kinds[(m + n) % 3], kinds[(n + k // 16) % 3]
+    x, v = _x(m, k, dtype, m + 3 * n + k)
+    w, ws = _w((2, n, k) if swiglu else (n, k), k + n)
+    y = moe.gemm_i8(x, _dev(w), _dev(ws), swiglu=swiglu, out_dtype=ref.torch_dtype(out))
+    codes, scales = ref.quant(v)
+    if swiglu:
+        g, u = ref.product(codes, scales, w[0], ws[0]), ref.product(codes, scales, w[1], ws[1])
+        _close(y, ref.silu(g) * u, ref.swiglu_bound(g, u, out))
+    else:
+        want = ref.product(codes, scales, w, ws)
+        _close(y, want, ref.product_bound(want, out))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m", [1, 20, 150])
+def test_gemm_types(dtype, out, m):
+    n, k = 200, 320
+    x, v = _x(m, k, dtype, m)
+    w, ws = _w((n, k), 8)
+    want = ref.product(*ref.quant(v), w, ws)
+    _close(moe.gemm_i8(x, _dev(w), _dev(ws), out_dtype=ref.torch_dtype(out)), want, ref.product_bound(want, out))
+
+
+@pytest.mark.parametrize("m", [1, 4, 40, 300])
+def test_gemm_of_codes(m):
+    """Rows that are codes already, rows apart, and the same answer as from the float rows."""
+    import torch
+    n, k = 150, 416
+    x, v = _x(m, k, "bf16", m)
+    w, ws = _w((n, k), 2)
+    q, s = moe.quant_rows_i8(x)
+    wide = torch.full((m, k + 48), 77, dtype=torch.int8, device="cuda")
+    wide[:, :k] = q
+    a = moe.gemm_i8(wide[:, :k], _dev(w), _dev(ws), x_scale=s, out_dtype=torch.float32)
+    b = moe.gemm_i8(x, _dev(w), _dev(ws), out_dtype=torch.float32)
+    assert torch.equal(a, b)
+    want = ref.product(*ref.quant(v), w, ws)
+    _close(a, want, ref.product_bound(want, "f32"))
+
+
+@pytest.mark.parametrize("m", [1, 17, 200])
+def test_gemm_float_rows_apart(m):
+    x, v = _x(m, 300, "f32", m)
+    w, ws = _w((70, 96), 4)
+    want = ref.product(*ref.quant(v[:, 5:101]), w, ws)
+    _close(moe.gemm_i8(x[:, 5:101], _dev(w), _dev(ws)), want, ref.product_bound(want, "bf16"))
+
+
+@pytest.mark.parametrize("m", [1, 16, 130])
+def test_gemm_largest_sums(m):
+    """Every code at its end, K at its limit: the sums stay inside int32 and exact."""
+    import torch
+    n, k = 40, 65536
+    q = torch.full((m, k), -128, dtype=torch.int8, device="cuda")
+    q[:, ::2] = 127
+    w = torch.full((n, k), -128, dtype=torch.int8, device="cuda")
+    w[::2] = 127
+    w[3] = q[0]
+    ones_m, ones_n = torch.ones(m, device="cuda"), torch.ones(n, device="cuda")
+    y = moe.gemm_i8(q, w, ones_n, x_scale=ones_m, out_dtype=torch.float32)
+    want = q[:1].cpu().numpy().astype(np.float64) @ w.cpu().numpy().astype(np.float64).T
+    _close(y, np.repeat(want, m, 0), np.abs(want) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("m", [3, 90])
+def test_gemm_bad_and_empty_rows(m):
+    """A row with a NaN gives a row of NaN and no other; a row of zeros gives zeros; far gates stay finite."""
+    import torch
+    n, k = 64, 128
+    x, _ = _x(m, k, "f32", 1)
+    x[1, 5] = float("nan")
+    x[2] = 0.0
+    w, ws = _w((2, n, k), 2)
+    y = moe.gemm_i8(x, _dev(w[0]), _dev(ws[0]), out_dtype=torch.float32)
+    assert torch.isnan(y[1]).all() and not torch.isnan(y[[0, 2]]).any() and (y[2] == 0).all()
+    h = moe.gemm_i8(x * 3e4, _dev(w), _dev(ws), swiglu=True, out_dtype=torch.float32)
+    assert torch.isnan(h[1]).all() and torch.isfinite(h[0]).all() and (h[2] == 0).all()
+
+
+def test_gemm_leaves_the_rest_alone():
+    import torch
+    for m, n in ((1, 50), (20, 50), (70, 260), (300, 300)):
+        x, _ = _x(m, 160, "bf16", m)
+        w, ws = _w((n, 160), 2)
+        buf = torch.full((m * n + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+        moe.gemm_i8(x, _dev(w), _dev(ws), out=buf[:m * n].view(m, n))
+        assert (buf[m * n:] == 7).all() and not (buf[:m * n] == 7).all()
+
+
+# ---- slots by expert ------------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("tokens,k,E", [(1, 1, 1), (1, 16, 896), (8, 16, 128), (64, 8, 256), (3, 2, 4096), (100, 64, 1500),
+                                        (1000, 6, 60), (777, 16, 896), (5000, 8, 64), (33333, 3, 1024), (40000, 8, 4096),
+                                        (20000, 16, 7)])
+def test_group_slots(tokens, k, E):
+    rng = np.random.default_rng(tokens + E)
+    idx = rng.integers(0, E, (tokens, k)).astype(np.int32)
+    idx[rng.random((tokens, k)) < 0.1] = -1
+    idx[rng.random((tokens, k)) < 0.02] = E
+    idx[0, 0] = 2 ** 31 - 1
+    order, offsets = ref.group_slots(idx, E)
+    g = moe.moe_group_slots(_dev(idx), E)
+    assert np.array_equal(g.offsets.cpu().numpy(), offsets)
+    assert np.array_equal(g.order.cpu().numpy(), order)
+
+
+@pytest.mark.parametrize("value", [-1, 0, 5])
+@pytest.mark.parametrize("tokens", [1, 130, 9000])
+def test_group_slots_all_alike(value, tokens):
+    idx = np.full((tokens, 4), value, np.int32)
+    order, offsets = ref.group_slots(idx, 6)
+    g = moe.moe_group_slots(_dev(idx), 6)
+    g = moe.moe_group_slots(_dev(idx), 6, groups=g)  # a buffer used again
+    assert np.array_equal(g.offsets.cpu().numpy(), offsets) and np.array_equal(g.order.cpu().numpy(), order)
+
+
+# ---- the experts' products ----------------------------------------------------------------------------------------
+
+
+def _experts_case(tokens, top_k, E, n, k, swiglu, by_slot, dtype, out, idx=None):
+    import torch
+    rng = np.random.default_rng(tokens * 13 + n + k)
+    if idx is None:
+        idx = rng.integers(-1, E, (tokens, top_k)).astype(np.int32)
+    x, v = _x(tokens * top_k if by_slot else tokens, k, dtype, tokens + k)
+    w, ws = _w((E, 2, n, k) if swiglu else (E, n, k), n)
+    g = moe.moe_group_slots(_dev(idx), E)
+    y = torch.full((tokens * top_k + 1, n), 5.0, dtype=ref.torch_dtype(out), device="cuda")
+    moe.experts_gemm_i8(x, g, _dev(w), _dev(ws), swiglu=swiglu, out=y[:-1])
+    assert (y[-1] == 5).all()
+    codes, scales = ref.quant(v)
+    want, bound = np.zeros((tokens * top_k, n)), np.full((tokens * top_k, n), 0.0)
+    flat = idx.reshape(-1)
+    for s in range(tokens * top_k):
+        e, r = flat[s], s if by_slot else s // top_k
+        if not 0 <= e < E:
+            continue
+        c, sc = codes[r:r + 1], scales[r:r + 1]
+        if swiglu:
+            a, b = ref.product(c, sc, w[e, 0], ws[e, 0]), ref.product(c, sc, w[e, 1], ws[e, 1])
+            want[s], bound[s] = (ref.silu(a) * b)[0], ref.swiglu_bound(a, b, out)[0]
+        else:
+            a = ref.product(c, sc, w[e], ws[e])
+            want[s], bound[s] = a[0], ref.product_bound(a, out)[0]
+    _close(y[:-1], want, bound)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("by_slot", [False, True])
+@pytest.mark.parametrize("tokens,top_k,E,n,k", [
+    (1, 1, 1, 16, 64), (1, 16, 32, 48, 272), (8, 6, 20, 33, 1040), (64, 2, 4, 130, 128), (50, 8, 3, 100, 80),
+    (333, 4, 5, 64, 144), (600, 2, 2, 260, 64)])
+def test_experts(tokens, top_k, E, n, k, swiglu, by_slot):
+    kinds = ["bf16", "f16", "f32"]
+    _experts_case(tokens, top_k, E, n, k, swiglu, by_slot, kinds[(n + E) % 3], kinds[(tokens + k // 16) % 3])
+
+
+@pytest.mark.parametrize("tokens", [1, 40, 400])
+@pytest.mark.parametrize("value", [-1, 2, 7])
+def test_experts_all_alike(tokens, value):
+    """No slot has an expert (zeros), one expert has every slot, an index that is past the last expert."""
+    _experts_case(tokens, 2, 6, 96, 112, False, False, "bf16", "bf16", idx=np.full((tokens, 2), value, np.int32))
+
+
+def test_experts_same_expert_twice_in_a_row():
+    _experts_case(5, 3, 4, 64, 64, False, True, "f32", "f32", idx=np.array([[1, 1, 1], [3, 3, 0], [0, 0, 0], [2, 1, 2], [3, 3, 3]],
+                                                                           np.int32))
+
+
+def test_experts_of_codes():
+    import torch
+    tokens, top_k, E, n, k = 30, 4, 8, 80, 192
+    idx = np.random.default_rng(0).integers(0, E, (tokens, top_k)).astype(np.int32)
+    x, _ = _x(tokens, k, "bf16", 3)
+    w, ws = _w((E, n, k), 1)
+    q, s = moe.quant_rows_i8(x)
+    g = moe.moe_group_slots(_dev(idx), E)
+    a = moe.experts_gemm_i8(x, g, _dev(w), _dev(ws))
+    assert torch.equal(a, moe.experts_gemm_i8(q, g, _dev(w), _dev(ws), x_scale=s))
+
+
+# ---- the gated sum --------------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("tokens,top_k,hidden", [(1, 1, 1), (1, 16, 7168), (3, 2, 33), (70, 8, 256), (9, 64, 100), (5, 3, 1030),
+                                                 (70000, 1, 8)])
+def test_combine(dtype, tokens, top_k, hidden):
+    import torch
+    y, v = _x(tokens * top_k, hidden, dtype, tokens)
+    rng = np.random.default_rng(hidden)
+    gate, res = rng.random((tokens, top_k)).astype(np.float32), rng.standard_normal((tokens, hidden)).astype(np.float32)
+    terms = v.reshape(tokens, top_k, hidden) * gate[:, :, None].astype(np.float64)
+    size = np.abs(terms).sum(1)
+    for r in (None, res):
+        want = terms.sum(1) + (0 if r is None else r)
+        bound = (size + (0 if r is None else np.abs(r))) * (top_k + 1) * 2.0 ** -24
+        rt = None if r is None else _dev(r)
+        got = moe.moe_combine(y, _dev(gate), residual=rt)
+        _close(got, want, bound)
+        if rt is not None:
+            moe.moe_combine(y, _dev(gate), residual=rt, out=rt)
+            assert torch.equal(rt, got)
+
+
+# ---- together ---------------------------------------------------------------------------------------------------------
+
+
+class _Layer:
+    """A mixture-of-experts block in 8 bits: routing, the experts' two products, the gated sum."""
+
+    def __init__(self, tokens, hidden, inter, E, top_k, seed=0):
+        import torch
+        self.E, self.k = E, top_k
+        self.w1, self.s1 = map(_dev, _w((E, 2, inter, hidden), seed))
+        self.w2, self.s2 = map(_dev, _w((E, hidden, inter), seed + 1))
+        self.bias = _dev((np.random.default_rng(seed).standard_normal(E) * 0.1).astype(np.float32))
+        empty = lambda *s, dtype: torch.empty(s, dtype=dtype, device="cuda")
+        self.idx, self.gate = empty(tokens, top_k, dtype=torch.int32), empty(tokens, top_k, dtype=torch.float32)
+        self.groups = moe.alloc_slot_groups(tokens, top_k, E)
+        self.h = empty(tokens * top_k, inter, dtype=torch.bfloat16)
+        self.y = empty(tokens * top_k, hidden, dtype=torch.bfloat16)
+        size = max(moe.experts_gemm_i8_workspace_size(self.groups, tokens, inter, hidden, True, torch.bfloat16),
+                   moe.experts_gemm_i8_workspace_size(self.groups, tokens * top_k, hidden, inter, False, torch.bfloat16))
+        self.ws = empty(size, dtype=torch.uint8)
+
+    def __call__(self, logits, x, residual, out, stream=None):
+        moe.moe_route(logits, self.k, bias=self.bias, score="sigmoid", groups=4, top_groups=2, group_top=2, scale=2.5,
+                      idx=self.idx, gate=self.gate, stream=stream)
+        moe.moe_group_slots(self.idx, self.E, groups=self.groups, stream=stream)
+        moe.experts_gemm_i8(x, self.groups, self.w1, self.s1, swiglu=True, out=self.h, ws=self.ws, stream=stream)
+        moe.experts_gemm_i8(self.h, self.groups, self.w2, self.s2, out=self.y, ws=self.ws, stream=stream)
+        return moe.moe_combine(self.y, self.gate, residual=residual, out=out, stream=stream)
+
+    def reference(self, logits, x, residual):
+        idx, gate = ref.route(logits, self.k, bias=self.bias.cpu().numpy(), score="sigmoid", groups=4, top_groups=2,
+                              group_top=2, scale=2.5)
+        w1, s1, w2, s2 = (t.cpu().numpy() for t in (self.w1, self.s1, self.w2, self.s2))
+        out = residual.astype(np.float64).copy()
+        c, s = ref.quant(x)
+        for t in range(x.shape[0]):
+            for j in range(self.k):
+                e = idx[t, j]
+                if e < 0:
+                    continue
+                g, u = (ref.product(c[t:t + 1], s[t:t + 1], w1[e, p], s1[e, p]) for p in (0, 1))
+                out[t] += gate[t, j] * ref.product(*ref.quant(ref.silu(g) * u), w2[e], s2[e])[0]
+        return idx, out
+
+
+def _layer_inputs(tokens, hidden, E, seed):
+    import torch
+    rng = np.random.default_rng(seed)
+    logits = (rng.standard_normal((tokens, E)) * 1.7).astype(np.float32)
+    if tokens > 2:
+        logits[tokens - 2:] = -np.inf  # padded rows
+    x, v = _x(tokens, hidden, "bf16", seed)
+    residual = rng.standard_normal((tokens, hidden)).astype(np.float32)
+    return logits, x, v, residual
+
+
+@pytest.mark.parametrize("tokens,hidden,inter", [(1, 512, 256), (7, 256, 128), (150, 256, 144)])
+def test_layer(tokens, hidden, inter):
+    """The operators in a row against the chain in 64 bits.  Codes of the inner rows that lie next to a border may
+    fall on the other side (their bf16 rounding moves them by up to 2^-9 of a value, half a code at most): the row's
+    relative error stays under 2 * 2^-9 """
+    import torch
+    E, k = 16, 4
+    layer = _Layer(tokens, hidden, inter, E, k)
+    logits, x, v, residual = _layer_inputs(tokens, hidden, E, tokens)
+    out = torch.empty(tokens, hidden, device="cuda")
+    layer(_dev(logits), x, _dev(residual), out)
+    idx, want = layer.reference(logits, v, residual)
+    assert np.array_equal(layer.idx.cpu().numpy(), idx)
+    got = out.cpu().numpy().astype(np.float64)
+    part = want - residual
+    err = np.linalg.norm(got - want, axis=1) / np.maximum(np.linalg.norm(part, axis=1), 1e-30)
+    assert (err[np.linalg.norm(part, axis=1) > 0] <= 2e-2).all(), err.max()
+    empty = (idx < 0).all(1)
+    assert np.array_equal(got[empty], residual[empty].astype(np.float64))
+
+
+@pytest.mark.parametrize("tokens", [1, 37, 300])
+def test_layer_in_a_graph_and_on_another_stream(tokens):
+    """Captured once and replayed on new inputs, with the program's own eager work in between; and eagerly on a side
+    stream: the same bits as an eager run."""
+    import torch
+    hidden, inter, E, k = 256, 128, 16, 4
+    layer, check = _Layer(tokens, hidden, inter, E, k), _Layer(tokens, hidden, inter, E, k)
+    ins = [_layer_inputs(tokens, hidden, E, 50 + i) for i in range(4)]
+    logits, x, res, out = _dev(ins[0][0]), ins[0][1].clone(), _dev(ins[0][3]), torch.empty(tokens, hidden, device="cuda")
+    want_out = torch.empty_like(out)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        layer(logits, x, res, out)
+    s.synchronize()
+    check(logits, x, res, want_out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want_out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        layer(logits, x, res, out)
+    for lg, xi, _, ri in ins + ins[:2]:
+        logits.copy_(_dev(lg))
+        x.copy_(xi)
+        res.copy_(_dev(ri))
+        torch.cuda.synchronize()
+        graph.replay()
+        check(logits, x, res, want_out)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want_out)
+
+
+def test_two_streams_at_once():
+    """Two layers with their own buffers on two streams: each has the bits of a run alone."""
+    import torch
+    hidden, inter, E, k, tokens = 256, 128, 16, 4, 200
+    layers = [_Layer(tokens, hidden, inter, E, k, seed=i) for i in range(2)]
+    ins = [_layer_inputs(tokens, hidden, E, i) for i in range(2)]
+    dev = [(_dev(i[0]), i[1], _dev(i[3])) for i in ins]
+    alone = [l(*d, torch.empty(tokens, hidden, device="cuda")).clone() for l, d in zip(layers, dev)]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [torch.empty(tokens, hidden, device="cuda") for _ in range(2)]
+    for _ in range(5):
+        for l, d, s, o in zip(layers, dev, streams, outs):
+            l(*d, o, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(alone, outs))

@@ -1,0 +1,171 @@
+"""The routing and 8-bit entry points turn bad arguments down on the host,
+before anything is enqueued (no GPU needed), and the binding checks what the
+C interface cannot see."""
+import ctypes
+
+import pytest
+
+import memory_bound_mxfp4_amd as moe
+
+P = ctypes.c_void_p
+BF16, F32, F16, I8 = moe.MOE_DTYPE_BF16, moe.MOE_DTYPE_F32, moe.MOE_DTYPE_F16, moe.MOE_DTYPE_I8
+INVALID, UNSUPPORTED, SMALL = moe.MOE_ERR_INVALID_ARGUMENT, moe.MOE_ERR_UNSUPPORTED, moe.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+def _route(**over):
+    a = dict(logits=P(0x1000), dtype=F32, stride=256, rows=4, bias=None, E=256, k=8, score=0, groups=8, top_groups=4,
+             group_top=2, renorm=1, scale=1.0, idx=P(0x2000), gate=P(0x3000))
+    a.update(over)
+    p = moe.RouteParamsC(a["E"], a["k"], a["score"], a["groups"], a["top_groups"], a["group_top"], a["renorm"], a["scale"])
+    return moe.load().moe_route(a["logits"], a["dtype"], a["stride"], a["rows"], a["bias"], ctypes.byref(p), a["idx"],
+                                a["gate"], None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(logits=None), dict(idx=None), dict(gate=None), dict(dtype=I8), dict(dtype=9), dict(stride=255), dict(rows=0),
+    dict(E=0), dict(k=0), dict(k=65), dict(k=129, top_groups=4), dict(score=2), dict(groups=0), dict(groups=7),
+    dict(top_groups=0), dict(top_groups=9), dict(group_top=0), dict(group_top=3), dict(renorm=2),
+    dict(k=33, top_groups=1), dict(logits=P(0x1002)), dict(logits=P(0x1001), dtype=F16), dict(bias=P(0x1002)),
+    dict(groups=1, top_groups=2)], ids=str)
+def test_route_invalid(over):
+    assert _route(**over) == INVALID
+
+
+def test_route_unsupported():
+    assert _route(E=4104, stride=4104) == UNSUPPORTED
+    assert _route(E=260, stride=260, groups=65, top_groups=65) == UNSUPPORTED
+    assert _route(rows=1 << 24) == UNSUPPORTED
+    assert moe.load().moe_route(P(0x1000), F32, 8, 1, None, None, P(0x2000), P(0x3000), None) == INVALID
+
+
+def test_quant_refusals():
+    f = moe.load().quant_rows_i8
+    x, q, s = P(0x1000), P(0x2000), P(0x3000)
+    for args in ((None, BF16, 64, 1, 64, q, s), (x, BF16, 64, 1, 64, None, s), (x, BF16, 64, 1, 64, q, None),
+                 (x, I8, 64, 1, 64, q, s), (x, BF16, 63, 2, 64, q, s), (x, BF16, 64, 0, 64, q, s),
+                 (x, BF16, 64, 1, 0, q, s), (P(0x1001), BF16, 64, 1, 64, q, s), (P(0x1002), F32, 64, 1, 64, q, s),
+                 (x, BF16, 64, 1, 64, q, P(0x3002))):
+        assert f(*args, None) == INVALID, args
+    assert f(x, BF16, 65537, 1, 65537, q, s, None) == UNSUPPORTED
+    assert f(x, BF16, 64, 1 << 24, 64, q, s, None) == UNSUPPORTED
+
+
+def _gemm(**over):
+    a = dict(x=P(0x1000), xd=BF16, stride=64, xs=None, m=4, k=64, w=P(0x2000), ws=P(0x3000), n=32, swiglu=0,
+             y=P(0x4000), yd=BF16, work=P(0x10000), size=1 << 20)
+    a.update(over)
+    return moe.load().gemm_i8(a["x"], a["xd"], a["stride"], a["xs"], a["m"], a["k"], a["w"], a["ws"], a["n"], a["swiglu"],
+                              a["y"], a["yd"], a["work"], a["size"], None)
+
+
+BAD_PRODUCT = [
+    dict(x=None), dict(w=None), dict(ws=None), dict(y=None), dict(m=0), dict(n=0), dict(k=0), dict(k=8), dict(k=40),
+    dict(stride=48), dict(swiglu=2), dict(xd=7), dict(yd=I8), dict(yd=5), dict(xd=I8), dict(xs=P(0x5000)),
+    dict(xd=I8, xs=P(0x5000), stride=72), dict(xd=I8, xs=P(0x5000), x=P(0x1008)), dict(x=P(0x1001)),
+    dict(w=P(0x2008)), dict(y=P(0x4008)), dict(ws=P(0x3002)), dict(work=None), dict(work=P(0x10010))]
+
+
+@pytest.mark.parametrize("over", BAD_PRODUCT, ids=str)
+def test_gemm_invalid(over):
+    assert _gemm(**over) == INVALID
+
+
+def test_gemm_unsupported_and_workspace():
+    assert _gemm(k=65552, stride=65552) == UNSUPPORTED
+    assert _gemm(n=(1 << 20) + 1) == UNSUPPORTED
+    assert _gemm(m=1 << 24) == UNSUPPORTED
+    need = moe.load().gemm_i8_workspace_size(4, 32, 64, 0, BF16)
+    assert need > 0 and _gemm(size=need - 1) == SMALL
+
+
+def test_groups_refusals():
+    lib = moe.load()
+    idx, buf = P(0x1000), P(0x10000)
+    assert lib.moe_slot_groups_size(0, 1, 8) == 0 and lib.moe_slot_groups_size(1, 65, 8) == 0
+    assert lib.moe_slot_groups_size(1, 1, 0) == 0 and lib.moe_slot_groups_size(1, 1, 4097) == 0
+    assert lib.moe_slot_groups_size(1 << 23, 16, 8) == 0
+    need = lib.moe_slot_groups_size(4, 2, 8)
+    assert need >= 4 * 8 + 4 * 10
+    assert lib.moe_group_slots(None, 4, 2, 8, buf, need, None) == INVALID
+    assert lib.moe_group_slots(idx, 4, 2, 8, None, need, None) == INVALID
+    assert lib.moe_group_slots(idx, 4, 2, 8, P(0x10010), need, None) == INVALID
+    assert lib.moe_group_slots(P(0x1002), 4, 2, 8, buf, need, None) == INVALID
+    assert lib.moe_group_slots(idx, 4, 2, 0, buf, need, None) == INVALID
+    assert lib.moe_group_slots(idx, 4, 2, 8, buf, need - 1, None) == SMALL
+
+
+def _experts(**over):
+    a = dict(x=P(0x1000), xd=BF16, stride=64, xs=None, rows=4, k=64, g=P(0x20000), gb=1 << 20, tokens=4, top_k=2, E=8,
+             w=P(0x2000), ws=P(0x3000), n=32, swiglu=0, y=P(0x4000), yd=BF16, work=P(0x10000), size=1 << 20)
+    a.update(over)
+    if "m" in over:
+        a["rows"] = over["m"]
+    return moe.load().experts_gemm_i8(a["x"], a["xd"], a["stride"], a["xs"], a["rows"], a["k"], a["g"], a["gb"],
+                                      a["tokens"], a["top_k"], a["E"], a["w"], a["ws"], a["n"], a["swiglu"], a["y"],
+                                      a["yd"], a["work"], a["size"], None)
+
+
+@pytest.mark.parametrize("over", BAD_PRODUCT + [
+    dict(g=None), dict(g=P(0x20080)), dict(rows=5), dict(rows=2), dict(tokens=0), dict(top_k=0), dict(top_k=65),
+    dict(E=0), dict(E=4097)], ids=str)
+def test_experts_invalid(over):
+    assert _experts(**over) == INVALID
+
+
+def test_experts_workspaces():
+    lib = moe.load()
+    assert _experts(gb=lib.moe_slot_groups_size(4, 2, 8) - 1) == SMALL
+    assert _experts(size=lib.experts_gemm_i8_workspace_size(4, 2, 8, 4, 32, 64, 0, BF16) - 1) == SMALL
+
+
+def test_combine_refusals():
+    f = moe.load().moe_combine
+    y, g, r, o = P(0x1000), P(0x2000), P(0x3000), P(0x4000)
+    for args in ((None, BF16, g, 1, 2, 64, r, o), (y, BF16, None, 1, 2, 64, r, o), (y, BF16, g, 1, 2, 64, r, None),
+                 (y, I8, g, 1, 2, 64, r, o), (y, BF16, g, 0, 2, 64, r, o), (y, BF16, g, 1, 0, 64, r, o),
+                 (y, BF16, g, 1, 65, 64, r, o), (y, BF16, g, 1, 2, 0, r, o), (P(0x1001), BF16, g, 1, 2, 64, r, o),
+                 (y, BF16, P(0x2002), 1, 2, 64, r, o), (y, BF16, g, 1, 2, 64, P(0x3002), o),
+                 (y, BF16, g, 1, 2, 64, r, P(0x4002))):
+        assert f(*args, None) == INVALID, args
+    assert f(y, BF16, g, 1, 2, (1 << 20) + 1, r, o, None) == UNSUPPORTED
+    assert f(y, BF16, g, 1 << 24, 2, 64, r, o, None) == UNSUPPORTED
+
+
+def test_binding_checks():
+    """What the binding sees and the C interface cannot: types, shapes, strides and devices of tensors."""
+    import torch
+    x, w, s = torch.zeros(4, 64), torch.zeros(32, 64, dtype=torch.int8), torch.zeros(32)
+    for call in (
+            lambda: moe.gemm_i8(x, w, s),                                  # on the CPU
+            lambda: moe.gemm_i8(x.double(), w, s),                         # type of x
+            lambda: moe.gemm_i8(x, w.float(), s),                          # type of w
+            lambda: moe.gemm_i8(x, w, s.double()),
+            lambda: moe.gemm_i8(x, w[:, :48], s),                          # k of w, and not contiguous
+            lambda: moe.gemm_i8(x, w, s[:31]),
+            lambda: moe.gemm_i8(x, w, s, swiglu=True),                     # w needs two matrices
+            lambda: moe.gemm_i8(x, w, s, x_scale=torch.zeros(4)),          # scales of rows that are no codes
+            lambda: moe.gemm_i8(x.to(torch.int8), w, s),                   # codes without scales
+            lambda: moe.gemm_i8(x.t(), w, s),                              # elements apart
+            lambda: moe.gemm_i8(x, w, s, out=torch.zeros(4, 31)),
+            lambda: moe.gemm_i8(x, w, s, out=torch.zeros(4, 32), out_dtype=torch.float16),
+            lambda: moe.moe_route(x, 2, score="other"),
+            lambda: moe.moe_route(x, 2, bias=torch.zeros(63)),
+            lambda: moe.moe_route(x.expand(4, 64).t(), 2),
+            lambda: moe.moe_route(x.to(torch.int8), 2),
+            lambda: moe.moe_route(x[:1].expand(4, 64), 2),                 # rows on top of each other
+            lambda: moe.quant_rows_i8(x, q=torch.zeros(4, 64)),
+            lambda: moe.moe_group_slots(torch.zeros(4, 2), 8),
+            lambda: moe.alloc_slot_groups(4, 2, 5000, device="cpu"),
+            lambda: moe.moe_combine(torch.zeros(8, 16), torch.zeros(4, 3)),
+    ):
+        with pytest.raises(ValueError):
+            call()
+    groups = moe.alloc_slot_groups(4, 2, 8, device="cpu")
+    assert groups.order.shape == (8,) and groups.offsets.shape == (10,)
+    wide, scales = torch.zeros(8, 32, 64, dtype=torch.int8), torch.zeros(8, 32)
+    with pytest.raises(ValueError):
+        moe.experts_gemm_i8(torch.zeros(5, 64), groups, wide, scales)
+    with pytest.raises(ValueError):
+        moe.experts_gemm_i8(x, groups, wide[:7], scales[:7])
+    with pytest.raises(ValueError):
+        moe.moe_group_slots(torch.zeros(4, 2, dtype=torch.int32), 9, groups=groups)
