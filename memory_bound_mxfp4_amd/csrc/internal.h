@@ -115,8 +115,8 @@ hipError_t launch_route(const void* logits, int dtype, size_t row_stride, int ro
 // each map, and the maps.  Map i lists, for every expert that has slots (and
 // for the slots without one, as expert num_experts), the tiles of kTileRows[i]
 // of its positions: {expert, first position}.
-constexpr int kTileMaps = 2;
-constexpr int kTileRows[kTileMaps] = {16, 64};
+constexpr int kTileMaps = 3;
+constexpr int kTileRows[kTileMaps] = {16, 64, 256};
 struct TileMaps {
   int2* t[kTileMaps];
 };
