@@ -35,6 +35,26 @@ struct Elem<MOE_DTYPE_F32> {
   static constexpr int bytes = 4;
 };
 
+// 16 bytes of a row: 8 elements of 2 bytes or 4 of 4.
+template <int DT>
+struct Chunk {
+  static constexpr int N = 16 / Elem<DT>::bytes;
+  static __device__ __forceinline__ void widen(const u32x4& c, float* v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == MOE_DTYPE_BF16) {
+        v[2 * i] = bf16_lo(c[i]);
+        v[2 * i + 1] = bf16_hi(c[i]);
+      } else if constexpr (DT == MOE_DTYPE_F16) {
+        v[2 * i] = __half2float(__ushort_as_half((uint16_t)c[i]));
+        v[2 * i + 1] = __half2float(__ushort_as_half((uint16_t)(c[i] >> 16)));
+      } else {
+        v[i] = __uint_as_float(c[i]);
+      }
+    }
+  }
+};
+
 __device__ __forceinline__ uint16_t f32_to_f16(float f) { return __half_as_ushort(__float2half(f)); }
 
 __device__ __forceinline__ void store_y(void* y, int dtype, size_t i, float v) {

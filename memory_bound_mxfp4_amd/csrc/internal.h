@@ -121,8 +121,9 @@ struct TileMaps {
   int2* t[kTileMaps];
 };
 struct GroupsLayout {
-  size_t offsets, counts, tiles[kTileMaps];
+  size_t offsets, counts, tiles[kTileMaps], hist;
   int max_tiles[kTileMaps];
+  int blocks;  // workgroups of the sort
   size_t bytes;
 };
 GroupsLayout groups_layout(int tokens, int top_k, int E);
