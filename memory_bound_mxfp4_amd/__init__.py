@@ -379,38 +379,49 @@ class RouteParamsC(ctypes.Structure):
 
 
 _SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
-_dtypes = None
+_dtypes: dict = {}
+
+
+def _torch():
+    import torch
+    if not _dtypes:
+        _dtypes.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16})
+    return torch
 
 
 def _dtype_code(dtype, what: str, int8: bool = False) -> int:
-    global _dtypes
-    if _dtypes is None:
-        import torch
-        _dtypes = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16,
-                   torch.int8: MOE_DTYPE_I8}
+    torch = _torch()
     code = _dtypes.get(dtype)
-    if code is None or (code == MOE_DTYPE_I8 and not int8):
-        raise ValueError(f"{what} must be bfloat16, float16 or float32{' or int8' if int8 else ''}, not {dtype}")
-    return code
+    if code is not None:
+        return code
+    if int8 and dtype == torch.int8:
+        return MOE_DTYPE_I8
+    raise ValueError(f"{what} must be bfloat16, float16 or float32{' or int8' if int8 else ''}, not {dtype}")
 
 
-def _want(t, shape, dtype, device, what: str):
+def _want(t, shape: tuple, dtype, device, what: str):
     """Checks a tensor that a kernel takes by address: shape, type, device, dense rows one after another."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, not "
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on {device}, not "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t
 
 
 def _rows(t, what: str):
     """Checks a matrix whose rows may lie apart; returns rows, columns and the row stride."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be a matrix with consecutive elements in a row")
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be a matrix")
     rows, cols = t.shape
+    if t.is_contiguous():
+        return rows, cols, cols
     stride = t.stride(0) if rows > 1 else cols
-    if stride < cols:
-        raise ValueError(f"{what} must not have overlapping rows")
+    if (cols > 1 and t.stride(1) != 1) or stride < cols:
+        raise ValueError(f"{what} must have consecutive elements in a row and rows that do not overlap")
     return rows, cols, stride
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _launch(what: str, device, stream, *args):
@@ -418,22 +429,25 @@ def _launch(what: str, device, stream, *args):
     import torch
     if device.type != "cuda":
         raise ValueError(f"{what} takes tensors on the GPU, not on {device}")
-    f = getattr(load(), what)
+    f = getattr(_lib or load(), what)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    s = ctypes.c_void_p(stream if isinstance(stream, int) else stream.cuda_stream)
+        s = torch._C._cuda_getCurrentRawStream(device.index)  # as current_stream(device), without building a Stream
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        _check(f(*args, s), what)
+        rc = f(*args, s)
     else:
         with torch.cuda.device(device):
-            _check(f(*args, s), what)
+            rc = f(*args, s)
+    if rc != MOE_OK:
+        raise MoeError(rc, what)
 
 
 def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int = 1, top_groups: int = 1,
               group_top: int = 1, renorm: bool = True, scale: float = 1.0, idx=None, gate=None, stream=None):
     """Router logits [rows][E] to experts and gates (moe_route): softmax or sigmoid scores, a bias for the
     selection, groups of experts, renormalised gates. Returns (idx int32 [rows][k], gate fp32 [rows][k])."""
-    import torch
+    torch = _torch()
     rows, E, stride = _rows(logits, "logits")
     dev = logits.device
     if score not in _SCORES:
@@ -446,20 +460,20 @@ def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int
     idx = torch.empty(shape, dtype=torch.int32, device=dev) if idx is None else _want(idx, shape, torch.int32, dev, "idx")
     gate = torch.empty(shape, dtype=torch.float32, device=dev) if gate is None else \
         _want(gate, shape, torch.float32, dev, "gate")
-    _launch("moe_route", dev, stream, _ptr(logits), code, stride, rows, _ptr(bias), ctypes.byref(p), _ptr(idx), _ptr(gate))
+    _launch("moe_route", dev, stream, _addr(logits), code, stride, rows, _addr(bias), ctypes.byref(p), _addr(idx), _addr(gate))
     return idx, gate
 
 
 def quant_rows_i8(x, q=None, scale=None, stream=None):
     """Rows of x [rows][k] to 8-bit codes with one scale each (quant_rows_i8). Returns (q int8, scale fp32 [rows])."""
-    import torch
+    torch = _torch()
     rows, k, stride = _rows(x, "x")
     dev = x.device
     code = _dtype_code(x.dtype, "x")
     q = torch.empty((rows, k), dtype=torch.int8, device=dev) if q is None else _want(q, (rows, k), torch.int8, dev, "q")
     scale = torch.empty((rows,), dtype=torch.float32, device=dev) if scale is None else \
         _want(scale, (rows,), torch.float32, dev, "scale")
-    _launch("quant_rows_i8", dev, stream, _ptr(x), code, stride, rows, k, _ptr(q), _ptr(scale))
+    _launch("quant_rows_i8", dev, stream, _addr(x), code, stride, rows, k, _addr(q), _addr(scale))
     return q, scale
 
 
@@ -498,7 +512,7 @@ def _workspace(ws, need: int, device):
     import torch
     if ws is None:
         return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    return _want(ws, ws.shape, torch.uint8, device, "ws")
+    return _want(ws, tuple(ws.shape), torch.uint8, device, "ws")
 
 
 def gemm_i8(x, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dtype=None, ws=None, stream=None):
@@ -509,8 +523,8 @@ def gemm_i8(x, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dty
     dev = x.device
     y = _out(out, (m, n), out_dtype, dev)
     ws = _workspace(ws, 0 if ws is not None else load().gemm_i8_workspace_size(m, n, k, int(swiglu), code), dev)
-    _launch("gemm_i8", dev, stream, _ptr(x), code, stride, _ptr(x_scale), m, k, _ptr(w), _ptr(w_scale), n, int(swiglu),
-            _ptr(y), _dtype_code(y.dtype, "out"), _ptr(ws), 0 if ws is None else ws.numel())
+    _launch("gemm_i8", dev, stream, _addr(x), code, stride, _addr(x_scale), m, k, _addr(w), _addr(w_scale), n, int(swiglu),
+            _addr(y), _dtype_code(y.dtype, "out"), _addr(ws), 0 if ws is None else ws.numel())
     return y
 
 
@@ -550,7 +564,7 @@ def moe_group_slots(idx, num_experts: int, groups: Optional[SlotGroups] = None, 
     elif (groups.tokens, groups.top_k, groups.num_experts) != (tokens, top_k, num_experts) or \
             groups.buffer.device != idx.device:
         raise ValueError("groups were allocated for another shape or device")
-    _launch("moe_group_slots", idx.device, stream, _ptr(idx), tokens, top_k, num_experts, _ptr(groups.buffer),
+    _launch("moe_group_slots", idx.device, stream, _addr(idx), tokens, top_k, num_experts, _addr(groups.buffer),
             groups.buffer.numel())
     return groups
 
@@ -575,9 +589,9 @@ def experts_gemm_i8(x, groups: SlotGroups, w, w_scale, x_scale=None, swiglu: boo
     need = 0 if ws is not None else load().experts_gemm_i8_workspace_size(groups.tokens, groups.top_k, E, rows, n, k,
                                                                           int(swiglu), code)
     ws = _workspace(ws, need, dev)
-    _launch("experts_gemm_i8", dev, stream, _ptr(x), code, stride, _ptr(x_scale), rows, k, _ptr(groups.buffer),
-            groups.buffer.numel(), groups.tokens, groups.top_k, E, _ptr(w), _ptr(w_scale), n, int(swiglu), _ptr(y),
-            _dtype_code(y.dtype, "out"), _ptr(ws), 0 if ws is None else ws.numel())
+    _launch("experts_gemm_i8", dev, stream, _addr(x), code, stride, _addr(x_scale), rows, k, _addr(groups.buffer),
+            groups.buffer.numel(), groups.tokens, groups.top_k, E, _addr(w), _addr(w_scale), n, int(swiglu), _addr(y),
+            _dtype_code(y.dtype, "out"), _addr(ws), 0 if ws is None else ws.numel())
     return y
 
 
@@ -594,6 +608,6 @@ def moe_combine(y, gate, residual=None, out=None, stream=None):
     if residual is not None:
         _want(residual, shape, torch.float32, dev, "residual")
     out = torch.empty(shape, dtype=torch.float32, device=dev) if out is None else _want(out, shape, torch.float32, dev, "out")
-    _launch("moe_combine", dev, stream, _ptr(y), _dtype_code(y.dtype, "y"), _ptr(gate), tokens, top_k, hidden,
-            _ptr(residual), _ptr(out))
+    _launch("moe_combine", dev, stream, _addr(y), _dtype_code(y.dtype, "y"), _addr(gate), tokens, top_k, hidden,
+            _addr(residual), _addr(out))
     return out
