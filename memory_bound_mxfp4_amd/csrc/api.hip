@@ -439,27 +439,38 @@ static moe_status check_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
   return MOE_OK;
 }
 
-// Quantises rows into the workspace if they are not codes already.
-static moe_status rows_to_i8(I8Args& a, const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale,
-                             int x_rows, int k, void* ws, size_t ws_bytes, hipStream_t s) {
+// Workspace of a product: the codes and scales of rows it quantises, then the
+// sums of a split K.
+static size_t i8_ws_bytes(int x_rows, int k, moe_dtype x_dtype, const I8Plan& plan) {
+  return (x_dtype == MOE_DTYPE_I8 ? 0 : quant_ws(nullptr, x_rows, k).bytes) + align256(plan.part_bytes);
+}
+
+// Takes the workspace apart and quantises rows that are not codes already.
+static moe_status i8_inputs(I8Args& a, const I8Plan& plan, const void* x, moe_dtype x_dtype, size_t x_stride,
+                            const float* x_scale, int x_rows, int k, void* ws, size_t ws_bytes, hipStream_t s) {
   a.x = static_cast<const int8_t*>(x);
   a.x_stride = x_stride;
   a.x_scale = x_scale;
-  if (x_dtype == MOE_DTYPE_I8) return MOE_OK;
+  const size_t need = i8_ws_bytes(x_rows, k, x_dtype, plan);
+  if (!need) return MOE_OK;
   if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARGUMENT;
-  const QuantWs w = quant_ws(ws, x_rows, k);
-  if (ws_bytes < w.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (launch_quant_rows(x, x_dtype, x_stride, x_rows, k, w.q, w.scale, s) != hipSuccess) return MOE_ERR_HIP;
-  a.x = w.q;
-  a.x_stride = (size_t)k;
-  a.x_scale = w.scale;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  char* p = static_cast<char*>(ws);
+  if (x_dtype != MOE_DTYPE_I8) {
+    const QuantWs w = quant_ws(p, x_rows, k);
+    if (launch_quant_rows(x, x_dtype, x_stride, x_rows, k, w.q, w.scale, s) != hipSuccess) return MOE_ERR_HIP;
+    a.x = w.q;
+    a.x_stride = (size_t)k;
+    a.x_scale = w.scale;
+    p += w.bytes;
+  }
+  a.parts = reinterpret_cast<int32_t*>(p);
   return MOE_OK;
 }
 
 size_t gemm_i8_workspace_size(int m, int n, int k, int swiglu, moe_dtype x_dtype) {
-  if (m < 1 || n < 1 || k < 1 || x_dtype == MOE_DTYPE_I8) return 0;
-  (void)swiglu;
-  return quant_ws(nullptr, m, k).bytes;
+  if (m < 1 || n < 1 || k < 1 || m > MOE_MAX_ROWS || n > kMaxCols || k > kMaxI8K) return 0;
+  return i8_ws_bytes(m, k, x_dtype, i8_plan(m, 1, false, n, k, swiglu != 0));
 }
 
 moe_status gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int m, int k,
@@ -468,9 +479,10 @@ moe_status gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const floa
   moe_status st = check_i8(x, x_dtype, x_stride, x_scale, m, k, w, w_scale, n, swiglu, y, y_dtype);
   if (st != MOE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  const I8Plan plan = i8_plan(m, 1, false, n, k, swiglu != 0);
+  const int tiles = (m + plan.tile_rows - 1) / plan.tile_rows;
+  if (!i8_launchable(plan, n, swiglu != 0, tiles)) return MOE_ERR_UNSUPPORTED;
   I8Args a{};
-  st = rows_to_i8(a, x, x_dtype, x_stride, x_scale, m, k, ws, ws_bytes, s);
-  if (st != MOE_OK) return st;
   a.rows = m;
   a.k = k;
   a.n = n;
@@ -481,8 +493,9 @@ moe_status gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const floa
   a.y_dtype = y_dtype;
   a.num_experts = 1;
   a.x_div = 1;
-  const int bm = i8_tile_rows(a);
-  if (launch_gemm_i8(a, bm, (int)(((size_t)m + bm - 1) / bm), s) != hipSuccess) return MOE_ERR_HIP;
+  st = i8_inputs(a, plan, x, x_dtype, x_stride, x_scale, m, k, ws, ws_bytes, s);
+  if (st != MOE_OK) return st;
+  if (launch_gemm_i8(a, plan, tiles, s) != hipSuccess) return MOE_ERR_HIP;
   return MOE_OK;
 }
 
@@ -507,9 +520,10 @@ moe_status moe_group_slots(const int32_t* idx, int tokens, int top_k, int num_ex
 
 size_t experts_gemm_i8_workspace_size(int tokens, int top_k, int num_experts, int x_rows, int n, int k, int swiglu,
                                       moe_dtype x_dtype) {
-  if (!slots_ok(tokens, top_k, num_experts) || x_rows < 1 || n < 1 || k < 1 || x_dtype == MOE_DTYPE_I8) return 0;
-  (void)swiglu;
-  return quant_ws(nullptr, x_rows, k).bytes;
+  if (!slots_ok(tokens, top_k, num_experts) || x_rows < 1 || n < 1 || k < 1 || x_rows > MOE_MAX_ROWS ||
+      n > kMaxCols || k > kMaxI8K)
+    return 0;
+  return i8_ws_bytes(x_rows, k, x_dtype, i8_plan(tokens * top_k, num_experts, true, n, k, swiglu != 0));
 }
 
 moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int x_rows, int k,
@@ -524,9 +538,11 @@ moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
   const GroupsLayout g = groups_layout(tokens, top_k, num_experts);
   if (groups_bytes < g.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  const I8Plan plan = i8_plan((int)slots, num_experts, true, n, k, swiglu != 0);
+  int map = 0;
+  while (map + 1 < kTileMaps && kTileRows[map] != plan.tile_rows) ++map;
+  if (!i8_launchable(plan, n, swiglu != 0, g.max_tiles[map])) return MOE_ERR_UNSUPPORTED;
   I8Args a{};
-  st = rows_to_i8(a, x, x_dtype, x_stride, x_scale, x_rows, k, ws, ws_bytes, s);
-  if (st != MOE_OK) return st;
   const char* gp = static_cast<const char*>(groups);
   a.rows = (int)slots;
   a.k = k;
@@ -539,13 +555,11 @@ moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
   a.num_experts = num_experts;
   a.x_div = (size_t)x_rows == slots ? 1 : top_k;
   a.order = reinterpret_cast<const int32_t*>(gp);
-  a.offsets = reinterpret_cast<const int32_t*>(gp + g.offsets);
-  const int bm = i8_tile_rows(a);
-  int map = 0;
-  while (map + 1 < kTileMaps && kTileRows[map] != bm) ++map;
   a.num_tiles = reinterpret_cast<const int32_t*>(gp + g.counts) + map;
   a.tiles = reinterpret_cast<const int2*>(gp + g.tiles[map]);
-  if (launch_gemm_i8(a, bm, g.max_tiles[map], s) != hipSuccess) return MOE_ERR_HIP;
+  st = i8_inputs(a, plan, x, x_dtype, x_stride, x_scale, x_rows, k, ws, ws_bytes, s);
+  if (st != MOE_OK) return st;
+  if (launch_gemm_i8(a, plan, g.max_tiles[map], s) != hipSuccess) return MOE_ERR_HIP;
   return MOE_OK;
 }
 

@@ -28,92 +28,19 @@ __device__ __forceinline__ bool find_tile(const I8Args& a, int t, Tile& o) {
     o.rows = min(BM, a.rows - o.p0);
     return true;
   }
-  if (t >= a.num_tiles[0]) return false;
-  o.e = a.tiles[t].x;
-  o.p0 = a.tiles[t].y;
-  if ((unsigned)o.e > (unsigned)a.num_experts || (unsigned)o.p0 >= (unsigned)a.rows) return false;
-  o.rows = min(min(BM, a.offsets[o.e + 1] - o.p0), a.rows - o.p0);
-  return o.rows > 0;
+  // both loads at once: an entry past the number of tiles is inside the buffer
+  const int n = a.num_tiles[0];
+  const int2 d = a.tiles[t];
+  o.e = d.x & 0xFFFF;
+  o.p0 = d.y;
+  o.rows = min(min(d.x >> 16, BM), a.rows - o.p0);
+  return t < n && o.e <= a.num_experts && o.p0 >= 0 && o.rows > 0;
 }
 
-// 16 weight rows (of each of P matrices) by up to 16 * NCG rows of x.  Both
-// operands come straight from memory as the matrix instruction takes them:
-// lane 16 q + r holds 16 codes of weight row r and of activation row r.  The
-// four waves split K into 256-byte segments; their int32 sums meet in LDS.
-template <int NCG, int P>
-__global__ __launch_bounds__(256) void k_i8_direct(I8Args a) {
-  __shared__ int red[4][P][NCG][16][16];
-  Tile t;
-  if (!find_tile<16 * NCG>(a, blockIdx.y, t)) return;
-  const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16, K = a.k;
-  const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
-  if (t.e >= a.num_experts) {  // slots without an expert: rows of zeros
-#pragma unroll
-    for (int c = 0; c < NCG; ++c)
-      if (16 * c + row < t.rows && n0 + col < a.n)
-        store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + 16 * c + row) * a.n + n0 + col, 0.0f);
-    return;
-  }
-  const int8_t* wp[P];
-#pragma unroll
-  for (int p = 0; p < P; ++p) wp[p] = a.w + (((size_t)t.e * P + p) * a.n + min(n0 + r, a.n - 1)) * K;
-  const int8_t* xp[NCG];
-#pragma unroll
-  for (int c = 0; c < NCG; ++c)
-    xp[c] = a.x + (size_t)x_row(a, y_row(a, t.p0 + min(16 * c + r, t.rows - 1))) * a.x_stride;
-  i32x4 acc[P][NCG];
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int c = 0; c < NCG; ++c) acc[p][c] = i32x4{0, 0, 0, 0};
-  const i32x4 z{0, 0, 0, 0};
-  for (int s = wv * 256; s < K; s += 1024) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = s + 64 * j + 16 * q, kc = min(k, K - 16);
-      i32x4 xv[NCG];
-#pragma unroll
-      for (int c = 0; c < NCG; ++c) xv[c] = *reinterpret_cast<const i32x4*>(xp[c] + kc);
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        i32x4 wvv = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wp[p] + kc));
-        if (k >= K) wvv = z;
-#pragma unroll
-        for (int c = 0; c < NCG; ++c) acc[p][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wvv, xv[c], acc[p][c], 0, 0, 0);
-      }
-    }
-  }
-  // accumulator register i of lane 16 q + r: weight row 4 q + i, activation row r
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int c = 0; c < NCG; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[wv][p][c][r][4 * q + i] = acc[p][c][i];
-  __syncthreads();
-#pragma unroll
-  for (int c = 0; c < NCG; ++c) {
-    if (16 * c + row >= t.rows || n0 + col >= a.n) continue;
-    const int yr = y_row(a, t.p0 + 16 * c + row);
-    const float sx = a.x_scale[x_row(a, yr)];
-    float v[P];
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int sum = red[0][p][c][row][col] + red[1][p][c][row][col] + red[2][p][c][row][col] + red[3][p][c][row][col];
-      v[p] = (float)sum * (sx * a.w_scale[((size_t)t.e * P + p) * a.n + n0 + col]);
-    }
-    store_y(a.y, a.y_dtype, (size_t)yr * a.n + n0 + col, P == 2 ? swiglu_f(v[0], v[P - 1]) : v[0]);
-  }
-}
-
-// ---- many rows: tiles through LDS ----------------------------------------------
-//
-// A workgroup computes BM rows of x by BN rows of the matrix (with SwiGLU BN/2
-// gate rows and their BN/2 up rows, alternating by 16).  K runs in stages of
-// 64 codes, kept in ST buffers: the loads of stage k + ST - 1 are issued, straight into
-// LDS, before stage k is computed.
-constexpr int KS = 64;
+// Codes of K that a wave or workgroup moves at a time: a whole cache line of
+// every row.  (With 64 codes, each line crosses from L2 twice: the few-rows
+// kernel reached 4.3 TB/s that way, see below.)
+constexpr int KS = 128;
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) const void glb_void;
@@ -122,8 +49,10 @@ typedef __attribute__((address_space(1))) const void glb_void;
 __device__ const __attribute__((aligned(16))) int8_t kZeroCodes[16] = {0};
 
 // One wave copies 64 x 16 bytes from its lanes' addresses to 1 KB of LDS.
+// NT: not kept in the caches (a matrix that is read once).
+template <bool NT = false>
 __device__ __forceinline__ void load_to_lds(const int8_t* src, int8_t* dst) {
-  __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)dst, 16, 0, 0);
+  __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)dst, 16, 0, NT ? 2 : 0);
 }
 
 // Waits until at most VM of the wave's loads are out, and for its LDS reads.
@@ -132,106 +61,311 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4));
 }
 
-template <int DT>
-__device__ __forceinline__ void store4(void* y, size_t i, const float* v) {
-  if constexpr (DT == MOE_DTYPE_F32) {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(y) + i) = f32x4{v[0], v[1], v[2], v[3]};
-  } else {
-    uint32_t h[4];
+// Waits for the wave's LDS reads alone.
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
+
+// Barrier of the workgroup that neither memory accesses nor multiplications cross.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// ---- few rows -------------------------------------------------------------------
+//
+// 16 * NN matrix rows by up to 16 * NX rows of x a workgroup; bound by reading
+// the matrix.  The NW waves take stages of K in turn, each through a ring of ST
+// buffers of its own: no barrier until their int32 sums meet at the end, and a
+// buffer is loaded again as soon as its fragments are in registers.
+template <int NX, int NN, int P, int NW, int ST>
+__global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
+  constexpr int STAGE = (NX + NN) * 16 * KS, L = 2 * (NX + NN), COLS = 16 * NN / P, T = 64 * NW;
+  static_assert(NN % P == 0 && NW * ST * STAGE >= NW * NX * NN * 1024, "stream");
+  __shared__ __attribute__((aligned(1024))) int8_t lds[NW * ST * STAGE];
+  __shared__ float scales[16 * (NN + NX)];
+  __shared__ int yr[16 * NX];
+  Tile t;
+  if (!find_tile<16 * NX>(a, blockIdx.x / tiles_n, t)) return;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i0 = blockIdx.x % tiles_n * COLS, K = a.k;
+  if (t.e >= a.num_experts) {  // slots without an expert: rows of zeros
+    for (int i = threadIdx.x; i < t.rows * COLS; i += T)
+      if (i0 + i % COLS < a.n) store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + i / COLS) * a.n + i0 + i % COLS, 0.0f);
+    return;
+  }
+  for (int i = threadIdx.x; i < 16 * NX; i += T) yr[i] = y_row(a, t.p0 + min(i, t.rows - 1));
+  __syncthreads();
+  // lane l of a load brings chunk (l ^ row) & 7 of row l >> 3, as in the tiles below
+  const int lr = lane >> 3, chunk = (lane ^ lr) & 7;
+  const int8_t* src[L];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) h[c] = DT == MOE_DTYPE_BF16 ? f32_to_bf16(v[c]) : f32_to_f16(v[c]);
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(y) + i) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+  for (int i = 0; i < L; ++i) {
+    if (i < 2 * NX) {
+      src[i] = a.x + (size_t)x_row(a, yr[8 * i + lr]) * a.x_stride;
+    } else {
+      const int gw = 8 * (i - 2 * NX), n = min(i0 + (P == 2 ? gw / 32 * 16 + gw % 16 : gw) + lr, a.n - 1);
+      src[i] = a.w + (((size_t)t.e * P + (P == 2 ? gw / 16 % 2 : 0)) * a.n + n) * K;
+    }
+  }
+  const int stages = (K + KS - 1) / KS, mine = wv < stages ? (stages - wv + NW - 1) / NW : 0;
+  int8_t* ring = lds + wv * ST * STAGE;
+  auto load = [&](int i, int8_t* buf) {  // this wave's i-th stage
+    const int k = (wv + NW * i) * KS + 16 * chunk;
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      const int8_t* p = src[j] + min(k, K - 16);
+      if (j < 2 * NX) load_to_lds(k < K ? p : kZeroCodes, buf + 1024 * j);
+      else load_to_lds<true>(p, buf + 1024 * j);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < ST; ++i)
+    if (i < mine) load(i, ring + i * STAGE);
+  i32x4 acc[NX][NN];
+#pragma unroll
+  for (int i = 0; i < NX; ++i)
+#pragma unroll
+    for (int j = 0; j < NN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  int8_t* buf = ring;
+  for (int st = 0; st < mine; ++st) {
+    const int later = mine - 1 - st;  // stages that are out behind this one
+    if (later >= ST - 1) wait_vm<(ST - 1) * L>();
+    else if (ST > 3 && later == 2) wait_vm<2 * L>();
+    else if (ST > 2 && later == 1) wait_vm<L>();
+    else wait_vm<0>();
+    asm volatile("" ::: "memory");
+    i32x4 fw[2][NN], fx[2][NX];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int8_t* at = buf + 16 * ((4 * h + q) ^ (r & 7)) + r * KS;
+#pragma unroll
+      for (int i = 0; i < NX; ++i) fx[h][i] = *reinterpret_cast<const i32x4*>(at + 16 * KS * i);
+#pragma unroll
+      for (int j = 0; j < NN; ++j) fw[h][j] = *reinterpret_cast<const i32x4*>(at + 16 * KS * (NX + j));
+    }
+    wait_lds();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (st + ST < mine) load(st + ST, buf);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < NX; ++i)
+#pragma unroll
+        for (int j = 0; j < NN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h][j], fx[h][i], acc[i][j], 0, 0, 0);
+    buf = buf + STAGE == ring + ST * STAGE ? ring : buf + STAGE;
+  }
+  for (int i = threadIdx.x; i < 16 * NN; i += T) {
+    const int n = min(i0 + (P == 2 ? i / 32 * 16 + i % 16 : i), a.n - 1);
+    scales[i] = a.w_scale[((size_t)t.e * P + (P == 2 ? i / 16 % 2 : 0)) * a.n + n];
+  }
+  for (int i = threadIdx.x; i < 16 * NX; i += T) scales[16 * NN + i] = a.x_scale[x_row(a, yr[i])];
+  __syncthreads();
+  // accumulator register c of lane 16 q + r: matrix row 16 j + 4 q + c, row 16 i + r of x
+  int* red = reinterpret_cast<int*>(lds);
+#pragma unroll
+  for (int i = 0; i < NX; ++i)
+#pragma unroll
+    for (int j = 0; j < NN; ++j)
+      *reinterpret_cast<i32x4*>(red + ((wv * NX + i) * 16 + r) * (16 * NN) + 16 * j + 4 * q) = acc[i][j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < t.rows * COLS; i += T) {
+    const int m = i / COLS, c = i % COLS;
+    if (i0 + c >= a.n) continue;
+    float v[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int tc = c / 16 * 16 * P + 16 * p + c % 16;  // column of the tile
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) sum += red[(w * 16 * NX + m) * (16 * NN) + tc];
+      v[p] = (float)sum * (scales[16 * NN + m] * scales[tc]);
+    }
+    store_y(a.y, a.y_dtype, (size_t)yr[m] * a.n + i0 + c, P == 2 ? swiglu_f(v[0], v[P - 1]) : v[0]);
+  }
+}
+
+// ---- many rows: tiles through LDS ----------------------------------------------
+//
+// A workgroup computes BM rows of x by BN rows of the matrix (with SwiGLU BN/2
+// gate rows and their BN/2 up rows, alternating by 16).  K runs in
+// stages kept in ST buffers: the loads of stage k + ST - 1 are issued, straight
+// into LDS, before stage k is computed.
+
+// One tile configuration: BM rows of x by BN matrix rows (P matrices
+// interleaved), WGM x WGN waves, ST buffers of a stage.
+template <int BM_, int BN_, int WGM_, int WGN_, int P_, int ST_>
+struct TileCfg {
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, P = P_, ST = ST_;
+  static constexpr int NW = WGM * WGN, T = 64 * NW, MF = BM / WGM / 16, NF = BN / WGN / 16;  // fragments of a wave
+  static constexpr bool SPLIT = BM == 64;  // K may be split over workgroups
+  static constexpr int STAGE = (BM + BN) * KS, RING = ST * STAGE;
+  // Rows of outputs on their way through LDS: C columns of B bytes and 16
+  // more, which spreads the rows of a fragment over the banks.
+  static constexpr int row_bytes(int C, int B) { return (C + 16) * B; }
+  static constexpr int OUT16 = BM * row_bytes(BN / P, 2);
+  static constexpr int LDS = RING > OUT16 ? RING : OUT16;
+  // fragment rows of a wave that fit at once
+  static constexpr int fit(int C, int B, int n) { return WGM * n * 16 * row_bytes(C, B) <= LDS ? n : fit(C, B, n / 2); }
+};
+
+// A tile's results on their way out.  In the registers a lane holds 4 columns
+// of 16 rows apart, and storing those would touch 16 cache lines of 32 bytes
+// each an instruction (it took 13 us of a 256 x 256 tile's call); through LDS a
+// wave stores whole lines.  make(i, j, v): the 4 values (OB bytes each, packed)
+// of fragment i, j; put(m, c, chunk): stores 16 bytes of row m from column c.
+template <class C, int COLS, int STEP, int OB, class Make, class Put>
+__device__ __forceinline__ void tile_out(int8_t* lds, int wm, int wn, int rows, Make make, Put put) {
+  constexpr int MI = C::fit(COLS, OB, C::MF), RB = C::row_bytes(COLS, OB), CPR = COLS * OB / 16;
+  static_assert(MI > 0, "a fragment row does not fit");
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int h = 0; h < C::MF; h += MI) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < C::NF; j += STEP) {
+        int8_t* at = lds + ((wm * MI + i) * 16 + r) * RB + ((wn * C::NF + j) / STEP * 16 + 4 * q) * OB;
+        if constexpr (OB == 2) *reinterpret_cast<u32x2*>(at) = make(h + i, j);
+        else *reinterpret_cast<u32x4*>(at) = make(h + i, j);
+      }
+    __syncthreads();
+    for (int c = threadIdx.x; c < C::WGM * MI * 16 * CPR; c += C::T) {
+      const int row = c / CPR, col = c - row * CPR, m = row / (MI * 16) * (C::BM / C::WGM) + h * 16 + row % (MI * 16);
+      if (m < rows) put(m, col * (16 / OB), *reinterpret_cast<const u32x4*>(lds + row * RB + col * 16));
+    }
   }
 }
 
 // Scales a wave's sums and stores them.  Register c of acc[i][j] of lane
 // 16 q + r: matrix row 16 j + 4 q + c, row 16 i + r of x.
-template <int DT, int BM, int BN, int WGM, int WGN, int P>
-__device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, int i0, int wm, int wn,
-                                           const i32x4 (&acc)[BM / WGM / 16][BN / WGN / 16]) {
-  constexpr int MF = BM / WGM / 16, NF = BN / WGN / 16;
+template <int DT, class C>
+__device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, int8_t* lds, int i0, int wm, int wn,
+                                           const i32x4 (&acc)[C::MF][C::NF]) {
+  constexpr int P = C::P, OB = Elem<DT>::bytes;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const bool vec = a.n % 4 == 0;
-  const float* sw = a.w_scale + (size_t)t.e * P * a.n;
+  const float* sw = reinterpret_cast<const float*>(lds + C::LDS);
+  const float* sx = sw + C::BN;
+  const int* yr = reinterpret_cast<const int*>(sx + C::BM);
+  auto make = [&](int i, int j) {
+    const float s = sx[wm * (C::BM / C::WGM) + 16 * i + r];
+    f32x4 v;
 #pragma unroll
-  for (int j = 0; j < NF; j += P) {
-    const int n = i0 + (wn * (BN / WGN) + 16 * j) / P + 4 * q;
-    float s[P][4];
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s[p][c] = sw[p * a.n + min(n + c, a.n - 1)];
-#pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      const int m = wm * (BM / WGM) + 16 * i + r;
-      if (m >= t.rows) continue;
-      const int yr = y_row(a, t.p0 + m);
-      const float sx = a.x_scale[x_row(a, yr)];
-      const size_t at = (size_t)yr * a.n + n;
-      float v[4];
+    for (int p = 0; p < P; ++p) {
+      const f32x4 w = *reinterpret_cast<const f32x4*>(sw + (wn * C::NF + j + p) * 16 + 4 * q);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        v[c] = (float)acc[i][j][c] * (sx * s[0][c]);
-        if (P == 2) v[c] = swiglu_f(v[c], (float)acc[i][j + P - 1][c] * (sx * s[P - 1][c]));
-      }
-      if (vec) {
-        if (n < a.n) store4<DT>(a.y, at, v);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n + c < a.n) store_y(a.y, DT, at + c, v[c]);
+        const float u = (float)acc[i][j + p][c] * (s * w[c]);
+        v[c] = p ? swiglu_f(v[c], u) : u;
       }
     }
-  }
+    if constexpr (OB == 4) return __builtin_bit_cast(u32x4, v);
+    else return u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+  };
+  constexpr int V = 16 / OB;
+  const bool whole = a.n % V == 0;  // 16-byte stores stay aligned, and a chunk is inside the row or outside
+  auto put = [&](int m, int c, const u32x4& d) {
+    const size_t at = (size_t)yr[m] * a.n + i0 + c;
+    if (whole) {
+      if (i0 + c < a.n) *reinterpret_cast<u32x4*>(static_cast<char*>(a.y) + at * OB) = d;
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (i0 + c + k < a.n) {
+          if constexpr (OB == 4) static_cast<uint32_t*>(a.y)[at + k] = d[k];
+          else static_cast<uint16_t*>(a.y)[at + k] = (uint16_t)(d[k / 2] >> (k % 2 * 16));
+        }
+    }
+  };
+  tile_out<C, C::BN / P, P, OB>(lds, wm, wn, t.rows, make, put);
 }
 
-template <int BM, int BN, int WGM, int WGN, int P, int ST>
-__global__ __launch_bounds__(64 * WGM * WGN) void k_i8_tile(I8Args a, int tiles_n, int m_tiles) {
-  constexpr int NW = WGM * WGN, MF = BM / WGM / 16, NF = BN / WGN / 16;  // fragments of a wave
-  constexpr int LX = BM / 16 / NW, LW = BN / 16 / NW, L = LX + LW;       // loads of a wave and stage
-  static_assert(LX * 16 * NW == BM && LW * 16 * NW == BN && NF % P == 0, "tile");
-  __shared__ __attribute__((aligned(1024))) int8_t lds[ST][(BM + BN) * KS];
+// With K split over workgroups: the sums of one part, by position, in rows of
+// all tiles' columns (the matrices interleaved as in the tile).
+template <class C>
+__device__ __forceinline__ void tile_store_part(const I8Args& a, const Tile& t, int8_t* lds, int tn, int tiles_n,
+                                                int wm, int wn, int part, const i32x4 (&acc)[C::MF][C::NF]) {
+  int* dst = a.parts + ((size_t)part * a.rows + t.p0) * ((size_t)tiles_n * C::BN) + tn * C::BN;
+  tile_out<C, C::BN, 1, 4>(
+      lds, wm, wn, t.rows, [&](int i, int j) { return __builtin_bit_cast(u32x4, acc[i][j]); },
+      [&](int m, int c, const u32x4& d) {
+        *reinterpret_cast<u32x4*>(dst + (size_t)m * ((size_t)tiles_n * C::BN) + c) = d;
+      });
+}
+
+// Workgroup -> tile.  Workgroups go to the 8 XCDs in turn; each XCD gets one
+// contiguous run of tiles, in bands of `band` tile rows walked column by column,
+// so that the tiles its CUs work on at a time share rows of x and of the
+// matrix in its L2.  A band of 8 in a dense product (both are read again and
+// again); in a grouped one about the tile rows of an expert, so that its rows
+// stay in L2 while its matrix, which nobody else needs, streams by once.
+
+template <class C>
+__global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int tiles_m, int parts, int band_rows) {
+  constexpr int BM = C::BM, BN = C::BN, WGM = C::WGM, WGN = C::WGN, P = C::P, ST = C::ST, NW = C::NW, MF = C::MF,
+                NF = C::NF, GX = BM / 8, L = (BM + BN) / 8 / NW;  // L: loads of a wave and stage
+  static_assert(L * 8 * NW == BM + BN && NF % P == 0 && (ST == 2 || ST == 4), "tile");
+  // the ring (outputs later), then the tile's matrix scales, row scales and output rows
+  __shared__ __attribute__((aligned(1024))) int8_t lds[C::LDS + 4 * (BN + 2 * BM)];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wv % WGM, wn = wv / WGM;
-  const int tn = blockIdx.x % tiles_n, tm = blockIdx.x / tiles_n;
+  // a grouped product's grid is sized for the most tiles its slots can make: the
+  // XCDs share the ones there are
+  if (a.order) tiles_m = min(tiles_m, a.num_tiles[0]);
+  const int tiles = tiles_n * tiles_m, per_xcd = (tiles * parts + 7) / 8;
+  int id = (int)(blockIdx.x & 7) * per_xcd + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per_xcd || id >= tiles * parts) return;
+  const int part = id / tiles;
+  id -= part * tiles;
+  const int band = id / (band_rows * tiles_n), in = id - band * band_rows * tiles_n;
+  const int high = min(band_rows, tiles_m - band * band_rows), tn = in / high, tm = band * band_rows + in - tn * high;
   Tile t;
   if (!find_tile<BM>(a, tm, t)) return;
   const int K = a.k, i0 = tn * (BN / P);  // first output column
   if (t.e >= a.num_experts) {
+    if (part) return;
     for (int m = threadIdx.x / 64; m < t.rows; m += NW)
       for (int n = i0 + lane; n < min(i0 + BN / P, a.n); n += 64)
         store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + m) * a.n + n, 0.0f);
     return;
   }
-  // Loads: a wave copies 16 rows x 64 codes at a time; lane l brings chunk
-  // (l & 3) ^ swz of row l >> 2, so that the 16-byte chunks of consecutive rows
-  // lie in different banks when a fragment reads one chunk of 16 rows.
-  const int lr = lane >> 2, chunk = (lane & 3) ^ ((lr >> 1) & 3);
+  float* scales = reinterpret_cast<float*>(lds + C::LDS);
+  int* yr = reinterpret_cast<int*>(scales + BN + BM);
+  for (int i = threadIdx.x; i < BM; i += C::T) yr[i] = y_row(a, t.p0 + min(i, t.rows - 1));
+  __syncthreads();
+  // Loads: a wave copies 8 rows x 128 codes at a time; lane l brings chunk
+  // (l ^ row) & 7 of row l >> 3, so that the same 16-byte chunk of 8 consecutive
+  // rows lies in 8 different bank groups when a fragment reads it.
+  const int lr = lane >> 3, chunk = (lane ^ lr) & 7;
   const int8_t* src[L];
 #pragma unroll
-  for (int i = 0; i < LX; ++i) {
-    const int m = min(16 * (wv + NW * i) + lr, t.rows - 1);
-    src[i] = a.x + (size_t)x_row(a, y_row(a, t.p0 + m)) * a.x_stride;
+  for (int i = 0; i < L; ++i) {
+    const int g = wv + NW * i;  // group of 8 rows: first those of x, then the matrix's
+    if (g < GX) {
+      src[i] = a.x + (size_t)x_row(a, yr[8 * g + lr]) * a.x_stride;
+    } else {
+      const int gw = 8 * (g - GX);  // first row of the tile's matrix part; P 2: 16 gate rows, 16 up rows, ...
+      const int n = min(i0 + (P == 2 ? gw / 32 * 16 + gw % 16 : gw) + lr, a.n - 1);
+      src[i] = a.w + (((size_t)t.e * P + (P == 2 ? gw / 16 % 2 : 0)) * a.n + n) * K;
+    }
   }
-#pragma unroll
-  for (int i = 0; i < LW; ++i) {
-    const int g = wv + NW * i;  // group of 16 tile rows
-    const int n = min(i0 + (P == 2 ? 16 * (g >> 1) : 16 * g) + lr, a.n - 1);
-    src[LX + i] = a.w + (((size_t)t.e * P + (P == 2 ? g & 1 : 0)) * a.n + n) * K;
-  }
-  const int S = (K + KS - 1) / KS;
+  const int stages = (K + KS - 1) / KS;
+  const int s0 = (int)((size_t)stages * part / parts), S = (int)((size_t)stages * (part + 1) / parts);
   auto load = [&](int st) {
-    int8_t* buf = lds[st % ST];
+    int8_t* buf = lds + (st & (ST - 1)) * C::STAGE;
     const int k = st * KS + 16 * chunk;
     if ((st + 1) * KS <= K) {
 #pragma unroll
-      for (int i = 0; i < L; ++i)
-        load_to_lds(src[i] + k, buf + (i < LX ? 1024 * (wv + NW * i) : BM * KS + 1024 * (wv + NW * (i - LX))));
-    } else {  // the last stage of a K that is no multiple of 64: zeros past K on x's side
+      for (int i = 0; i < L; ++i) load_to_lds(src[i] + k, buf + 1024 * (wv + NW * i));
+    } else {  // the last stage of a K that is no multiple of 128: zeros past K on x's side
 #pragma unroll
       for (int i = 0; i < L; ++i)
-        load_to_lds(i < LX && k >= K ? kZeroCodes : src[i] + min(k, K - 16),
-                    buf + (i < LX ? 1024 * (wv + NW * i) : BM * KS + 1024 * (wv + NW * (i - LX))));
+        load_to_lds(wv + NW * i < GX && k >= K ? kZeroCodes : src[i] + min(k, K - 16), buf + 1024 * (wv + NW * i));
     }
   };
   i32x4 acc[MF][NF];
@@ -240,64 +374,214 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_i8_tile(I8Args a, int tiles_
 #pragma unroll
     for (int j = 0; j < NF; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 #pragma unroll
-  for (int st = 0; st < ST - 1; ++st)
-    if (st < S) load(st);
-  const int frag = r * KS + 16 * (q ^ ((r >> 1) & 3));
-  for (int st = 0; st < S; ++st) {
-    // stage st has landed when at most the loads of the stages after it are out
-    const int later = min(ST - 2, S - 1 - st);
-    if (later == 2) wait_vm<2 * L>();
-    else if (later == 1) wait_vm<L>();
-    else wait_vm<0>();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    // every wave is past stage st - 1: its buffer takes stage st + ST - 1
-    if (st + ST - 1 < S) load(st + ST - 1);
-    const int8_t* bx = lds[st % ST] + wm * (BM / WGM) * KS + frag;
-    const int8_t* bw = lds[st % ST] + BM * KS + wn * (BN / WGN) * KS + frag;
-    i32x4 fw[NF], fx[MF];
+  for (int i = 0; i < ST - 1; ++i)
+    if (s0 + i < S) load(s0 + i);
+  // the scales travel with the first stage; the loop's barriers stand before their use
+  for (int i = threadIdx.x; i < BN; i += C::T) {
+    const int n = min(i0 + (P == 2 ? i / 32 * 16 + i % 16 : i), a.n - 1);
+    scales[i] = a.w_scale[((size_t)t.e * P + (P == 2 ? i / 16 % 2 : 0)) * a.n + n];
+  }
+  for (int i = threadIdx.x; i < BM; i += C::T) scales[BN + i] = a.x_scale[x_row(a, yr[i])];
+  i32x4 fw[NF], fx[MF];
+  auto read = [&](int st, int half) {
+    const int at = 16 * ((4 * half + q) ^ (r & 7)) + r * KS;
+    const int8_t* bx = lds + (st & (ST - 1)) * C::STAGE + wm * (BM / WGM) * KS + at;
+    const int8_t* bw = lds + (st & (ST - 1)) * C::STAGE + BM * KS + wn * (BN / WGN) * KS + at;
 #pragma unroll
-    for (int j = 0; j < NF; ++j) fw[j] = *reinterpret_cast<const i32x4*>(bw + 1024 * j);
+    for (int j = 0; j < NF; ++j) fw[j] = *reinterpret_cast<const i32x4*>(bw + 16 * KS * j);
 #pragma unroll
-    for (int i = 0; i < MF; ++i) fx[i] = *reinterpret_cast<const i32x4*>(bx + 1024 * i);
+    for (int i = 0; i < MF; ++i) fx[i] = *reinterpret_cast<const i32x4*>(bx + 16 * KS * i);
+  };
+  auto multiply = [&]() {
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
       for (int j = 0; j < NF; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fx[i], acc[i][j], 0, 0, 0);
-  }
-  if (a.y_dtype == MOE_DTYPE_BF16) tile_store<MOE_DTYPE_BF16, BM, BN, WGM, WGN, P>(a, t, i0, wm, wn, acc);
-  else if (a.y_dtype == MOE_DTYPE_F16) tile_store<MOE_DTYPE_F16, BM, BN, WGM, WGN, P>(a, t, i0, wm, wn, acc);
-  else tile_store<MOE_DTYPE_F32, BM, BN, WGM, WGN, P>(a, t, i0, wm, wn, acc);
-}
-
-int i8_tile_rows(const I8Args& a) {
-  if (a.rows <= 16) return 16;
-  const int per = a.order ? a.rows / a.num_experts : a.rows;
-  return per >= 128 ? 256 : per > 16 ? 64 : 16;
-}
-
-template <int BM, int BN, int WGM, int WGN, int P, int ST>
-static void tile_launch(const I8Args& a, int max_tiles, hipStream_t s) {
-  const int tiles_n = (a.n * P + BN - 1) / BN;
-  hipLaunchKernelGGL((k_i8_tile<BM, BN, WGM, WGN, P, ST>), dim3(tiles_n * max_tiles), dim3(64 * WGM * WGN), 0, s, a,
-                     tiles_n, max_tiles);
-}
-
-hipError_t launch_gemm_i8(const I8Args& a, int tile_rows, int max_tiles, hipStream_t s) {
-  if (tile_rows == 256) {
-    if (a.swiglu) tile_launch<256, 256, 2, 4, 2, 4>(a, max_tiles, s);
-    else tile_launch<256, 256, 2, 4, 1, 4>(a, max_tiles, s);
-    return hipGetLastError();
-  }
-  const dim3 grid((a.n + 15) / 16, max_tiles), block(256);
-  if (tile_rows == 16) {
-    if (a.swiglu) hipLaunchKernelGGL((k_i8_direct<1, 2>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_i8_direct<1, 1>), grid, block, 0, s, a);
+  };
+  // waits until all loads of this wave but those of the `later` newest stages have landed
+  auto landed = [&](int later) {
+    if (later >= 2) wait_vm<2 * L>();
+    else if (later == 1) wait_vm<L>();
+    else wait_vm<0>();
+  };
+  if constexpr (NW == 8) {
+    // Two waves a SIMD, of two groups one step apart: while the waves of one
+    // group multiply, those of the other read the fragments of half a stage from
+    // LDS and issue loads, then they change places at a barrier.  A stage has
+    // landed for every wave when a group reads it: each wave waited for its own
+    // loads of stage st + 1 before the barrier that ends its reads of stage st.
+    const bool second = wv >= 4;
+    landed(min(ST - 2, S - 1 - s0));
+    meet();
+    if (second) meet();
+    for (int st = s0; st < S; ++st) {
+      read(st, 0);
+      if (st + ST - 1 < S) load(st + ST - 1);  // into the buffer of stage st - 1, which both groups have read
+      wait_lds();
+      meet();
+      __builtin_amdgcn_s_setprio(1);
+      multiply();
+      __builtin_amdgcn_s_setprio(0);
+      meet();
+      read(st, 1);
+      landed(min(ST - 2, S - 2 - st));
+      meet();
+      __builtin_amdgcn_s_setprio(1);
+      multiply();
+      __builtin_amdgcn_s_setprio(0);
+      meet();
+    }
+    if (!second) meet();
   } else {
-    if (a.swiglu) hipLaunchKernelGGL((k_i8_direct<4, 2>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_i8_direct<4, 1>), grid, block, 0, s, a);
+    for (int st = s0; st < S; ++st) {
+      landed(min(ST - 2, S - 1 - st));
+      meet();
+      if (st + ST - 1 < S) load(st + ST - 1);  // every wave is past stage st - 1: its buffer is free
+      read(st, 0);
+      multiply();
+      read(st, 1);
+      multiply();
+    }
   }
+  if constexpr (C::SPLIT) {
+    if (parts > 1) {
+      tile_store_part<C>(a, t, lds, tn, tiles_n, wm, wn, part, acc);
+      return;
+    }
+  }
+  if (a.y_dtype == MOE_DTYPE_BF16) tile_store<MOE_DTYPE_BF16, C>(a, t, lds, i0, wm, wn, acc);
+  else if (a.y_dtype == MOE_DTYPE_F16) tile_store<MOE_DTYPE_F16, C>(a, t, lds, i0, wm, wn, acc);
+  else tile_store<MOE_DTYPE_F32, C>(a, t, lds, i0, wm, wn, acc);
+}
+
+// The parts of a split K added up, scaled and stored: a workgroup takes 4 rows
+// (a wave each) by 256 columns of a tile.
+template <class C>
+__global__ __launch_bounds__(256) void k_i8_parts(I8Args a, int parts, int tiles_n, int tiles_m, int cols) {
+  constexpr int P = C::P, BM = C::BM, BO = C::BN / P;
+  const int c = blockIdx.x % cols, u = blockIdx.x / cols, tm = u / (BM / 4), m = u % (BM / 4) * 4 + (threadIdx.x >> 6);
+  Tile t;
+  if (!find_tile<BM>(a, tm, t) || t.e >= a.num_experts || m >= t.rows) return;
+  const int n = c * 256 + (threadIdx.x & 63) * 4;
+  if (n >= a.n) return;
+  const int yr = y_row(a, t.p0 + m);
+  const float sx = a.x_scale[x_row(a, yr)];
+  const float* sw = a.w_scale + (size_t)t.e * P * a.n;
+  const size_t width = (size_t)tiles_n * C::BN, step = (size_t)a.rows * width;
+  const int* src = a.parts + (size_t)(t.p0 + m) * width + n / BO * C::BN + n % BO / 16 * 16 * P + n % 16;
+  float v[P][4];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    i32x4 sum{0, 0, 0, 0};
+    for (int i = 0; i < parts; ++i) sum += *reinterpret_cast<const i32x4*>(src + i * step + 16 * p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[p][k] = (float)sum[k] * (sx * sw[p * a.n + min(n + k, a.n - 1)]);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (P == 2) v[0][k] = swiglu_f(v[0][k], v[P - 1][k]);
+    if (n + k < a.n) store_y(a.y, a.y_dtype, (size_t)yr * a.n + n + k, v[0][k]);
+  }
+}
+
+template <class C>
+static void tile_launch(const I8Args& a, int max_tiles, int parts, hipStream_t s) {
+  const int tiles_n = (a.n * C::P + C::BN - 1) / C::BN;
+  const int per_xcd = (tiles_n * max_tiles * parts + 7) / 8;
+  int band = 8;
+  if (a.order) {
+    band = (a.rows / a.num_experts + C::BM / 2) / C::BM;
+    band = band < 1 ? 1 : band > 8 ? 8 : band;
+  }
+  hipLaunchKernelGGL(k_i8_tile<C>, dim3(8 * per_xcd), dim3(C::T), 0, s, a, tiles_n, max_tiles, parts, band);
+  if constexpr (C::SPLIT) {
+    if (parts == 1) return;
+    const int cols = (a.n + 255) / 256;
+    hipLaunchKernelGGL(k_i8_parts<C>, dim3(cols * max_tiles * (C::BM / 4)), dim3(256), 0, s, a, parts, tiles_n,
+                       max_tiles, cols);
+  }
+}
+
+template <int NX, int NN, int NW, int ST>
+static void stream_launch(const I8Args& a, int max_tiles, hipStream_t s) {
+  const int P = a.swiglu ? 2 : 1, tiles_n = (a.n * P + 16 * NN - 1) / (16 * NN);
+  const dim3 grid(tiles_n * max_tiles), block(64 * NW);
+  if (a.swiglu) hipLaunchKernelGGL((k_i8_stream<NX, NN, 2, NW, ST>), grid, block, 0, s, a, tiles_n);
+  else hipLaunchKernelGGL((k_i8_stream<NX, NN, 1, NW, ST>), grid, block, 0, s, a, tiles_n);
+}
+
+// Which kernel a product runs on.
+// Up to 16 rows (of an expert, on average 8: some have twice that): 16 rows of
+// x by 32 matrix rows; up to 32 (24): 32 by 32.  Measured at N 7168, K 7168:
+// 1 row 10.3 us, 8 rows 11.4, 32 rows 15.0 (64 x 64 tiles, K in two parts: 16.5);
+// at N 65536 8 rows 72 us (6.5 TB/s), 32 rows 90 (64 x 64 tiles: 88).
+// Above that the tile with the least estimated time, c0 + c1 * T / 256 per 56
+// stages (K 7168) for T workgroups; the larger tiles run one or two to a CU, so
+// theirs go in whole rounds of 256.  Measured at N 7168, K 7168: 256 x 256 95 us at
+// 224 tiles, 373 us at 896; 128 x 128 42 us at 224, 68 at 448, 415 at 3584;
+// 128 x 64 30 us at 224, 51 at 448; 64 x 64 22 us at 224, 34 at 448, 128 at 2048.
+// K is split over parts while 64 x 64 tiles leave CUs without work (64 rows of
+// N 7168: 18 us in 2 parts, 44 in one; 128 rows of N 1536: 13 us in 4 parts, 23
+// in one).
+I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
+  const int used = grouped ? (rows < experts ? rows : experts) : 1;
+  const double per = (double)rows / used;
+  if (per <= (grouped ? 8 : 16)) return {0, 16, 1, 0};
+  if (per <= (grouped ? 24 : 32)) return {1, 32, 1, 0};
+  struct Model {
+    int bm, bn;
+    double c0, c1;
+    bool rounds;
+  };
+  static constexpr Model models[] = {
+      {64, 64, 4.0, 17.0, false}, {128, 64, 9.0, 21.0, true}, {128, 128, 12.0, 29.0, true}, {256, 256, 4.0, 91.0, true}};
+  const int P = swiglu ? 2 : 1, stages = (k + KS - 1) / KS;
+  I8Plan best{};
+  double least = 0.0;
+  for (int i = 0; i < 4; ++i) {
+    const Model& m = models[i];
+    const int cols = (n * P + m.bn - 1) / m.bn;
+    // the rows of an expert end inside a tile: half a tile lost on average
+    const double down = grouped ? (double)rows / m.bm + 0.5 * used : (rows + m.bm - 1) / m.bm;
+    const double tiles = down * cols;
+    const double load = m.rounds ? ceil(tiles / 256.0) : fmax(tiles / 256.0, 1.0);
+    const double time = m.c0 + m.c1 * load * stages / 56.0;
+    if (i && time >= least) continue;
+    least = time;
+    int parts = 1;
+    if (i == 0 && tiles < 150.0) {
+      parts = (int)(224.0 / tiles);
+      if (parts > 8) parts = 8;
+      if (parts > stages / 6) parts = stages / 6;
+      if (parts < 1) parts = 1;
+    }
+    best.kind = 2 + i;
+    best.tile_rows = m.bm;
+    best.parts = parts;
+    best.part_bytes = parts > 1 ? (size_t)parts * rows * cols * m.bn * 4 : 0;
+  }
+  return best;
+}
+
+template <int P>
+static void tiles_launch(const I8Args& a, const I8Plan& plan, int max_tiles, hipStream_t s) {
+  if (plan.kind == 2) tile_launch<TileCfg<64, 64, 2, 2, P, 2>>(a, max_tiles, plan.parts, s);
+  else if (plan.kind == 3) tile_launch<TileCfg<128, 64, 2, 2, P, 2>>(a, max_tiles, plan.parts, s);
+  else if (plan.kind == 4) tile_launch<TileCfg<128, 128, 2, 2, P, 2>>(a, max_tiles, plan.parts, s);
+  else tile_launch<TileCfg<256, 256, 4, 2, P, 2>>(a, max_tiles, plan.parts, s);
+}
+
+bool i8_launchable(const I8Plan& plan, int n, bool swiglu, int max_tiles) {
+  const size_t bn = plan.kind <= 1 ? 32 : plan.kind <= 3 ? 64 : plan.kind == 4 ? 128 : 256;
+  const size_t cols = ((size_t)n * (swiglu ? 2 : 1) + bn - 1) / bn;
+  return cols * max_tiles * plan.parts < ((size_t)1 << 31) / 512;  // threads of a launch, and ids in int
+}
+
+hipError_t launch_gemm_i8(const I8Args& a, const I8Plan& plan, int max_tiles, hipStream_t s) {
+  if (plan.kind == 0) stream_launch<1, 2, 4, 3>(a, max_tiles, s);
+  else if (plan.kind == 1) stream_launch<2, 2, 4, 2>(a, max_tiles, s);
+  else if (a.swiglu) tiles_launch<2>(a, plan, max_tiles, s);
+  else tiles_launch<1>(a, plan, max_tiles, s);
   return hipGetLastError();
 }
 

@@ -57,6 +57,19 @@ struct Chunk {
 
 __device__ __forceinline__ uint16_t f32_to_f16(float f) { return __half_as_ushort(__float2half(f)); }
 
+// Two values rounded to nearest even and packed, the first one low.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (DT == MOE_DTYPE_BF16) {
+    bf16x2 h;
+    h[0] = (__bf16)a;
+    h[1] = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, h);
+  } else {
+    return (uint32_t)f32_to_f16(a) | ((uint32_t)f32_to_f16(b) << 16);
+  }
+}
+
 __device__ __forceinline__ void store_y(void* y, int dtype, size_t i, float v) {
   if (dtype == MOE_DTYPE_BF16) static_cast<uint16_t*>(y)[i] = f32_to_bf16(v);
   else if (dtype == MOE_DTYPE_F16) static_cast<uint16_t*>(y)[i] = f32_to_f16(v);

@@ -114,9 +114,9 @@ hipError_t launch_route(const void* logits, int dtype, size_t row_stride, int ro
 // A slot-groups buffer: order at byte 0, then offsets, the number of tiles of
 // each map, and the maps.  Map i lists, for every expert that has slots (and
 // for the slots without one, as expert num_experts), the tiles of kTileRows[i]
-// of its positions: {expert, first position}.
-constexpr int kTileMaps = 3;
-constexpr int kTileRows[kTileMaps] = {16, 64, 256};
+// of its positions: {expert | positions << 16, first position}.
+constexpr int kTileMaps = 5;
+constexpr int kTileRows[kTileMaps] = {16, 32, 64, 128, 256};
 struct TileMaps {
   int2* t[kTileMaps];
 };
@@ -145,12 +145,22 @@ struct I8Args {
   void* y;
   int y_dtype;
   // grouped products; order NULL: dense
-  const int32_t *order, *offsets, *num_tiles;
+  const int32_t *order, *num_tiles;
   const int2* tiles;
   int num_experts, x_div;
+  int32_t* parts;  // int32 sums of each part of a split K: [part][position][1 or 2][n]
 };
-int i8_tile_rows(const I8Args& a);
-hipError_t launch_gemm_i8(const I8Args& a, int tile_rows, int max_tiles, hipStream_t s);
+// How a product runs: kernel and tile (kind), rows of a tile, parts that K is
+// split into and the bytes of their sums.  rows: dense rows, or slots of
+// `experts` experts.
+struct I8Plan {
+  int kind, tile_rows, parts;
+  size_t part_bytes;
+};
+I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu);
+// Whether the launch of a plan stays inside the size of a grid.
+bool i8_launchable(const I8Plan& plan, int n, bool swiglu, int max_tiles);
+hipError_t launch_gemm_i8(const I8Args& a, const I8Plan& plan, int max_tiles, hipStream_t s);
 
 int num_cus();
 

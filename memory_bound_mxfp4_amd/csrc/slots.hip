@@ -176,7 +176,7 @@ __global__ __launch_bounds__(64 * W) void k_group_slots(const int32_t* __restric
 #pragma unroll
       for (int k = 0; k < kTileMaps; ++k)
         if ((int)blockIdx.x == k % (int)gridDim.x)  // the maps are shared out over the first blocks
-          for (int p = 0; p < tot[i]; p += kTileRows[k]) maps.t[k][at[1 + k] + p / kTileRows[k]] = int2{e, at[0] + p};
+          for (int p = 0; p < tot[i]; p += kTileRows[k]) maps.t[k][at[1 + k] + p / kTileRows[k]] = int2{e | min(tot[i] - p, kTileRows[k]) << 16, at[0] + p};
 #pragma unroll
       for (int k = 0; k < kTileMaps; ++k) at[1 + k] += (tot[i] + kTileRows[k] - 1) / kTileRows[k];
       at[0] += tot[i];
