@@ -9,7 +9,7 @@
 // fp64: two fp32 scores can tie, or turn round, where the formula does not.
 // But fp64 exponentials of all experts are only computed where a sum of all
 // of them enters the comparison (softmax with a bias) or every expert may
-// count for its group.  Otherwise the selection works on a 32-bit key per
+// count for its group.  Otherwise the selection works on an fp32 key per
 // expert: the logit itself without a bias (the scores grow with it), the fp32
 // score + bias with one.  The k-th largest of the lanes' best keys, T, is no
 // better than the k-th best expert (the lanes are disjoint), so only experts
@@ -18,6 +18,8 @@
 // exact 64-bit key there, and are ranked against each other.  Ties in a
 // logit are cut by index already at T.  More than 64 survivors (equal scores
 // under a bias, or a large k) go the slow way: k rounds over all experts.
+//
+// A long call is bound by vector instructions, a short one by latency.
 #include "i8_common.h"
 #include "moe_device.h"
 
@@ -34,10 +36,11 @@ __device__ __forceinline__ uint64_t readlane64(uint64_t v, int l) {
   return ((uint64_t)hi << 32) | lo;
 }
 
-// The largest T with at least k lanes holding v >= T (0 if fewer than k hold
-// more than 0), and how many hold v >= T.
+// A T with at least k lanes holding v >= T: the largest such T, or a smaller one
+// with at most k + slack lanes above it; 0 if fewer than k hold more than 0.
+// held: how many hold v >= T.
 template <int BITS>
-__device__ __forceinline__ uint32_t kth_largest(uint32_t v, int k, int& held) {
+__device__ __forceinline__ uint32_t kth_largest(uint32_t v, int k, int slack, int& held) {
   uint32_t t = 0;
   held = 64;
 #pragma unroll 1
@@ -47,25 +50,28 @@ __device__ __forceinline__ uint32_t kth_largest(uint32_t v, int k, int& held) {
     if (n >= k) {
       t = c;
       held = n;
-      if (n == k) break;  // T may stay coarse: the same k lanes are above it
+      if (n <= k + slack) break;
     }
   }
   return t;
 }
 
-template <int DT, int KPL>
+// GROUPED: L lanes a group; else the row is one group of 64 lanes.
+template <int DT, int KPL, bool GROUPED>
 __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, size_t row_stride, int rows,
-                                               const float* __restrict__ bias, moe_route_params p, int L,
+                                               const float* __restrict__ bias, moe_route_params p, int lanes,
                                                int32_t* __restrict__ idx_out, float* __restrict__ gate_out) {
-  __shared__ uint32_t list_e[4][64];
-  __shared__ float list_l[4][64];
+  __shared__ float2 list_lb[4][65];  // a survivor's logit and bias
+  __shared__ int list_e[4][65];
+  __shared__ __attribute__((aligned(16))) uint64_t list_k[4][66];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int row_i = blockIdx.x * 4 + wv;
   if (row_i >= rows) return;
   const size_t row = row_i, base = row * row_stride;
-  const int size = p.num_experts / p.groups, grp = lane / L, sub = lane & (L - 1);
+  const int L = GROUPED ? lanes : 64, size = GROUPED ? p.num_experts / p.groups : p.num_experts;
+  const int grp = GROUPED ? lane / L : 0, sub = GROUPED ? lane & (L - 1) : lane;
   const int e0 = grp * size;
-  int mine = grp < p.groups ? size : 0;  // experts of this lane: e0 + sub + L i, sub + L i < mine
+  int mine = !GROUPED || grp < p.groups ? size : 0;  // experts of this lane: e0 + sub + L i, sub + L i < mine
   const bool softmax = p.score == MOE_SCORE_SOFTMAX;
   const float LOWEST = -__builtin_inff();
 
@@ -74,24 +80,36 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
     const float v = load_f32<DT>(logits, base + e0 + at), b = bias ? bias[e0 + at] : 0.0f;
     return v > LOWEST && b > LOWEST ? fminf(v, __FLT_MAX__) : LOWEST;  // both false for NaN
   };
-  uint32_t key[KPL];
-  float l[KPL];
-  uint32_t best = 0;
-#pragma unroll
-  for (int i = 0; i < KPL; ++i) l[i] = sub + L * i < mine ? load_f32<DT>(logits, base + e0 + sub + L * i) : LOWEST;
+  // c: first the logits, then the keys; -inf or NaN: no candidate
+  float l[KPL], b[KPL], c[KPL];
 #pragma unroll
   for (int i = 0; i < KPL; ++i) {
-    const float b = bias && sub + L * i < mine ? bias[e0 + sub + L * i] : 0.0f;
-    l[i] = l[i] > LOWEST && b > LOWEST ? fminf(l[i], __FLT_MAX__) : LOWEST;  // both false for NaN
-    key[i] = l[i] > LOWEST ? order_key(l[i]) : 0u;
-    best = max(best, key[i]);
+    const int at = sub + L * i;
+    l[i] = LOWEST;
+    if (!GROUPED && 64 * (i + 1) <= size) l[i] = load_f32<DT>(logits, base + at);
+    else if (at < mine) l[i] = load_f32<DT>(logits, base + e0 + at);
   }
-  float top = 0.0f;
+  if (bias) {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      const int at = sub + L * i;
+      b[i] = LOWEST;
+      if (!GROUPED && 64 * (i + 1) <= size) b[i] = bias[at];
+      else if (at < mine) b[i] = bias[e0 + at];
+    }
+  }
+  if (!bias || softmax) {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) l[i] = l[i] > LOWEST && (!bias || b[i] > LOWEST) ? fminf(l[i], __FLT_MAX__) : LOWEST;
+  }
+  float best = LOWEST, top = 0.0f;
   double z = 1.0;
   if (softmax) {
-    const uint32_t m = wave_max_u32(best);
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) best = fmaxf(best, l[i]);
+    const uint32_t m = wave_max_u32(best > LOWEST ? order_key(best) : 0u);
     top = m ? order_value(m) : 0.0f;
-    if (bias || p.groups > 1) {
+    if (bias || GROUPED) {
       double sum = 0.0;
 #pragma unroll 1
       for (int at = sub; at < mine; at += L) {
@@ -108,9 +126,22 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
     }
     if (z == 0.0) z = 1.0;
   }
-  auto score = [&](float v) { return softmax ? exp((double)v - (double)top) / z : 1.0 / (1.0 + exp(-(double)v)); };
-
-  if (p.groups > 1) {
+  auto score = [&](float v) {
+    v = fminf(v, __FLT_MAX__);
+    return softmax ? exp((double)v - (double)top) / z : 1.0 / (1.0 + exp(-(double)v));
+  };
+  if (bias) {
+    const float rz = (float)(1.0 / z);
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      const float s = softmax ? __expf(l[i] - top) * rz : __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
+      c[i] = l[i] > LOWEST ? s + b[i] : LOWEST;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) c[i] = l[i];
+  }
+  if (GROUPED) {
     // the two best of each group, first in a lane, then over its lanes
     const double NONE = -__builtin_inf();
     double b1 = NONE, b2 = NONE;
@@ -118,9 +149,9 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
     for (int at = sub; at < mine; at += L) {
       const float v = logit(at);
       if (v > LOWEST) {
-        const double c = score(v) + (bias ? (double)bias[e0 + at] : 0.0);
-        b2 = fmax(b2, fmin(b1, c));
-        b1 = fmax(b1, c);
+        const double t = score(v) + (bias ? (double)bias[e0 + at] : 0.0);
+        b2 = fmax(b2, fmin(b1, t));
+        b1 = fmax(b1, t);
       }
     }
     for (int m = L / 2; m >= 1; m >>= 1) {
@@ -139,75 +170,88 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
     if (!any || before >= p.top_groups) {
       mine = 0;
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) key[i] = 0u;
+      for (int i = 0; i < KPL; ++i) c[i] = LOWEST;
     }
   }
-  uint32_t cut_key, cut_low = 0;  // survivors: key > cut_key, or equal and ~index >= cut_low
-  if (bias) {
-    const float rz = (float)(1.0 / z);
+  best = LOWEST;
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) {
-      const float s = softmax ? __expf(l[i] - top) * rz : __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
-      if (key[i]) key[i] = order_key(s + bias[e0 + sub + L * i]);
-    }
-  }
-  best = 0;
-#pragma unroll
-  for (int i = 0; i < KPL; ++i) best = max(best, key[i]);
-  int held;
-  cut_key = kth_largest<32>(best, p.top_k, held);
+  for (int i = 0; i < KPL; ++i) best = fmaxf(best, c[i]);
+  const uint32_t best_key = best > LOWEST ? order_key(best) : 0u;
+  int held, last_tied = MOE_MAX_EXPERTS;  // of the experts with key T, those up to this index survive
+  const uint32_t cut_key = kth_largest<32>(best_key, p.top_k, 4, held);
+  // below 2^23 in this order lie the NaN and -inf: fewer than k candidates
+  float cut = cut_key < 0x00800000u ? -__FLT_MAX__ : order_value(cut_key);
   if (bias) {
     // fp32 score: under 2^-21 off (exponential, reciprocal, a score is at most
     // 1); the sum: half a step.  Twice that on both sides of T.
-    const float t = order_value(cut_key);
-    if (cut_key && fabsf(t) <= __FLT_MAX__) cut_key = order_key(t - (0x1p-19f + fabsf(t) * 0x1p-22f));
-  } else if (held > p.top_k && cut_key) {
+    if (cut <= __FLT_MAX__) cut = fmaxf(cut - (0x1p-19f + fabsf(cut) * 0x1p-22f), -__FLT_MAX__);
+  } else if (held > p.top_k + 4 && cut_key) {
     // a tie at T: only the lowest indices of those lanes that hold it can come in
     uint32_t low = 0;
 #pragma unroll
     for (int i = KPL - 1; i >= 0; --i)
-      if (key[i] == cut_key) low = 0xFFFu - (uint32_t)(e0 + sub + L * i);
-    const int above = __popcll(__ballot(best > cut_key));
+      if (c[i] == cut) low = 0xFFFu - (uint32_t)(e0 + sub + L * i);
+    const int above = __popcll(__ballot(best_key > cut_key));
     int unused;
-    cut_low = kth_largest<12>(best == cut_key ? low : 0u, p.top_k - above, unused);
+    last_tied = 0xFFF - (int)kth_largest<12>(best_key == cut_key ? low : 0u, p.top_k - above, 0, unused);
   }
-  cut_key = max(cut_key, 1u);  // key 0: no candidate
   int n = 0;
 #pragma unroll
   for (int i = 0; i < KPL; ++i) {
-    const uint32_t e = (uint32_t)(e0 + sub + L * i);
-    const bool in = key[i] > cut_key || (key[i] == cut_key && 0xFFFu - e >= cut_low);
+    if (!GROUPED && 64 * i >= size) continue;
+    const int e = e0 + sub + L * i;
+    bool in = c[i] >= cut;
+    if (last_tied < MOE_MAX_EXPERTS) in = in && (c[i] > cut || e <= last_tied);
     const uint64_t m = __ballot(in);
-    const int at = n + __popcll(m & ((1ull << lane) - 1));
-    if (in && at < 64) {
+    if (in) {
+      const int at = min(n + __popcll(m & ((1ull << lane) - 1)), 64);
       list_e[wv][at] = e;
-      if (!bias) list_l[wv][at] = order_value(key[i]);
+      list_lb[wv][at] = float2{l[i], bias ? b[i] : 0.0f};
     }
     n += __popcll(m);
   }
   __builtin_amdgcn_wave_barrier();
-  int e = -1, place = 64;
+  int e = -1, place = lane;  // without an expert: places from n on stay empty
   double s = 0.0;
   if (n <= 64) {
-    uint64_t k64 = 0;
+    // Keys with the index behind them, so that no two are alike: the logit's 32
+    // bits, or the first 52 of the fp64 score + bias.
+    uint64_t exact = 0, k64 = 0;
     if (lane < n) {
-      e = (int)list_e[wv][lane];
-      const float v = bias ? fminf(load_f32<DT>(logits, base + e), __FLT_MAX__) : list_l[wv][lane];
-      s = score(v);
-      k64 = bias ? order64(s + (double)bias[e]) : (uint64_t)order_key(v);
+      e = list_e[wv][lane];
+      const float2 lb = list_lb[wv][lane];
+      s = score(lb.x);
+      exact = bias ? order64(s + (double)lb.y) : (uint64_t)order_key(lb.x);
+      k64 = bias ? (exact & ~0xFFFull) | (uint64_t)(0xFFF - e) : (exact << 32) | (uint64_t)(0xFFF - e);
     }
-    place = 0;
-    for (int j = 0; j < n; ++j) {
-      const uint64_t o = readlane64(k64, j);
-      const int oe = __builtin_amdgcn_readlane(e, j);
-      place += o > k64 || (o == k64 && oe < e);
+    list_k[wv][lane] = k64;
+    __builtin_amdgcn_wave_barrier();
+    int ahead = 0;
+    for (int j = 0; j < n; j += 2) {
+      typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+      const u64x2 o = *reinterpret_cast<const u64x2*>(&list_k[wv][j]);
+      ahead += (o[0] > k64) + (o[1] > k64);
     }
-    if (lane >= n) place = lane;  // fewer candidates than places: these stay empty
+    if (bias) {
+      // two neighbours with the same 52 bits: all of them, then the index, decide
+      __builtin_amdgcn_wave_barrier();
+      if (lane < n) list_k[wv][ahead] = k64;
+      __builtin_amdgcn_wave_barrier();
+      const bool close = lane < n && ahead + 1 < n && (list_k[wv][ahead + 1] >> 12) == (k64 >> 12);
+      if (__ballot(close)) {
+        ahead = 0;
+        for (int j = 0; j < n; ++j) {
+          const uint64_t o = readlane64(exact, j);
+          const int oe = __builtin_amdgcn_readlane(e, j);
+          ahead += o > exact || (o == exact && oe < e);
+        }
+      }
+    }
+    if (lane < n) place = ahead;
   } else {
     // lane j takes the best expert after the one of place j - 1
     uint64_t last_k = ~0ull;
     int last_e = -1;
-    place = lane;
 #pragma unroll 1
     for (int j = 0; j < p.top_k; ++j) {
       uint64_t bk = 0;
@@ -217,9 +261,9 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
         const int x = e0 + at;
         const float v = logit(at);
         if (!(v > LOWEST)) continue;
-        const uint64_t c = bias ? order64(score(v) + (double)bias[x]) : (uint64_t)order_key(v);
-        if ((c < last_k || (c == last_k && x > last_e)) && c > bk) {
-          bk = c;
+        const uint64_t k = bias ? order64(score(v) + (double)bias[x]) : (uint64_t)order_key(v);
+        if ((k < last_k || (k == last_k && x > last_e)) && k > bk) {
+          bk = k;
           be = x;
         }
       }
@@ -236,7 +280,7 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
       last_e = be;
       if (lane == j) e = be;
     }
-    if (e >= 0) s = score(fminf(load_f32<DT>(logits, base + e), __FLT_MAX__));
+    if (e >= 0) s = score(load_f32<DT>(logits, base + e));
   }
   if (place >= p.top_k) s = 0.0;
   if (p.renorm) {
@@ -256,16 +300,28 @@ static void route_dt(const void* logits, size_t row_stride, int rows, const floa
   while (L * p.groups > 64) L >>= 1;
   const int kpl = (p.num_experts / p.groups + L - 1) / L;
   const dim3 grid((rows + 3) / 4), block(256);
-#define ROUTE(KPL) \
-  hipLaunchKernelGGL((k_route<DT, KPL>), grid, block, 0, s, logits, row_stride, rows, bias, p, L, idx, gate)
-  if (kpl <= 1) ROUTE(1);
-  else if (kpl <= 2) ROUTE(2);
-  else if (kpl <= 4) ROUTE(4);
-  else if (kpl <= 8) ROUTE(8);
-  else if (kpl <= 16) ROUTE(16);
-  else if (kpl <= 32) ROUTE(32);
-  else if (kpl <= 64) ROUTE(64);
-  else ROUTE(128);
+#define ROUTE(KPL)                                                                                                   \
+  if (p.groups > 1)                                                                                                  \
+    hipLaunchKernelGGL((k_route<DT, KPL, true>), grid, block, 0, s, logits, row_stride, rows, bias, p, L, idx, gate); \
+  else                                                                                                               \
+    hipLaunchKernelGGL((k_route<DT, KPL, false>), grid, block, 0, s, logits, row_stride, rows, bias, p, L, idx, gate)
+  if (kpl <= 1) {
+    ROUTE(1);
+  } else if (kpl <= 2) {
+    ROUTE(2);
+  } else if (kpl <= 4) {
+    ROUTE(4);
+  } else if (kpl <= 8) {
+    ROUTE(8);
+  } else if (kpl <= 16) {
+    ROUTE(16);
+  } else if (kpl <= 32) {
+    ROUTE(32);
+  } else if (kpl <= 64) {
+    ROUTE(64);
+  } else {  // many groups leave a lane up to 124 experts
+    hipLaunchKernelGGL((k_route<DT, 128, true>), grid, block, 0, s, logits, row_stride, rows, bias, p, L, idx, gate);
+  }
 #undef ROUTE
 }
 
