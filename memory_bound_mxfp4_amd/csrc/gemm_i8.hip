@@ -189,6 +189,147 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
   }
 }
 
+// One float row of x, quantised on the way: each workgroup finds the row's scale
+// and codes itself (14 KB at K 7168, from L2) while the first stages of its 32
+// matrix rows travel, which costs less than a launch of its own.  Grouped: every
+// slot reads this row.
+constexpr int kTokenChunks = 8;  // of 16 bytes of x a thread
+
+template <int DT, int P>
+__global__ __launch_bounds__(256) void k_i8_token(I8Args a, const u32x4* __restrict__ x, int tiles_n) {
+  constexpr int NW = 4, NN = 2, ST = 3, STAGE = NN * 16 * KS, L = 2 * NN, COLS = 16 * NN / P, N = Chunk<DT>::N, NC = kTokenChunks;
+  __shared__ __attribute__((aligned(1024))) int8_t lds[NW * ST * STAGE];
+  __shared__ __attribute__((aligned(16))) int8_t row[256 * NC * N];  // the codes of x
+  __shared__ uint32_t part[NW];
+  __shared__ int red[NW][16 * NN];
+  Tile t;
+  if (!find_tile<16>(a, blockIdx.x / tiles_n, t)) return;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i0 = blockIdx.x % tiles_n * COLS, K = a.k, C = K / N;
+  if (t.e >= a.num_experts) {  // slots without an expert: rows of zeros
+    for (int i = threadIdx.x; i < t.rows * COLS; i += 256)
+      if (i0 + i % COLS < a.n) store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + i / COLS) * a.n + i0 + i % COLS, 0.0f);
+    return;
+  }
+  u32x4 c[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) c[i] = (int)threadIdx.x + 256 * i < C ? x[threadIdx.x + 256 * i] : u32x4{0u, 0u, 0u, 0u};
+  __builtin_amdgcn_sched_barrier(0);
+  const int lr = lane >> 3, chunk = (lane ^ lr) & 7;
+  const int8_t* src[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int n = min(i0 + (P == 2 ? 8 * i % 16 : 8 * i) + lr, a.n - 1);
+    src[i] = a.w + (((size_t)t.e * P + (P == 2 ? i / 2 : 0)) * a.n + n) * K;
+  }
+  const int stages = (K + KS - 1) / KS, mine = wv < stages ? (stages - wv + NW - 1) / NW : 0;
+  int8_t* ring = lds + wv * ST * STAGE;
+  auto load = [&](int i, int8_t* buf) {  // this wave's i-th stage
+    const int k = min((wv + NW * i) * KS + 16 * chunk, K - 16);
+#pragma unroll
+    for (int j = 0; j < L; ++j) load_to_lds<true>(src[j] + k, buf + 1024 * j);
+  };
+#pragma unroll
+  for (int i = 0; i < ST; ++i)
+    if (i < mine) load(i, ring + i * STAGE);
+  __builtin_amdgcn_sched_barrier(0);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    float v[N];
+    Chunk<DT>::widen(c[i], v);
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = max(m, abs_bits(v[j]));
+  }
+  m = wave_max_bits(m);
+  if (lane == 0) part[wv] = m;
+  wait_lds();
+  meet();
+  const RowScale rs = row_scale(max(max(part[0], part[1]), max(part[2], part[3])));
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    // chunks past K, up to the end of its last stage, come out as zeros
+    const int at = threadIdx.x + 256 * i;
+    if (at >= stages * (KS / N)) break;
+    float v[N];
+    Chunk<DT>::widen(c[i], v);
+    uint32_t o[N / 4];
+    quant_chunk<N>(v, rs, o);
+    if constexpr (N == 8) reinterpret_cast<u32x2*>(row)[at] = u32x2{o[0], o[1]};
+    else reinterpret_cast<uint32_t*>(row)[at] = o[0];
+  }
+  wait_lds();
+  meet();
+  i32x4 acc[NN];
+#pragma unroll
+  for (int j = 0; j < NN; ++j) acc[j] = i32x4{0, 0, 0, 0};
+  int8_t* buf = ring;
+  for (int st = 0; st < mine; ++st) {
+    const int later = mine - 1 - st;
+    if (later >= 2) wait_vm<2 * L>();
+    else if (later == 1) wait_vm<L>();
+    else wait_vm<0>();
+    asm volatile("" ::: "memory");
+    i32x4 fw[2][NN], fx[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      fx[h] = *reinterpret_cast<const i32x4*>(row + (wv + NW * st) * KS + 64 * h + 16 * q);  // the row in all 16 columns
+#pragma unroll
+      for (int j = 0; j < NN; ++j)
+        fw[h][j] = *reinterpret_cast<const i32x4*>(buf + 16 * ((4 * h + q) ^ (r & 7)) + r * KS + 16 * KS * j);
+    }
+    wait_lds();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (st + ST < mine) load(st + ST, buf);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < NN; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h][j], fx[h], acc[j], 0, 0, 0);
+    buf = buf + STAGE == ring + ST * STAGE ? ring : buf + STAGE;
+  }
+  if (r == 0) {
+#pragma unroll
+    for (int j = 0; j < NN; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) red[wv][16 * j + 4 * q + k] = acc[j][k];
+  }
+  __syncthreads();
+  const int n = i0 + (int)threadIdx.x;
+  if ((int)threadIdx.x >= COLS || n >= a.n) return;
+  float v[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int tc = threadIdx.x + 16 * p;
+    const int sum = (red[0][tc] + red[1][tc]) + (red[2][tc] + red[3][tc]);
+    v[p] = (float)sum * (rs.stored * a.w_scale[((size_t)t.e * P + p) * a.n + n]);
+  }
+  const float y = P == 2 ? swiglu_f(v[0], v[P - 1]) : v[0];
+  for (int i = 0; i < t.rows; ++i) store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + i) * a.n + n, y);
+}
+
+bool i8_token_ok(const void* x, int dtype, int k) {
+  const int n = dtype == MOE_DTYPE_F32 ? 4 : 8;  // elements of 16 bytes
+  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && k <= 256 * kTokenChunks * n - KS;
+}
+
+template <int DT>
+static void token_dt(const I8Args& a, const void* x, int max_tiles, hipStream_t s) {
+  const int tiles_n = (a.n * (a.swiglu ? 2 : 1) + 31) / 32;
+  const dim3 grid(tiles_n * max_tiles), block(256);
+  const u32x4* xv = static_cast<const u32x4*>(x);
+  if (a.swiglu) hipLaunchKernelGGL((k_i8_token<DT, 2>), grid, block, 0, s, a, xv, tiles_n);
+  else hipLaunchKernelGGL((k_i8_token<DT, 1>), grid, block, 0, s, a, xv, tiles_n);
+}
+
+hipError_t launch_i8_token(const I8Args& a, const void* x, int dtype, int max_tiles, hipStream_t s) {
+  if (dtype == MOE_DTYPE_BF16) token_dt<MOE_DTYPE_BF16>(a, x, max_tiles, s);
+  else if (dtype == MOE_DTYPE_F16) token_dt<MOE_DTYPE_F16>(a, x, max_tiles, s);
+  else token_dt<MOE_DTYPE_F32>(a, x, max_tiles, s);
+  return hipGetLastError();
+}
+
 // ---- many rows: tiles through LDS ----------------------------------------------
 //
 // A workgroup computes BM rows of x by BN rows of the matrix (with SwiGLU BN/2

@@ -81,4 +81,73 @@ __device__ __forceinline__ void store_y(void* y, int dtype, size_t i, float v) {
 // quotient to -0 for very negative g).
 __device__ __forceinline__ float swiglu_f(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
+// ---- rows to 8-bit codes ---------------------------------------------------------
+//
+// scale = fp32(amax / 127), q = the integer nearest to x / scale, ties to even.
+// The quotient is rounded as if it were exact: in fp64 x * (1 / scale) is within
+// 2^-44 of it, and unless it is the middle between two codes the exact quotient
+// is at least 2^-26 away from one (2 x and an odd multiple of the scale are
+// multiples of 2^-1 of the scale's last bit where they can be that close).  So a
+// first rounding to a multiple of 2^-40 gives the middle exactly where it is one
+// and leaves every other value on its side.
+__device__ __forceinline__ int quant_code(float x, double inv) {
+  const double t = ((double)x * inv + 6144.0) - 6144.0;  // 6144 = 1.5 * 2^12
+  return (int)fmin(fmax(rint(t), -127.0), 127.0);
+}
+
+// Bits of the largest magnitude: NaN and infinity compare above every finite
+// value as integers, so one maximum finds both the scale and a bad row.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+__device__ __forceinline__ uint32_t wave_max_bits(uint32_t m) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, WAVE));
+  return m;
+}
+
+// A row's scale and what its codes are computed with.
+struct RowScale {
+  float stored, inv;
+  double inv64;
+  bool zero;  // all codes 0
+  bool tiny;  // a scale whose fp32 reciprocal would overflow
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
+  RowScale r;
+  const bool bad = amax_bits >= 0x7F800000u;
+  const float s = __uint_as_float(amax_bits) / 127.0f;
+  r.stored = bad ? __uint_as_float(0x7FC00000u) : s;
+  r.zero = bad || s == 0.0f;
+  r.tiny = s < 0x1p-100f;
+  r.inv64 = 1.0 / (double)s;
+  r.inv = (float)r.inv64;
+  return r;
+}
+
+// N codes, four to a dword.  x * inv + 1.5 * 2^23 has the nearest integer to
+// x * inv in its low bits; where that quotient (off by under 2^-15) is not
+// clear of the middle between two codes, the exact rule above decides.
+template <int N>
+__device__ __forceinline__ void quant_chunk(const float* v, const RowScale& r, uint32_t* out) {
+  constexpr float MAGIC = 12582912.0f;
+  uint32_t b[N];
+  float off = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float t = fmaf(v[i], r.inv, MAGIC);
+    b[i] = __float_as_uint(t);
+    off = fmaxf(off, fabsf(fmaf(v[i], r.inv, MAGIC - t)));
+  }
+  if (off > 0.4999f || r.tiny) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] = (uint32_t)quant_code(v[i], r.inv64);
+  }
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const uint32_t lo = __builtin_amdgcn_perm(b[i + 1], b[i], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[i + 3], b[i + 2], 0x0C0C0400u);
+    out[i / 4] = r.zero ? 0u : (lo | (hi << 16));
+  }
+}
+
 }  // namespace moe

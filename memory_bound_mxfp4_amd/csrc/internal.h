@@ -158,6 +158,10 @@ struct I8Plan {
   size_t part_bytes;
 };
 I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu);
+// A product of one float row that the kernel quantises itself, on the tiles of
+// 16 positions; i8_token_ok: the rows it takes.
+bool i8_token_ok(const void* x, int dtype, int k);
+hipError_t launch_i8_token(const I8Args& a, const void* x, int dtype, int max_tiles, hipStream_t s);
 // Whether the launch of a plan stays inside the size of a grid.
 bool i8_launchable(const I8Plan& plan, int n, bool swiglu, int max_tiles);
 hipError_t launch_gemm_i8(const I8Args& a, const I8Plan& plan, int max_tiles, hipStream_t s);

@@ -1,49 +1,9 @@
-// quant.hip -- rows of activations to 8-bit codes with one scale each.
-//
-// scale = fp32(amax / 127), q = the integer nearest to x / scale.  The
-// quotient is rounded as if it were exact: x * (1 / scale) in fp32 is within
-// one unit of it, and x - q * scale, one fused multiply-add, is exact there
-// (both terms are multiples of 2^-25 of the scale's binade and the
-// difference stays under one scale), so comparing twice that remainder with
-// the scale decides which side of the middle between two codes x is on.
+// quant.hip -- rows of activations to 8-bit codes with one scale each, read
+// once: bound by memory (8192 rows of 7168 bf16: 33 us, 5.3 TB/s; one row: 2.6
+// us, latency).
 #include "i8_common.h"
 
 namespace moe {
-
-__device__ __forceinline__ int quant_code(float x, float s, float inv) {
-  float q = rintf(x * inv);
-  const float r = fmaf(-q, s, x), twice = 2.0f * fabsf(r);
-  // past the middle, or on it with an odd code (ties go to the even one)
-  if (twice > s || (twice == s && ((int)q & 1))) q += r > 0.0f ? 1.0f : -1.0f;
-  return (int)fminf(fmaxf(q, -127.0f), 127.0f);
-}
-
-// Bits of the largest magnitude: NaN and infinity compare above every finite
-// value as integers, so one maximum finds both the scale and a bad row.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-__device__ __forceinline__ uint32_t wave_max_bits(uint32_t m) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, WAVE));
-  return m;
-}
-
-// A row's scale and what its codes are computed with.
-struct RowScale {
-  float stored, s, inv, up;  // up: power of two that lifts a scale whose reciprocal would overflow
-  bool zero;                 // all codes 0
-};
-__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
-  RowScale r;
-  const bool bad = amax_bits >= 0x7F800000u;
-  const float s = __uint_as_float(amax_bits) / 127.0f;
-  r.stored = bad ? __uint_as_float(0x7FC00000u) : s;
-  r.zero = bad || s == 0.0f;
-  r.up = s < 0x1p-100f ? 0x1p64f : 1.0f;
-  r.s = s * r.up;
-  r.inv = 1.0f / r.s;
-  return r;
-}
 
 // Any stride, any alignment: element by element, the row read twice.
 template <int DT>
@@ -59,33 +19,7 @@ __global__ __launch_bounds__(256) void k_quant_rows_any(const void* __restrict__
   const RowScale rs = row_scale(max(max(part[0], part[1]), max(part[2], part[3])));
   if (threadIdx.x == 0) scale[row] = rs.stored;
   for (int i = threadIdx.x; i < K; i += 256)
-    q[row * K + i] = rs.zero ? (int8_t)0 : (int8_t)quant_code(load_f32<DT>(x, row * x_stride + i) * rs.up, rs.s, rs.inv);
-}
-
-// N codes, four to a dword.  x * inv + 1.5 * 2^23 has the nearest integer to
-// x * inv in its low bits; where that quotient (off by under 2^-15) is not
-// clear of the middle between two codes, the exact rule above decides.
-template <int N>
-__device__ __forceinline__ void quant_chunk(const float* v, const RowScale& r, uint32_t* out) {
-  constexpr float MAGIC = 12582912.0f;
-  uint32_t b[N];
-  float off = 0.0f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float t = fmaf(v[i], r.inv, MAGIC);
-    b[i] = __float_as_uint(t);
-    off = fmaxf(off, fabsf(fmaf(v[i], r.inv, MAGIC - t)));
-  }
-  if (off > 0.4999f || r.up != 1.0f) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) b[i] = (uint32_t)quant_code(v[i] * r.up, r.s, r.inv);
-  }
-#pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const uint32_t lo = __builtin_amdgcn_perm(b[i + 1], b[i], 0x0C0C0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(b[i + 3], b[i + 2], 0x0C0C0400u);
-    out[i / 4] = r.zero ? 0u : (lo | (hi << 16));
-  }
+    q[row * K + i] = rs.zero ? (int8_t)0 : (int8_t)quant_code(load_f32<DT>(x, row * x_stride + i), rs.inv64);
 }
 
 // Aligned rows of at most NC 16-byte chunks a thread: a row is read once, all

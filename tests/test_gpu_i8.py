@@ -445,3 +445,50 @@ def test_two_streams_at_once():
             l(*d, o, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(alone, outs))
+
+
+# ---- one float row, quantised inside the product ------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,k", [(1, 16), (40, 112), (33, 128), (100, 1040), (77, 4096), (64, 8064), (50, 16256), (50, 16272), (24, 65536)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_gemm_of_one_row(dtype, n, k, swiglu):
+    """Every length of the row, past the one that a workgroup quantises too; the bits of the two calls in a row."""
+    import torch
+    x, v = _x(1, k, dtype, n + k, sigma=2.0)
+    w, ws = _w((2, n, k) if swiglu else (n, k), k)
+    y = moe.gemm_i8(x, _dev(w), _dev(ws), swiglu=swiglu, out_dtype=torch.float32)
+    codes, scales = ref.quant(v)
+    if swiglu:
+        g, u = ref.product(codes, scales, w[0], ws[0]), ref.product(codes, scales, w[1], ws[1])
+        _close(y, ref.silu(g) * u, ref.swiglu_bound(g, u, "f32"))
+    else:
+        want = ref.product(codes, scales, w, ws)
+        _close(y, want, ref.product_bound(want, "f32"))
+    q, s = moe.quant_rows_i8(x)
+    assert torch.equal(y, moe.gemm_i8(q, _dev(w), _dev(ws), x_scale=s, swiglu=swiglu, out_dtype=torch.float32))
+
+
+def test_gemm_of_one_row_extremes():
+    import torch
+    n, k = 48, 640
+    w, ws = _w((n, k), 3)
+    for fill in (0.0, float("nan"), float("inf"), 2.0 ** -149, 3e38):
+        x = torch.zeros(1, k)
+        x[0, 7] = fill
+        x[0, 300] = 2.0 ** -140
+        y = moe.gemm_i8(x.cuda(), _dev(w), _dev(ws), out_dtype=torch.float32)
+        q, s = moe.quant_rows_i8(x.cuda())
+        z = moe.gemm_i8(q, _dev(w), _dev(ws), x_scale=s, out_dtype=torch.float32)
+        assert torch.equal(torch.isnan(y), torch.isnan(z)) and torch.equal(torch.nan_to_num(y), torch.nan_to_num(z))
+    x = torch.randn(1, k + 3)[:, 3:].cuda()  # not 16-byte aligned
+    q, s = moe.quant_rows_i8(x)
+    assert torch.equal(moe.gemm_i8(x, _dev(w), _dev(ws)), moe.gemm_i8(q, _dev(w), _dev(ws), x_scale=s))
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("idx", [[5], [0, 3, 5, 2], [1, -1, 1, 4], [-1, -1], [2] * 20, list(range(6)) * 8])
+def test_experts_of_one_token(idx, swiglu):
+    """One token: distinct experts, one that comes twice, none, more slots than a tile."""
+    _experts_case(1, len(idx), 6, 50, 272, swiglu, False, "bf16", "f32", idx=np.array([idx], np.int32))
