@@ -61,6 +61,17 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4));
 }
 
+// Waits until at most the newest n of a ring's stages are out; n is a constant
+// where this is called.
+template <int ST, int L>
+__device__ __forceinline__ void wait_ring(int n) {
+  static_assert(ST <= 4, "ring");
+  if (n >= 3) wait_vm<3 * L>();
+  else if (n == 2) wait_vm<2 * L>();
+  else if (n == 1) wait_vm<L>();
+  else wait_vm<0>();
+}
+
 // Waits for the wave's LDS reads alone.
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
 
@@ -130,14 +141,8 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
 #pragma unroll
     for (int j = 0; j < NN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
   int8_t* buf = ring;
-  for (int st = 0; st < mine; ++st) {
-    const int later = mine - 1 - st;  // stages that are out behind this one
-    if (later >= ST - 1) wait_vm<(ST - 1) * L>();
-    else if (ST > 3 && later == 2) wait_vm<2 * L>();
-    else if (ST > 2 && later == 1) wait_vm<L>();
-    else wait_vm<0>();
-    asm volatile("" ::: "memory");
-    i32x4 fw[2][NN], fx[2][NX];
+  i32x4 fw[2][NN], fx[2][NX];
+  auto read = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int8_t* at = buf + 16 * ((4 * h + q) ^ (r & 7)) + r * KS;
@@ -149,7 +154,8 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
     wait_lds();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    if (st + ST < mine) load(st + ST, buf);
+  };
+  auto multiply = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -158,6 +164,23 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
         for (int j = 0; j < NN; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h][j], fx[h][i], acc[i][j], 0, 0, 0);
     buf = buf + STAGE == ring + ST * STAGE ? ring : buf + STAGE;
+  };
+  // no branch in this loop, as in the tiles below; then what is left in the ring
+  for (int st = 0; st < mine - ST; ++st) {
+    wait_vm<(ST - 1) * L>();
+    asm volatile("" ::: "memory");
+    read();
+    load(st + ST, buf);
+    multiply();
+  }
+  if (mine < ST) wait_vm<0>();
+#pragma unroll
+  for (int j = 0; j < ST; ++j) {
+    if (j >= mine) break;
+    wait_ring<ST, L>(ST - 1 - j);
+    asm volatile("" ::: "memory");
+    read();
+    multiply();
   }
   for (int i = threadIdx.x; i < 16 * NN; i += T) {
     const int n = min(i0 + (P == 2 ? i / 32 * 16 + i % 16 : i), a.n - 1);
@@ -265,13 +288,8 @@ __global__ __launch_bounds__(256) void k_i8_token(I8Args a, const u32x4* __restr
 #pragma unroll
   for (int j = 0; j < NN; ++j) acc[j] = i32x4{0, 0, 0, 0};
   int8_t* buf = ring;
-  for (int st = 0; st < mine; ++st) {
-    const int later = mine - 1 - st;
-    if (later >= 2) wait_vm<2 * L>();
-    else if (later == 1) wait_vm<L>();
-    else wait_vm<0>();
-    asm volatile("" ::: "memory");
-    i32x4 fw[2][NN], fx[2];
+  i32x4 fw[2][NN], fx[2];
+  auto read = [&](int st) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       fx[h] = *reinterpret_cast<const i32x4*>(row + (wv + NW * st) * KS + 64 * h + 16 * q);  // the row in all 16 columns
@@ -282,12 +300,29 @@ __global__ __launch_bounds__(256) void k_i8_token(I8Args a, const u32x4* __restr
     wait_lds();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    if (st + ST < mine) load(st + ST, buf);
+  };
+  auto multiply = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < NN; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h][j], fx[h], acc[j], 0, 0, 0);
     buf = buf + STAGE == ring + ST * STAGE ? ring : buf + STAGE;
+  };
+  for (int st = 0; st < mine - ST; ++st) {
+    wait_vm<(ST - 1) * L>();
+    asm volatile("" ::: "memory");
+    read(st);
+    load(st + ST, buf);
+    multiply();
+  }
+  if (mine < ST) wait_vm<0>();
+#pragma unroll
+  for (int j = 0; j < ST; ++j) {
+    if (j >= mine) break;
+    wait_ring<ST, L>(ST - 1 - j);
+    asm volatile("" ::: "memory");
+    read(max(mine - ST, 0) + j);
+    multiply();
   }
   if (r == 0) {
 #pragma unroll
@@ -343,7 +378,7 @@ template <int BM_, int BN_, int WGM_, int WGN_, int P_, int ST_>
 struct TileCfg {
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, P = P_, ST = ST_;
   static constexpr int NW = WGM * WGN, T = 64 * NW, MF = BM / WGM / 16, NF = BN / WGN / 16;  // fragments of a wave
-  static constexpr bool SPLIT = BM == 64;  // K may be split over workgroups
+  static constexpr bool SPLIT = BM == 64 && BN == 64;  // K may be split over workgroups
   static constexpr int STAGE = (BM + BN) * KS, RING = ST * STAGE;
   // Rows of outputs on their way through LDS: C columns of B bytes and 16
   // more, which spreads the rows of a fragment over the banks.
@@ -497,13 +532,17 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
   }
   const int stages = (K + KS - 1) / KS;
   const int s0 = (int)((size_t)stages * part / parts), S = (int)((size_t)stages * (part + 1) / parts);
-  auto load = [&](int st) {
+  auto load_whole = [&](int st) {
     int8_t* buf = lds + (st & (ST - 1)) * C::STAGE;
-    const int k = st * KS + 16 * chunk;
-    if ((st + 1) * KS <= K) {
 #pragma unroll
-      for (int i = 0; i < L; ++i) load_to_lds(src[i] + k, buf + 1024 * (wv + NW * i));
+    for (int i = 0; i < L; ++i) load_to_lds(src[i] + (st * KS + 16 * chunk), buf + 1024 * (wv + NW * i));
+  };
+  auto load = [&](int st) {
+    if ((st + 1) * KS <= K) {
+      load_whole(st);
     } else {  // the last stage of a K that is no multiple of 128: zeros past K on x's side
+      int8_t* buf = lds + (st & (ST - 1)) * C::STAGE;
+      const int k = st * KS + 16 * chunk;
 #pragma unroll
       for (int i = 0; i < L; ++i)
         load_to_lds(wv + NW * i < GX && k >= K ? kZeroCodes : src[i] + min(k, K - 16), buf + 1024 * (wv + NW * i));
@@ -545,6 +584,9 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
     else if (later == 1) wait_vm<L>();
     else wait_vm<0>();
   };
+  // Stages whose own load is a whole one go first, in a loop without a branch (each
+  // costs tens of clocks, and a stage of a small tile is a few hundred).
+  int st = s0;
   if constexpr (NW == 8) {
     // Two waves a SIMD, of two groups one step apart: while the waves of one
     // group multiply, those of the other read the fragments of half a stage from
@@ -555,33 +597,50 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
     landed(min(ST - 2, S - 1 - s0));
     meet();
     if (second) meet();
-    for (int st = s0; st < S; ++st) {
-      read(st, 0);
-      if (st + ST - 1 < S) load(st + ST - 1);  // into the buffer of stage st - 1, which both groups have read
-      wait_lds();
+    auto turn = [&]() {
       meet();
       __builtin_amdgcn_s_setprio(1);
       multiply();
       __builtin_amdgcn_s_setprio(0);
       meet();
+    };
+    for (; st < S - ST; ++st) {
+      read(st, 0);
+      load_whole(st + ST - 1);  // into the buffer of stage st - 1, which both groups have read
+      wait_lds();
+      turn();
+      read(st, 1);
+      wait_vm<(ST - 2) * L>();
+      turn();
+    }
+    for (; st < S; ++st) {
+      read(st, 0);
+      if (st + ST - 1 < S) load(st + ST - 1);
+      wait_lds();
+      turn();
       read(st, 1);
       landed(min(ST - 2, S - 2 - st));
-      meet();
-      __builtin_amdgcn_s_setprio(1);
-      multiply();
-      __builtin_amdgcn_s_setprio(0);
-      meet();
+      turn();
     }
     if (!second) meet();
   } else {
-    for (int st = s0; st < S; ++st) {
-      landed(min(ST - 2, S - 1 - st));
-      meet();
-      if (st + ST - 1 < S) load(st + ST - 1);  // every wave is past stage st - 1: its buffer is free
+    auto multiply_stage = [&](int st) {
       read(st, 0);
       multiply();
       read(st, 1);
       multiply();
+    };
+    for (; st < S - ST; ++st) {
+      wait_vm<(ST - 2) * L>();
+      meet();
+      load_whole(st + ST - 1);  // every wave is past stage st - 1: its buffer is free
+      multiply_stage(st);
+    }
+    for (; st < S; ++st) {
+      landed(min(ST - 2, S - 1 - st));
+      meet();
+      if (st + ST - 1 < S) load(st + ST - 1);
+      multiply_stage(st);
     }
   }
   if constexpr (C::SPLIT) {
@@ -656,14 +715,16 @@ static void stream_launch(const I8Args& a, int max_tiles, hipStream_t s) {
 // x by 32 matrix rows; up to 32 (24): 32 by 32.  Measured at N 7168, K 7168:
 // 1 row 10.3 us, 8 rows 11.4, 32 rows 15.0 (64 x 64 tiles, K in two parts: 16.5);
 // at N 65536 8 rows 72 us (6.5 TB/s), 32 rows 90 (64 x 64 tiles: 88).
-// Above that the tile with the least estimated time, c0 + c1 * T / 256 per 56
-// stages (K 7168) for T workgroups; the larger tiles run one or two to a CU, so
-// theirs go in whole rounds of 256.  Measured at N 7168, K 7168: 256 x 256 95 us at
-// 224 tiles, 373 us at 896; 128 x 128 42 us at 224, 68 at 448, 415 at 3584;
-// 128 x 64 30 us at 224, 51 at 448; 64 x 64 22 us at 224, 34 at 448, 128 at 2048.
+// Above that the tile with the least estimated time for T workgroups per 56
+// stages (K 7168): c0 + c1 * T / 256, the larger tiles in whole rounds of 256,
+// since they run one or two to a CU; up to 256 workgroups, where each has a CU to
+// itself and a stage is a chain of latencies, `lone`.  Measured at N 7168, K 7168:
+// 64 x 64 23 us at 224 tiles, 34 at 448; 64 x 128 30 us at 224, 57 at 448; 128 x 128
+// 38 us at 224 (four buffers), 66 at 448 and 127 at 896 (two buffers, two
+// workgroups to a CU; four: 73, 141); 256 x 256 94 us at 224, 356 at 896.
 // K is split over parts while 64 x 64 tiles leave CUs without work (64 rows of
-// N 7168: 18 us in 2 parts, 44 in one; 128 rows of N 1536: 13 us in 4 parts, 23
-// in one).
+// N 7168: 18 us in 2 parts, 22 in one; 37 rows of N 1536: 11 us in 6 parts, 17 in
+// one).
 I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
   const int used = grouped ? (rows < experts ? rows : experts) : 1;
   const double per = (double)rows / used;
@@ -671,11 +732,13 @@ I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
   if (per <= (grouped ? 24 : 32)) return {1, 32, 1, 0};
   struct Model {
     int bm, bn;
-    double c0, c1;
+    double c0, c1, lone;
     bool rounds;
   };
-  static constexpr Model models[] = {
-      {64, 64, 4.0, 17.0, false}, {128, 64, 9.0, 21.0, true}, {128, 128, 12.0, 29.0, true}, {256, 256, 4.0, 91.0, true}};
+  static constexpr Model models[] = {{64, 64, 4.0, 16.0, 22.5, false},
+                                     {64, 128, 3.0, 27.0, 30.5, true},
+                                     {128, 128, 10.0, 28.0, 38.0, true},
+                                     {256, 256, 3.0, 89.0, 92.0, true}};
   const int P = swiglu ? 2 : 1, stages = (k + KS - 1) / KS;
   I8Plan best{};
   double least = 0.0;
@@ -685,8 +748,8 @@ I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
     // the rows of an expert end inside a tile: half a tile lost on average
     const double down = grouped ? (double)rows / m.bm + 0.5 * used : (rows + m.bm - 1) / m.bm;
     const double tiles = down * cols;
-    const double load = m.rounds ? ceil(tiles / 256.0) : fmax(tiles / 256.0, 1.0);
-    const double time = m.c0 + m.c1 * load * stages / 56.0;
+    const double load = m.rounds ? ceil(tiles / 256.0) : tiles / 256.0;
+    const double time = tiles <= 256.0 ? m.lone * stages / 56.0 : m.c0 + m.c1 * load * stages / 56.0;
     if (i && time >= least) continue;
     least = time;
     int parts = 1;
@@ -696,7 +759,7 @@ I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
       if (parts > stages / 6) parts = stages / 6;
       if (parts < 1) parts = 1;
     }
-    best.kind = 2 + i;
+    best.kind = i < 2 ? 2 + i : i == 2 && tiles <= 256.0 ? 4 : 3 + i;
     best.tile_rows = m.bm;
     best.parts = parts;
     best.part_bytes = parts > 1 ? (size_t)parts * rows * cols * m.bn * 4 : 0;
@@ -706,14 +769,15 @@ I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
 
 template <int P>
 static void tiles_launch(const I8Args& a, const I8Plan& plan, int max_tiles, hipStream_t s) {
-  if (plan.kind == 2) tile_launch<TileCfg<64, 64, 2, 2, P, 2>>(a, max_tiles, plan.parts, s);
-  else if (plan.kind == 3) tile_launch<TileCfg<128, 64, 2, 2, P, 2>>(a, max_tiles, plan.parts, s);
-  else if (plan.kind == 4) tile_launch<TileCfg<128, 128, 2, 2, P, 2>>(a, max_tiles, plan.parts, s);
-  else tile_launch<TileCfg<256, 256, 4, 2, P, 2>>(a, max_tiles, plan.parts, s);
+  if (plan.kind == 2) tile_launch<TileCfg<64, 64, 2, 2, P, 4>>(a, max_tiles, plan.parts, s);
+  else if (plan.kind == 3) tile_launch<TileCfg<64, 128, 2, 2, P, 4>>(a, max_tiles, 1, s);
+  else if (plan.kind == 4) tile_launch<TileCfg<128, 128, 4, 2, P, 4>>(a, max_tiles, 1, s);
+  else if (plan.kind == 5) tile_launch<TileCfg<128, 128, 4, 2, P, 2>>(a, max_tiles, 1, s);
+  else tile_launch<TileCfg<256, 256, 4, 2, P, 2>>(a, max_tiles, 1, s);
 }
 
 bool i8_launchable(const I8Plan& plan, int n, bool swiglu, int max_tiles) {
-  const size_t bn = plan.kind <= 1 ? 32 : plan.kind <= 3 ? 64 : plan.kind == 4 ? 128 : 256;
+  const size_t bn = plan.kind <= 1 ? 32 : plan.kind == 2 ? 64 : plan.kind <= 5 ? 128 : 256;
   const size_t cols = ((size_t)n * (swiglu ? 2 : 1) + bn - 1) / bn;
   return cols * max_tiles * plan.parts < ((size_t)1 << 31) / 512;  // threads of a launch, and ids in int
 }
