@@ -654,6 +654,8 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
   else tile_store<MOE_DTYPE_F32, C>(a, t, lds, i0, wm, wn, acc);
 }
 
+constexpr int kMaxParts = 8;
+
 // The parts of a split K added up, scaled and stored: a workgroup takes 4 rows
 // (a wave each) by 256 columns of a tile.
 template <class C>
@@ -672,8 +674,12 @@ __global__ __launch_bounds__(256) void k_i8_parts(I8Args a, int parts, int tiles
   float v[P][4];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    i32x4 sum{0, 0, 0, 0};
-    for (int i = 0; i < parts; ++i) sum += *reinterpret_cast<const i32x4*>(src + i * step + 16 * p);
+    i32x4 sum{0, 0, 0, 0}, part[kMaxParts];  // all parts requested before the first is added
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i)
+      part[i] = *reinterpret_cast<const i32x4*>(src + min(i, parts - 1) * step + 16 * p);
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) sum += i < parts ? part[i] : i32x4{0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[p][k] = (float)sum[k] * (sx * sw[p * a.n + min(n + k, a.n - 1)]);
   }
@@ -755,7 +761,7 @@ I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
     int parts = 1;
     if (i == 0 && tiles < 150.0) {
       parts = (int)(224.0 / tiles);
-      if (parts > 8) parts = 8;
+      if (parts > kMaxParts) parts = kMaxParts;
       if (parts > stages / 6) parts = stages / 6;
       if (parts < 1) parts = 1;
     }

@@ -4,8 +4,10 @@
 
 namespace moe {
 
-// Slots that one workgroup sorts: 4 rounds of 64 a wave, held in registers.
-static constexpr int kOneBlock = 4096;
+// Slots that one workgroup sorts: 4 rounds of 64 for each of 4 waves, held in
+// registers.  (With 16 waves a workgroup the two launches of 32768 slots took 7 and
+// 18 us.)
+static constexpr int kOneBlock = 1024;
 
 GroupsLayout groups_layout(int tokens, int top_k, int E) {
   GroupsLayout g;
@@ -21,7 +23,7 @@ GroupsLayout groups_layout(int tokens, int top_k, int E) {
     g.max_tiles[i] = (int)(slots / kTileRows[i] + partial);
     o += align256(8 * (size_t)g.max_tiles[i]);
   }
-  // blocks of the sort: one up to kOneBlock slots, then blocks of that many, at most 64
+  // workgroups of the sort: one up to kOneBlock slots, then one for that many, at most 64
   g.blocks = slots <= (size_t)kOneBlock ? 1 : (int)((slots + kOneBlock - 1) / kOneBlock < 64 ? (slots + kOneBlock - 1) / kOneBlock : 64);
   g.hist = o;
   if (g.blocks > 1) o += align256(4 * ((size_t)E + 1) * g.blocks);
@@ -29,10 +31,12 @@ GroupsLayout groups_layout(int tokens, int top_k, int E) {
   return g;
 }
 
-// Lanes of the wave that hold the same key (of `bits` bits) as this one.
-__device__ __forceinline__ uint64_t same_key(int key, int bits, uint64_t active) {
+// Lanes of the wave that hold the same key (of BITS bits) as this one.
+template <int BITS>
+__device__ __forceinline__ uint64_t same_key(int key, uint64_t active) {
   uint64_t m = active;
-  for (int b = 0; b < bits; ++b) {
+#pragma unroll
+  for (int b = 0; b < BITS; ++b) {
     const uint64_t bal = __ballot((key >> b) & 1);
     m &= ((key >> b) & 1) ? bal : ~bal;
   }
@@ -88,17 +92,17 @@ __global__ __launch_bounds__(64 * W) void k_group_slots(const int32_t* __restric
                                                         int E, int32_t* __restrict__ order,
                                                         int32_t* __restrict__ offsets, int32_t* __restrict__ counts,
                                                         int32_t* __restrict__ hist, TileMaps maps) {
-  constexpr int R = 4, NV = 1 + kTileMaps;
+  constexpr int R = 4, NV = 1 + kTileMaps, BITS = EMAX <= 1024 ? 11 : 13;  // keys 0 .. E, E: no expert
   __shared__ int cnt[W * (EMAX + 1)];
   __shared__ int part[W][NV];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, E1 = E + 1;
   int* mine = cnt + wv * E1;
   for (int i = threadIdx.x; i < W * E1; i += 64 * W) cnt[i] = 0;
-  const int bits = 32 - __clz(E);  // keys 0 .. E, E: no expert
   const int b0 = min((int)blockIdx.x * per_block, slots), b1 = min(b0 + per_block, slots);
   const int per = ((b1 - b0 + W - 1) / W + 63) / 64 * 64;
   const int s0 = min(b0 + wv * per, b1), s1 = min(s0 + per, b1);
   int key[R];
+  uint64_t same[R];
   auto fetch = [&](int b) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -106,6 +110,8 @@ __global__ __launch_bounds__(64 * W) void k_group_slots(const int32_t* __restric
       const int e = s < s1 ? idx[s] : E;
       key[i] = (unsigned)e < (unsigned)E ? e : E;
     }
+#pragma unroll
+    for (int i = 0; i < R; ++i) same[i] = same_key<BITS>(key[i], __ballot(b + 64 * i + lane < s1));
   };
   fetch(s0);
   __syncthreads();
@@ -113,9 +119,7 @@ __global__ __launch_bounds__(64 * W) void k_group_slots(const int32_t* __restric
     if (b > s0) fetch(b);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const bool in = b + 64 * i + lane < s1;
-      const uint64_t m = same_key(key[i], bits, __ballot(in));
-      if (in && (m & ((1ull << lane) - 1)) == 0) mine[key[i]] += __popcll(m);
+      if (b + 64 * i + lane < s1 && (same[i] & ((1ull << lane) - 1)) == 0) mine[key[i]] += __popcll(same[i]);
       __builtin_amdgcn_wave_barrier();
     }
   }
@@ -141,10 +145,15 @@ __global__ __launch_bounds__(64 * W) void k_group_slots(const int32_t* __restric
     tot[i] = ahead[i] = 0;
     if (i < ept && e < E1) {
       if (PHASE == 2) {
-        for (int g = 0; g < (int)gridDim.x; ++g) {
-          const int c = hist[(size_t)g * E1 + e];
-          tot[i] += c;
-          ahead[i] += g < (int)blockIdx.x ? c : 0;
+        for (int g = 0; g < (int)gridDim.x; g += 8) {  // eight loads at a time
+          int c[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) c[u] = hist[(size_t)min(g + u, (int)gridDim.x - 1) * E1 + e];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            tot[i] += g + u < (int)gridDim.x ? c[u] : 0;
+            ahead[i] += g + u < (int)blockIdx.x ? c[u] : 0;
+          }
         }
       } else {
 #pragma unroll
@@ -165,18 +174,24 @@ __global__ __launch_bounds__(64 * W) void k_group_slots(const int32_t* __restric
   for (int i = 0; i < EPT; ++i) {
     const int e = threadIdx.x * ept + i;
     if (i < ept && e < E1) {
-      int run = at[0] + ahead[i];
+      int run = at[0] + ahead[i], c[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) c[w] = cnt[w * E1 + e];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const int c = cnt[w * E1 + e];
         cnt[w * E1 + e] = run;
-        run += c;
+        run += c[w];
       }
       if (blockIdx.x == 0) offsets[e] = at[0];
 #pragma unroll
-      for (int k = 0; k < kTileMaps; ++k)
-        if ((int)blockIdx.x == k % (int)gridDim.x)  // the maps are shared out over the first blocks
-          for (int p = 0; p < tot[i]; p += kTileRows[k]) maps.t[k][at[1 + k] + p / kTileRows[k]] = int2{e | min(tot[i] - p, kTileRows[k]) << 16, at[0] + p};
+      for (int k = 0; k < kTileMaps; ++k) {
+        // the maps are shared out over the workgroups: those of map k take its tiles in turn
+        const int groups = min((int)gridDim.x, kTileMaps), sharers = (int)gridDim.x / groups;
+        const int turn = (int)blockIdx.x / groups;
+        if ((int)blockIdx.x % groups != k % groups || turn >= sharers) continue;
+        for (int p = turn * kTileRows[k]; p < tot[i]; p += sharers * kTileRows[k])
+          maps.t[k][at[1 + k] + p / kTileRows[k]] = int2{e | min(tot[i] - p, kTileRows[k]) << 16, at[0] + p};
+      }
 #pragma unroll
       for (int k = 0; k < kTileMaps; ++k) at[1 + k] += (tot[i] + kTileRows[k] - 1) / kTileRows[k];
       at[0] += tot[i];
@@ -189,13 +204,12 @@ __global__ __launch_bounds__(64 * W) void k_group_slots(const int32_t* __restric
     for (int i = 0; i < R; ++i) {
       const int s = b + 64 * i + lane;
       const bool in = s < s1;
-      const uint64_t m = same_key(key[i], bits, __ballot(in));
-      const int rank = __popcll(m & ((1ull << lane) - 1));
+      const int rank = __popcll(same[i] & ((1ull << lane) - 1));
       const int base = in ? mine[key[i]] : 0;
       __builtin_amdgcn_wave_barrier();
       if (in) {
         order[base + rank] = s;
-        if (rank == 0) mine[key[i]] = base + __popcll(m);
+        if (rank == 0) mine[key[i]] = base + __popcll(same[i]);
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -217,16 +231,16 @@ hipError_t launch_group_slots(const int32_t* idx, int tokens, int top_k, int E, 
                      offsets, counts, hist, maps)
   if (E <= 1024) {
     if (nb == 1) {
-      GROUP(16, 1024, 0, 1);
+      GROUP(4, 1024, 0, 1);
     } else {
-      GROUP(16, 1024, 1, nb);
-      GROUP(16, 1024, 2, nb);
+      GROUP(4, 1024, 1, nb);
+      GROUP(4, 1024, 2, nb);
     }
   } else if (nb == 1) {
-    GROUP(8, MOE_MAX_EXPERTS, 0, 1);
+    GROUP(4, MOE_MAX_EXPERTS, 0, 1);
   } else {
-    GROUP(8, MOE_MAX_EXPERTS, 1, nb);
-    GROUP(8, MOE_MAX_EXPERTS, 2, nb);
+    GROUP(4, MOE_MAX_EXPERTS, 1, nb);
+    GROUP(4, MOE_MAX_EXPERTS, 2, nb);
   }
 #undef GROUP
   return hipGetLastError();
