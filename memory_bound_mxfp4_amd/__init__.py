@@ -9,6 +9,7 @@ raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -378,6 +379,12 @@ class RouteParamsC(ctypes.Structure):
                 ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+@functools.lru_cache(maxsize=256)
+def _route_params(*fields):
+    """The C struct of a routing, by reference; a decode step routes the same way again and again."""
+    return ctypes.byref(RouteParamsC(*fields))
+
+
 _SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 _dtypes: dict = {}
 
@@ -455,12 +462,12 @@ def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int
     code = _dtype_code(logits.dtype, "logits")
     if bias is not None:
         _want(bias, (E,), torch.float32, dev, "bias")
-    p = RouteParamsC(E, top_k, _SCORES[score], groups, top_groups, group_top, int(renorm), scale)
+    p = _route_params(E, top_k, _SCORES[score], groups, top_groups, group_top, int(renorm), scale)
     shape = (rows, top_k)
     idx = torch.empty(shape, dtype=torch.int32, device=dev) if idx is None else _want(idx, shape, torch.int32, dev, "idx")
     gate = torch.empty(shape, dtype=torch.float32, device=dev) if gate is None else \
         _want(gate, shape, torch.float32, dev, "gate")
-    _launch("moe_route", dev, stream, _addr(logits), code, stride, rows, _addr(bias), ctypes.byref(p), _addr(idx), _addr(gate))
+    _launch("moe_route", dev, stream, _addr(logits), code, stride, rows, _addr(bias), p, _addr(idx), _addr(gate))
     return idx, gate
 
 

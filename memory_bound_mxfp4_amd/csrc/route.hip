@@ -41,17 +41,17 @@ __device__ __forceinline__ uint64_t readlane64(uint64_t v, int l) {
 // held: how many hold v >= T.
 template <int BITS>
 __device__ __forceinline__ uint32_t kth_largest(uint32_t v, int k, int slack, int& held) {
+  static_assert(BITS % 2 == 0, "two bits a round: a round costs a branch and little else");
   uint32_t t = 0;
   held = 64;
 #pragma unroll 1
-  for (int b = BITS - 1; b >= 0; --b) {
-    const uint32_t c = t | (1u << b);
-    const int n = __popcll(__ballot(v >= c));
-    if (n >= k) {
-      t = c;
-      held = n;
-      if (n <= k + slack) break;
-    }
+  for (int b = BITS - 2; b >= 0; b -= 2) {
+    const uint32_t c1 = t | (1u << b), c2 = t | (2u << b), c3 = t | (3u << b);
+    const int n1 = __popcll(__ballot(v >= c1)), n2 = __popcll(__ballot(v >= c2)), n3 = __popcll(__ballot(v >= c3));
+    const int n = n3 >= k ? n3 : n2 >= k ? n2 : n1;
+    t = n3 >= k ? c3 : n2 >= k ? c2 : n1 >= k ? c1 : t;
+    held = n >= k ? n : held;
+    if (n >= k && n <= k + slack) break;
   }
   return t;
 }
@@ -111,10 +111,15 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
     top = m ? order_value(m) : 0.0f;
     if (bias || GROUPED) {
       double sum = 0.0;
+      if constexpr (KPL <= 8) {
+#pragma unroll
+        for (int i = 0; i < KPL; ++i) sum += l[i] > LOWEST ? exp((double)l[i] - (double)top) : 0.0;
+      } else {  // one after the other: unrolled, the exponentials of 16 and more take all registers
 #pragma unroll 1
-      for (int at = sub; at < mine; at += L) {
-        const float v = logit(at);
-        if (v > LOWEST) sum += exp((double)v - (double)top);
+        for (int at = sub; at < mine; at += L) {
+          const float v = logit(at);
+          if (v > LOWEST) sum += exp((double)v - (double)top);
+        }
       }
       z = sum_lanes_f64<64>(sum);
     } else if (!p.renorm) {
@@ -145,13 +150,18 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
     // the two best of each group, first in a lane, then over its lanes
     const double NONE = -__builtin_inf();
     double b1 = NONE, b2 = NONE;
+    auto take = [&](double t) {
+      b2 = fmax(b2, fmin(b1, t));
+      b1 = fmax(b1, t);
+    };
+    if constexpr (KPL <= 8) {
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) take(c[i] >= -__FLT_MAX__ ? score(l[i]) + (bias ? (double)b[i] : 0.0) : NONE);
+    } else {
 #pragma unroll 1
-    for (int at = sub; at < mine; at += L) {
-      const float v = logit(at);
-      if (v > LOWEST) {
-        const double t = score(v) + (bias ? (double)bias[e0 + at] : 0.0);
-        b2 = fmax(b2, fmin(b1, t));
-        b1 = fmax(b1, t);
+      for (int at = sub; at < mine; at += L) {
+        const float v = logit(at);
+        if (v > LOWEST) take(score(v) + (bias ? (double)bias[e0 + at] : 0.0));
       }
     }
     for (int m = L / 2; m >= 1; m >>= 1) {
@@ -163,9 +173,13 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
     const double worth = !any ? NONE : p.group_top == 2 && b2 > NONE ? b1 + b2 : b1;
     const uint64_t w = order64(worth);
     int before = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      const uint64_t o = readlane64(w, g * L);
-      before += o > w || (o == w && g < grp);
+    for (int g0 = 0; g0 < p.groups; g0 += 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int g = g0 + u;
+        const uint64_t o = readlane64(w, min(g * L, 63));
+        before += g < p.groups && (o > w || (o == w && g < grp));
+      }
     }
     if (!any || before >= p.top_groups) {
       mine = 0;

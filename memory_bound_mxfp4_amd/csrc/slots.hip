@@ -248,7 +248,9 @@ hipError_t launch_group_slots(const int32_t* idx, int tokens, int top_k, int E, 
 
 // out[t] = sum_j gate[t][j] y[t k + j] (j ascending), + residual[t].  VEC: a
 // thread takes 16 bytes of columns of one token (8 or 4 of them) and keeps
-// the loads of 8 slots in flight; else one column.
+// the loads of 8 slots in flight (16 of them halved the rate); else one column.
+// y is read once: its loads are not kept in the caches.  Bound by reading y:
+// 4096 x 16 x 7168 bf16 205 us, 5.2 TB/s; one token 4.5 us, latency.
 template <int DT, bool VEC>
 __global__ __launch_bounds__(256) void k_combine(const void* __restrict__ y, const float* __restrict__ gate, int top_k,
                                                  unsigned per_row, size_t total, int H, const float* residual,
@@ -270,7 +272,7 @@ __global__ __launch_bounds__(256) void k_combine(const void* __restrict__ y, con
     for (int u = 0; u < U; ++u) {
       const int j = min(j0 + u, top_k - 1);
       w[u] = gt[j];
-      if constexpr (VEC) c[u] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(y) + (y0 + (size_t)j * H) * Elem<DT>::bytes);
+      if constexpr (VEC) c[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const char*>(y) + (y0 + (size_t)j * H) * Elem<DT>::bytes));
       else c[u][0] = __float_as_uint(load_f32<DT>(y, y0 + (size_t)j * H));
     }
 #pragma unroll
