@@ -371,6 +371,10 @@ def residual_add_rmsnorm_bf16(h, t, eps: float = 1e-6, out=None, stream=None):
 
 
 # ---- routing, slots by expert, 8-bit products ---------------------------------------------------------------
+#
+# With `stream` (a torch stream or its address) a call runs there, and the outputs and workspaces it makes belong to
+# that stream; what it is given has to be ready there, and what it returns is used elsewhere as any tensor of another
+# stream is: behind a wait, and with record_stream if it may be freed while in use.
 
 
 class RouteParamsC(ctypes.Structure):
@@ -431,6 +435,16 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream`, from that stream's own pool: what is freed there is used again only behind the
+    call, and nothing of another stream still works on it."""
+    import torch
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _launch(what: str, device, stream, *args):
     """Calls an entry point with `device` current, on the given stream or on that device's current one."""
     import torch
@@ -464,9 +478,8 @@ def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int
         _want(bias, (E,), torch.float32, dev, "bias")
     p = _route_params(E, top_k, _SCORES[score], groups, top_groups, group_top, int(renorm), scale)
     shape = (rows, top_k)
-    idx = torch.empty(shape, dtype=torch.int32, device=dev) if idx is None else _want(idx, shape, torch.int32, dev, "idx")
-    gate = torch.empty(shape, dtype=torch.float32, device=dev) if gate is None else \
-        _want(gate, shape, torch.float32, dev, "gate")
+    idx = _empty(shape, torch.int32, dev, stream) if idx is None else _want(idx, shape, torch.int32, dev, "idx")
+    gate = _empty(shape, torch.float32, dev, stream) if gate is None else _want(gate, shape, torch.float32, dev, "gate")
     _launch("moe_route", dev, stream, _addr(logits), code, stride, rows, _addr(bias), p, _addr(idx), _addr(gate))
     return idx, gate
 
@@ -477,8 +490,8 @@ def quant_rows_i8(x, q=None, scale=None, stream=None):
     rows, k, stride = _rows(x, "x")
     dev = x.device
     code = _dtype_code(x.dtype, "x")
-    q = torch.empty((rows, k), dtype=torch.int8, device=dev) if q is None else _want(q, (rows, k), torch.int8, dev, "q")
-    scale = torch.empty((rows,), dtype=torch.float32, device=dev) if scale is None else \
+    q = _empty((rows, k), torch.int8, dev, stream) if q is None else _want(q, (rows, k), torch.int8, dev, "q")
+    scale = _empty((rows,), torch.float32, dev, stream) if scale is None else \
         _want(scale, (rows,), torch.float32, dev, "scale")
     _launch("quant_rows_i8", dev, stream, _addr(x), code, stride, rows, k, _addr(q), _addr(scale))
     return q, scale
@@ -506,19 +519,19 @@ def _i8_operands(x, x_scale, w, w_scale, swiglu: bool, lead: tuple):
     return rows, k, stride, n, _dtype_code(x.dtype, "x", int8=True)
 
 
-def _out(out, shape, out_dtype, device):
+def _out(out, shape, out_dtype, device, stream):
     import torch
     if out is None:
-        return torch.empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=device)
+        return _empty(shape, torch.bfloat16 if out_dtype is None else out_dtype, device, stream)
     if out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out is {out.dtype}, not {out_dtype}")
     return _want(out, shape, out.dtype, device, "out")
 
 
-def _workspace(ws, need: int, device):
+def _workspace(ws, need: int, device, stream):
     import torch
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        return _empty(need, torch.uint8, device, stream) if need else None
     return _want(ws, tuple(ws.shape), torch.uint8, device, "ws")
 
 
@@ -528,8 +541,8 @@ def gemm_i8(x, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dty
     type, out_dtype or bfloat16."""
     m, k, stride, n, code = _i8_operands(x, x_scale, w, w_scale, swiglu, ())
     dev = x.device
-    y = _out(out, (m, n), out_dtype, dev)
-    ws = _workspace(ws, 0 if ws is not None else load().gemm_i8_workspace_size(m, n, k, int(swiglu), code), dev)
+    y = _out(out, (m, n), out_dtype, dev, stream)
+    ws = _workspace(ws, 0 if ws is not None else load().gemm_i8_workspace_size(m, n, k, int(swiglu), code), dev, stream)
     _launch("gemm_i8", dev, stream, _addr(x), code, stride, _addr(x_scale), m, k, _addr(w), _addr(w_scale), n, int(swiglu),
             _addr(y), _dtype_code(y.dtype, "out"), _addr(ws), 0 if ws is None else ws.numel())
     return y
@@ -547,12 +560,12 @@ class SlotGroups:
     offsets: object
 
 
-def alloc_slot_groups(tokens: int, top_k: int, num_experts: int, device=None) -> SlotGroups:
+def alloc_slot_groups(tokens: int, top_k: int, num_experts: int, device=None, stream=None) -> SlotGroups:
     import torch
     size = int(load().moe_slot_groups_size(tokens, top_k, num_experts))
     if not size:
         raise ValueError(f"slot groups of {tokens} tokens, {top_k} slots each and {num_experts} experts are out of range")
-    buf = torch.empty(size, dtype=torch.uint8, device="cuda" if device is None else device)
+    buf = _empty(size, torch.uint8, torch.device("cuda" if device is None else device), stream)
     slots = tokens * top_k
     at = (4 * slots + 255) // 256 * 256
     return SlotGroups(tokens, top_k, num_experts, buf, buf[:4 * slots].view(torch.int32),
@@ -567,7 +580,7 @@ def moe_group_slots(idx, num_experts: int, groups: Optional[SlotGroups] = None, 
     tokens, top_k = idx.shape
     _want(idx, (tokens, top_k), torch.int32, idx.device, "idx")
     if groups is None:
-        groups = alloc_slot_groups(tokens, top_k, num_experts, idx.device)
+        groups = alloc_slot_groups(tokens, top_k, num_experts, idx.device, stream)
     elif (groups.tokens, groups.top_k, groups.num_experts) != (tokens, top_k, num_experts) or \
             groups.buffer.device != idx.device:
         raise ValueError("groups were allocated for another shape or device")
@@ -592,10 +605,10 @@ def experts_gemm_i8(x, groups: SlotGroups, w, w_scale, x_scale=None, swiglu: boo
         raise ValueError(f"x has {rows} rows, neither the tokens nor the slots of the groups")
     if groups.buffer.device != dev:
         raise ValueError("groups are on another device")
-    y = _out(out, (groups.tokens * groups.top_k, n), out_dtype, dev)
+    y = _out(out, (groups.tokens * groups.top_k, n), out_dtype, dev, stream)
     need = 0 if ws is not None else load().experts_gemm_i8_workspace_size(groups.tokens, groups.top_k, E, rows, n, k,
                                                                           int(swiglu), code)
-    ws = _workspace(ws, need, dev)
+    ws = _workspace(ws, need, dev, stream)
     _launch("experts_gemm_i8", dev, stream, _addr(x), code, stride, _addr(x_scale), rows, k, _addr(groups.buffer),
             groups.buffer.numel(), groups.tokens, groups.top_k, E, _addr(w), _addr(w_scale), n, int(swiglu), _addr(y),
             _dtype_code(y.dtype, "out"), _addr(ws), 0 if ws is None else ws.numel())
@@ -614,7 +627,7 @@ def moe_combine(y, gate, residual=None, out=None, stream=None):
     shape = (tokens, hidden)
     if residual is not None:
         _want(residual, shape, torch.float32, dev, "residual")
-    out = torch.empty(shape, dtype=torch.float32, device=dev) if out is None else _want(out, shape, torch.float32, dev, "out")
+    out = _empty(shape, torch.float32, dev, stream) if out is None else _want(out, shape, torch.float32, dev, "out")
     _launch("moe_combine", dev, stream, _addr(y), _dtype_code(y.dtype, "y"), _addr(gate), tokens, top_k, hidden,
             _addr(residual), _addr(out))
     return out

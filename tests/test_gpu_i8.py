@@ -492,3 +492,38 @@ def test_gemm_of_one_row_extremes():
 def test_experts_of_one_token(idx, swiglu):
     """One token: distinct experts, one that comes twice, none, more slots than a tile."""
     _experts_case(1, len(idx), 6, 50, 272, swiglu, False, "bf16", "f32", idx=np.array([idx], np.int32))
+
+
+def test_memory_of_a_call_on_another_stream():
+    """A call given a stream makes its outputs and workspace there: what the current stream allocates and writes while
+    that stream still works never lands in them."""
+    import torch
+    m, n, k, top_k, E = 48, 512, 1024, 2, 4
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(m, k, generator=g).cuda()
+    w = torch.randint(-127, 128, (E, n, k), generator=g, dtype=torch.int8).cuda()
+    s = torch.rand(E, n, generator=g).cuda()
+    logits = torch.randn(m, E, generator=g).cuda()
+
+    def run(stream):
+        idx, gate = moe.moe_route(logits, top_k, stream=stream)
+        groups = moe.moe_group_slots(idx, E, stream=stream)
+        q, qs = moe.quant_rows_i8(x, stream=stream)
+        y = moe.experts_gemm_i8(x, groups, w, s, stream=stream)
+        return (idx, gate, groups.order, groups.offsets, q, qs, moe.gemm_i8(x, w[0], s[0], stream=stream), y,
+                moe.moe_combine(y, gate, stream=stream))
+
+    want = [t.clone() for t in run(None)]
+    need = moe.gemm_i8_workspace_size(m, n, k, False, torch.float32)
+    torch.cuda.synchronize()
+    for as_int in (False, True):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # the calls below wait behind this
+        got = run(side.cuda_stream if as_int else side)
+        trash = [torch.full((size,), 0x55, dtype=torch.uint8, device="cuda")
+                 for size in (need, m * k, 4 * m, 1 << 16, 1 << 12) for _ in range(4)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+        assert all(bool((t == 0x55).all()) for t in trash)
