@@ -354,8 +354,8 @@ moe_status residual_add_rmsnorm_bf16(float* h, const uint16_t* t, int batch, int
  * formula also where their fp32 scores would tie; gates are rounded once.
  * 1 <= rows <= MOE_MAX_ROWS, 1 <= top_k <= min(64, top_groups * num_experts / groups),
  * num_experts <= 4096 and a multiple of groups, 1 <= top_groups <= groups <=
- * 64, group_top 1 or 2; groups == 1 needs top_groups == 1.  bias 4-byte
- * aligned, logits aligned to their element.
+ * 64, group_top 1 or 2; groups == 1 needs top_groups == 1; scale finite.  bias
+ * 4-byte aligned, logits aligned to their element.
  */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
@@ -379,7 +379,7 @@ moe_status moe_route(const void* logits, moe_dtype dtype, size_t row_stride, int
  *   q[m][k]  = the integer nearest to x[m][k] / scale[m] (the exact quotient,
  *              ties to even), within +-127
  *   x        [rows][k] bf16, fp16 or fp32, row m at x + m * x_stride elements
- *   q        out int8 [rows][k]; scale out fp32 [rows]
+ *   q        out int8 [rows][k]; scale out fp32 [rows]; neither overlaps x
  * A row of zeros (or so small that its scale rounds to 0) has scale 0 and
  * codes 0.  A row that holds a NaN or an infinity has scale NaN and codes 0,
  * so every product of it is NaN.  1 <= rows <= MOE_MAX_ROWS, 1 <= k <= 65536.
@@ -396,13 +396,15 @@ moe_status quant_rows_i8(const void* x, moe_dtype dtype, size_t x_stride, int ro
  *   w         int8 [n][k] codes, w_scale fp32 [n]
  *   swiglu    0, or 1: w is [2][n][k], gate then up, w_scale [2][n], and
  *             y[m][i] = silu(g) * u of the two products g and u
- *   y         out [m][n], bf16, fp16 or fp32 (y_dtype); must not alias x
+ *   y         out [m][n], bf16, fp16 or fp32 (y_dtype); must not overlap x
  *   ws        workspace of >= gemm_i8_workspace_size(...) bytes, 256-byte
  *             aligned (may be NULL where that is 0).  It needs no
  *             initialisation and holds nothing between calls.
  * The sum is exact; it is rounded to fp32, multiplied by the two scales and
  * rounded to y_dtype; SwiGLU runs in fp32 on the scaled sums.
- * 1 <= m <= MOE_MAX_ROWS, 1 <= n <= 2^20, k a multiple of 16 in 16 .. 65536; 16-byte aligned x
+ * 1 <= m <= MOE_MAX_ROWS, 1 <= n <= 2^20, k a multiple of 16 in 16 .. 65536;
+ * MOE_ERR_UNSUPPORTED also where its tiles make 2^22 workgroups or more (an
+ * output of some 10^11 elements, fewer with few rows an expert).  16-byte aligned x
  * (x_stride a multiple of 16) if it is int8, else aligned to its element; w
  * and y 16-byte aligned.
  */
@@ -458,9 +460,11 @@ moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
  *   y         [tokens * top_k][hidden], bf16, fp16 or fp32 (`dtype`)
  *   gate      fp32 [tokens][top_k]
  *   residual  fp32 [tokens][hidden], or NULL for zeros; may be out itself
- *   out       fp32 [tokens][hidden]
+ *   out       fp32 [tokens][hidden]; overlaps neither y nor, otherwise,
+ *             residual
  * Summed in fp32, j ascending, then the residual.  1 <= tokens <=
- * MOE_MAX_ROWS, 1 <= top_k <= 64, 1 <= hidden <= 2^20.  Pointers aligned to their element.
+ * MOE_MAX_ROWS, 1 <= top_k <= 64, 1 <= hidden <= 2^20.  Pointers aligned to
+ * their element.
  */
 moe_status moe_combine(const void* y, moe_dtype dtype, const float* gate, int tokens, int top_k, int hidden,
                        const float* residual, float* out, void* stream);

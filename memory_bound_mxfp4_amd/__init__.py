@@ -418,11 +418,20 @@ def _want(t, shape: tuple, dtype, device, what: str):
     return t
 
 
+def _int(v: int, what: str) -> int:
+    """Sizes go to the C interface as 32-bit integers, and a longer one would lose its upper bits on the way."""
+    if not -0x80000000 <= v <= 0x7FFFFFFF:
+        raise ValueError(f"{what} is out of range: {v}")
+    return v
+
+
 def _rows(t, what: str):
     """Checks a matrix whose rows may lie apart; returns rows, columns and the row stride."""
     if t.dim() != 2:
         raise ValueError(f"{what} must be a matrix")
     rows, cols = t.shape
+    _int(rows, f"the rows of {what}")
+    _int(cols, f"the columns of {what}")
     if t.is_contiguous():
         return rows, cols, cols
     stride = t.stride(0) if rows > 1 else cols
@@ -476,7 +485,9 @@ def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int
     code = _dtype_code(logits.dtype, "logits")
     if bias is not None:
         _want(bias, (E,), torch.float32, dev, "bias")
-    p = _route_params(E, top_k, _SCORES[score], groups, top_groups, group_top, int(renorm), scale)
+    for v, what in ((top_k, "top_k"), (groups, "groups"), (top_groups, "top_groups"), (group_top, "group_top")):
+        _int(v, what)
+    p = _route_params(E, top_k, _SCORES[score], groups, top_groups, group_top, int(bool(renorm)), scale)
     shape = (rows, top_k)
     idx = _empty(shape, torch.int32, dev, stream) if idx is None else _want(idx, shape, torch.int32, dev, "idx")
     gate = _empty(shape, torch.float32, dev, stream) if gate is None else _want(gate, shape, torch.float32, dev, "gate")
@@ -498,7 +509,9 @@ def quant_rows_i8(x, q=None, scale=None, stream=None):
 
 
 def gemm_i8_workspace_size(m: int, n: int, k: int, swiglu: bool, x_dtype) -> int:
-    return int(load().gemm_i8_workspace_size(m, n, k, int(swiglu), _dtype_code(x_dtype, "x", int8=True)))
+    for v, what in ((m, "m"), (n, "n"), (k, "k")):
+        _int(v, what)
+    return int(load().gemm_i8_workspace_size(m, n, k, int(bool(swiglu)), _dtype_code(x_dtype, "x", int8=True)))
 
 
 def _i8_operands(x, x_scale, w, w_scale, swiglu: bool, lead: tuple):
@@ -509,7 +522,7 @@ def _i8_operands(x, x_scale, w, w_scale, swiglu: bool, lead: tuple):
     parts = (2,) if swiglu else ()
     if w.dim() != len(lead) + len(parts) + 2:
         raise ValueError(f"w has {w.dim()} dimensions, not {len(lead) + len(parts) + 2}")
-    n = w.shape[-2]
+    n = _int(w.shape[-2], "the rows of w")
     _want(w, lead + parts + (n, k), torch.int8, dev, "w")
     _want(w_scale, lead + parts + (n,), torch.float32, dev, "w_scale")
     if (x_scale is not None) != (x.dtype == torch.int8):
@@ -538,12 +551,12 @@ def _workspace(ws, need: int, device, stream):
 def gemm_i8(x, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dtype=None, ws=None, stream=None):
     """y = x w^T in 8-bit integers (gemm_i8): x [m][k] float rows, quantised on the way, or int8 codes with
     x_scale [m]; w int8 [n][k] with w_scale [n], or [2][n][k] and [2][n] with swiglu. Returns y [m][n] in out's
-    type, out_dtype or bfloat16."""
+    type, out_dtype or bfloat16; out must not overlap x."""
     m, k, stride, n, code = _i8_operands(x, x_scale, w, w_scale, swiglu, ())
     dev = x.device
     y = _out(out, (m, n), out_dtype, dev, stream)
-    ws = _workspace(ws, 0 if ws is not None else load().gemm_i8_workspace_size(m, n, k, int(swiglu), code), dev, stream)
-    _launch("gemm_i8", dev, stream, _addr(x), code, stride, _addr(x_scale), m, k, _addr(w), _addr(w_scale), n, int(swiglu),
+    ws = _workspace(ws, 0 if ws is not None else load().gemm_i8_workspace_size(m, n, k, int(bool(swiglu)), code), dev, stream)
+    _launch("gemm_i8", dev, stream, _addr(x), code, stride, _addr(x_scale), m, k, _addr(w), _addr(w_scale), n, int(bool(swiglu)),
             _addr(y), _dtype_code(y.dtype, "out"), _addr(ws), 0 if ws is None else ws.numel())
     return y
 
@@ -562,6 +575,8 @@ class SlotGroups:
 
 def alloc_slot_groups(tokens: int, top_k: int, num_experts: int, device=None, stream=None) -> SlotGroups:
     import torch
+    for v, what in ((tokens, "tokens"), (top_k, "top_k"), (num_experts, "num_experts")):
+        _int(v, what)
     size = int(load().moe_slot_groups_size(tokens, top_k, num_experts))
     if not size:
         raise ValueError(f"slot groups of {tokens} tokens, {top_k} slots each and {num_experts} experts are out of range")
@@ -590,8 +605,10 @@ def moe_group_slots(idx, num_experts: int, groups: Optional[SlotGroups] = None, 
 
 
 def experts_gemm_i8_workspace_size(groups: SlotGroups, x_rows: int, n: int, k: int, swiglu: bool, x_dtype) -> int:
+    for v, what in ((x_rows, "x_rows"), (n, "n"), (k, "k")):
+        _int(v, what)
     return int(load().experts_gemm_i8_workspace_size(groups.tokens, groups.top_k, groups.num_experts, x_rows, n, k,
-                                                     int(swiglu), _dtype_code(x_dtype, "x", int8=True)))
+                                                     int(bool(swiglu)), _dtype_code(x_dtype, "x", int8=True)))
 
 
 def experts_gemm_i8(x, groups: SlotGroups, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dtype=None,
@@ -607,10 +624,10 @@ def experts_gemm_i8(x, groups: SlotGroups, w, w_scale, x_scale=None, swiglu: boo
         raise ValueError("groups are on another device")
     y = _out(out, (groups.tokens * groups.top_k, n), out_dtype, dev, stream)
     need = 0 if ws is not None else load().experts_gemm_i8_workspace_size(groups.tokens, groups.top_k, E, rows, n, k,
-                                                                          int(swiglu), code)
+                                                                          int(bool(swiglu)), code)
     ws = _workspace(ws, need, dev, stream)
     _launch("experts_gemm_i8", dev, stream, _addr(x), code, stride, _addr(x_scale), rows, k, _addr(groups.buffer),
-            groups.buffer.numel(), groups.tokens, groups.top_k, E, _addr(w), _addr(w_scale), n, int(swiglu), _addr(y),
+            groups.buffer.numel(), groups.tokens, groups.top_k, E, _addr(w), _addr(w_scale), n, int(bool(swiglu)), _addr(y),
             _dtype_code(y.dtype, "out"), _addr(ws), 0 if ws is None else ws.numel())
     return y
 
@@ -619,8 +636,8 @@ def moe_combine(y, gate, residual=None, out=None, stream=None):
     """out[t] = residual[t] + sum_j gate[t][j] * y[t * k + j] (moe_combine), fp32 [tokens][hidden]; out may be
     residual itself. Returns out."""
     import torch
-    tokens, top_k = gate.shape
-    hidden = y.shape[-1]
+    tokens, top_k, _ = _rows(gate, "gate")
+    hidden = _int(y.shape[-1], "hidden")
     dev = y.device
     _want(gate, (tokens, top_k), torch.float32, dev, "gate")
     _want(y, (tokens * top_k, hidden), y.dtype, dev, "y")

@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cfloat>
+#include <cmath>
 #include <mutex>
 
 #include "internal.h"
@@ -379,6 +381,10 @@ static bool float_dtype(moe_dtype t) { return t == MOE_DTYPE_BF16 || t == MOE_DT
 static size_t dtype_bytes(moe_dtype t) { return t == MOE_DTYPE_F32 ? 4 : t == MOE_DTYPE_I8 ? 1 : 2; }
 static constexpr int kMaxI8K = 65536;  // 127 * 128 * k stays inside int32
 static constexpr int kMaxCols = 1 << 20;
+static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + b_bytes && q < p + a_bytes;
+}
 
 moe_status moe_route(const void* logits, moe_dtype dtype, size_t row_stride, int rows, const float* bias,
                      const moe_route_params* params, int32_t* topk_idx, float* topk_gate, void* stream) {
@@ -386,7 +392,7 @@ moe_status moe_route(const void* logits, moe_dtype dtype, size_t row_stride, int
   const moe_route_params p = *params;
   if (p.num_experts < 1 || p.top_k < 1 || p.groups < 1 || p.top_groups < 1 || p.top_groups > p.groups ||
       p.num_experts % p.groups || (p.group_top != 1 && p.group_top != 2) || (p.renorm != 0 && p.renorm != 1) ||
-      (p.score != MOE_SCORE_SOFTMAX && p.score != MOE_SCORE_SIGMOID))
+      (p.score != MOE_SCORE_SOFTMAX && p.score != MOE_SCORE_SIGMOID) || !(std::fabs(p.scale) <= FLT_MAX))
     return MOE_ERR_INVALID_ARGUMENT;
   if (p.top_k > p.top_groups * (p.num_experts / p.groups) || p.top_k > MOE_MAX_TOPK ||
       row_stride < (size_t)p.num_experts)
@@ -406,6 +412,9 @@ moe_status quant_rows_i8(const void* x, moe_dtype dtype, size_t x_stride, int ro
     return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(x, dtype_bytes(dtype)) || !aligned(scale, 4)) return MOE_ERR_INVALID_ARGUMENT;
   if (k > kMaxI8K || rows > MOE_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+  const size_t x_bytes = ((size_t)(rows - 1) * x_stride + k) * dtype_bytes(dtype);
+  if (overlap(x, x_bytes, q, (size_t)rows * k) || overlap(x, x_bytes, scale, 4 * (size_t)rows))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (launch_quant_rows(x, dtype, x_stride, rows, k, q, scale, static_cast<hipStream_t>(stream)) != hipSuccess)
     return MOE_ERR_HIP;
   return MOE_OK;
@@ -427,7 +436,8 @@ static QuantWs quant_ws(void* ws, int rows, int k) {
 }
 
 static moe_status check_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int x_rows, int k,
-                           const int8_t* w, const float* w_scale, int n, int swiglu, const void* y, moe_dtype y_dtype) {
+                           const int8_t* w, const float* w_scale, int n, int swiglu, const void* y, moe_dtype y_dtype,
+                           size_t y_rows) {
   if (!x || !w || !w_scale || !y || x_rows < 1 || n < 1 || k < 16 || k % 16 || (swiglu != 0 && swiglu != 1))
     return MOE_ERR_INVALID_ARGUMENT;
   if (!float_dtype(y_dtype) || !(float_dtype(x_dtype) || x_dtype == MOE_DTYPE_I8)) return MOE_ERR_INVALID_ARGUMENT;
@@ -436,6 +446,8 @@ static moe_status check_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
     return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(w, 16) || !aligned(y, 16) || !aligned(w_scale, 4) || !aligned(x_scale, 4)) return MOE_ERR_INVALID_ARGUMENT;
   if (k > kMaxI8K || n > kMaxCols || x_rows > MOE_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+  if (overlap(x, ((size_t)(x_rows - 1) * x_stride + k) * dtype_bytes(x_dtype), y, y_rows * n * dtype_bytes(y_dtype)))
+    return MOE_ERR_INVALID_ARGUMENT;
   return MOE_OK;
 }
 
@@ -476,7 +488,7 @@ size_t gemm_i8_workspace_size(int m, int n, int k, int swiglu, moe_dtype x_dtype
 moe_status gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int m, int k,
                    const int8_t* w, const float* w_scale, int n, int swiglu, void* y, moe_dtype y_dtype, void* ws,
                    size_t ws_bytes, void* stream) {
-  moe_status st = check_i8(x, x_dtype, x_stride, x_scale, m, k, w, w_scale, n, swiglu, y, y_dtype);
+  moe_status st = check_i8(x, x_dtype, x_stride, x_scale, m, k, w, w_scale, n, swiglu, y, y_dtype, m);
   if (st != MOE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const I8Plan plan = i8_plan(m, 1, false, n, k, swiglu != 0);
@@ -532,9 +544,10 @@ moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
                            const void* groups, size_t groups_bytes, int tokens, int top_k, int num_experts,
                            const int8_t* w, const float* w_scale, int n, int swiglu, void* y, moe_dtype y_dtype,
                            void* ws, size_t ws_bytes, void* stream) {
-  moe_status st = check_i8(x, x_dtype, x_stride, x_scale, x_rows, k, w, w_scale, n, swiglu, y, y_dtype);
-  if (st != MOE_OK) return st;
   if (!groups || !aligned(groups, 256) || !slots_ok(tokens, top_k, num_experts)) return MOE_ERR_INVALID_ARGUMENT;
+  moe_status st = check_i8(x, x_dtype, x_stride, x_scale, x_rows, k, w, w_scale, n, swiglu, y, y_dtype,
+                           (size_t)tokens * top_k);
+  if (st != MOE_OK) return st;
   const size_t slots = (size_t)tokens * top_k;
   if (x_rows != tokens && (size_t)x_rows != slots) return MOE_ERR_INVALID_ARGUMENT;
   const GroupsLayout g = groups_layout(tokens, top_k, num_experts);
@@ -577,6 +590,10 @@ moe_status moe_combine(const void* y, moe_dtype dtype, const float* gate, int to
   if (!aligned(y, dtype_bytes(dtype)) || !aligned(gate, 4) || !aligned(residual, 4) || !aligned(out, 4))
     return MOE_ERR_INVALID_ARGUMENT;
   if (tokens > MOE_MAX_ROWS || hidden > kMaxCols) return MOE_ERR_UNSUPPORTED;
+  const size_t bytes = (size_t)tokens * hidden * 4;
+  if (overlap(y, (size_t)tokens * top_k * hidden * dtype_bytes(dtype), out, bytes) ||
+      (residual && residual != out && overlap(residual, bytes, out, bytes)))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (launch_combine(y, dtype, gate, tokens, top_k, hidden, residual, out, static_cast<hipStream_t>(stream)) !=
       hipSuccess)
     return MOE_ERR_HIP;

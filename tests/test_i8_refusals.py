@@ -169,3 +169,52 @@ def test_binding_checks():
         moe.experts_gemm_i8(x, groups, wide[:7], scales[:7])
     with pytest.raises(ValueError):
         moe.moe_group_slots(torch.zeros(4, 2, dtype=torch.int32), 9, groups=groups)
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_route_scale(scale):
+    """An infinite scale would turn the gate 0 of a padded place into NaN."""
+    assert _route(scale=scale) == INVALID
+
+
+def test_outputs_over_inputs():
+    """A product's workgroups read x while others write y; a sum's threads read y and the residual in the same way."""
+    lib = moe.load()
+    assert _gemm(y=P(0x1000)) == INVALID                                    # y is x
+    assert _gemm(y=P(0x11F0)) == INVALID                                    # the last 16 of 512 bytes of x
+    assert _gemm(x=P(0x40F0)) == INVALID                                    # x in the last 16 of 256 bytes of y
+    assert _experts(y=P(0x11F0)) == INVALID
+    assert _experts(x=P(0x41F0)) == INVALID                                 # 8 slots of 64 bytes
+    q = lib.quant_rows_i8
+    x, s = P(0x1000), P(0x9000)
+    assert q(x, F32, 64, 4, 64, P(0x13FF), s, None) == INVALID              # 1024 bytes of x
+    assert q(x, F32, 64, 4, 64, P(0x0F01), s, None) == INVALID
+    assert q(x, F32, 64, 4, 64, P(0x8000), P(0x13FC), None) == INVALID
+    c, y, g = lib.moe_combine, P(0x10000), P(0x2000)
+    assert c(y, F32, g, 2, 2, 64, None, P(0x103FC), None) == INVALID        # 1024 bytes of y, 512 of out
+    assert c(y, F32, g, 2, 2, 64, None, P(0x0FE04), None) == INVALID
+    assert c(y, F32, g, 2, 2, 64, P(0x20000), P(0x20004), None) == INVALID  # residual, but not out itself
+
+
+def test_sizes_past_32_bits():
+    """Sizes whose low 32 bits would pass are turned down by the binding."""
+    import torch
+    big = (1 << 32) + 4
+    base = torch.zeros(1, dtype=torch.bfloat16)
+    rows = base.expand(big, 1)
+    w, s = torch.zeros(32, 16, dtype=torch.int8), torch.zeros(32)
+    for call in (
+            lambda: moe.quant_rows_i8(rows),
+            lambda: moe.quant_rows_i8(rows.t()),
+            lambda: moe.moe_route(rows, 1),
+            lambda: moe.gemm_i8(torch.zeros(4, 16), w[:1, :1].expand(big, 16), s),
+            lambda: moe.moe_route(torch.zeros(4, 16), 1 << 32 | 1),
+            lambda: moe.moe_route(torch.zeros(4, 16), 1, groups=(1 << 32) + 1),
+            lambda: moe.alloc_slot_groups(big, 1, 8, device="cpu"),
+            lambda: moe.gemm_i8_workspace_size(big, 32, 64, False, torch.bfloat16),
+            lambda: moe.experts_gemm_i8_workspace_size(moe.SlotGroups(4, 2, 8, None, None, None), 4, big, 64, False,
+                                                       torch.bfloat16),
+            lambda: moe.moe_combine(torch.zeros(1, 1).expand(2, big), torch.zeros(1, 2)),
+    ):
+        with pytest.raises(ValueError):
+            call()
