@@ -2,6 +2,8 @@
 // for one matrix or for the rows of each expert, with SwiGLU on pairs of
 // matrices.  Sums are int32 and exact, so neither the split of K nor its
 // order changes a result.
+#include <type_traits>
+
 #include "i8_common.h"
 
 namespace moe {
@@ -380,98 +382,104 @@ struct TileCfg {
   static constexpr int NW = WGM * WGN, T = 64 * NW, MF = BM / WGM / 16, NF = BN / WGN / 16;  // fragments of a wave
   static constexpr bool SPLIT = BM == 64 && BN == 64;  // K may be split over workgroups
   static constexpr int STAGE = (BM + BN) * KS, RING = ST * STAGE;
-  // Rows of outputs on their way through LDS: C columns of B bytes and 16
-  // more, which spreads the rows of a fragment over the banks.
-  static constexpr int row_bytes(int C, int B) { return (C + 16) * B; }
-  static constexpr int OUT16 = BM * row_bytes(BN / P, 2);
-  static constexpr int LDS = RING > OUT16 ? RING : OUT16;
-  // fragment rows of a wave that fit at once
-  static constexpr int fit(int C, int B, int n) { return WGM * n * 16 * row_bytes(C, B) <= LDS ? n : fit(C, B, n / 2); }
 };
 
-// A tile's results on their way out.  In the registers a lane holds 4 columns
-// of 16 rows apart, and storing those would touch 16 cache lines of 32 bytes
-// each an instruction (it took 13 us of a 256 x 256 tile's call); through LDS a
-// wave stores whole lines.  make(i, j, v): the 4 values (OB bytes each, packed)
-// of fragment i, j; put(m, c, chunk): stores 16 bytes of row m from column c.
-template <class C, int COLS, int STEP, int OB, class Make, class Put>
-__device__ __forceinline__ void tile_out(int8_t* lds, int wm, int wn, int rows, Make make, Put put) {
-  constexpr int MI = C::fit(COLS, OB, C::MF), RB = C::row_bytes(COLS, OB), CPR = COLS * OB / 16;
-  static_assert(MI > 0, "a fragment row does not fit");
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+// Exchanges between the 16-lane groups of a wave so that of two neighbouring fragments
+// (x: columns 4 q .. of the first, y: of the second) lane 16 q + r gets 8 columns from
+// 8 q: a store then writes 64 bytes of a row.
+__device__ __forceinline__ u32x4 join_fragments(const u32x2& x, const u32x2& y) {
+  u32x4 o;
 #pragma unroll
-  for (int h = 0; h < C::MF; h += MI) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < C::NF; j += STEP) {
-        int8_t* at = lds + ((wm * MI + i) * 16 + r) * RB + ((wn * C::NF + j) / STEP * 16 + 4 * q) * OB;
-        if constexpr (OB == 2) *reinterpret_cast<u32x2*>(at) = make(h + i, j);
-        else *reinterpret_cast<u32x4*>(at) = make(h + i, j);
-      }
-    __syncthreads();
-    for (int c = threadIdx.x; c < C::WGM * MI * 16 * CPR; c += C::T) {
-      const int row = c / CPR, col = c - row * CPR, m = row / (MI * 16) * (C::BM / C::WGM) + h * 16 + row % (MI * 16);
-      if (m < rows) put(m, col * (16 / OB), *reinterpret_cast<const u32x4*>(lds + row * RB + col * 16));
-    }
+  for (int k = 0; k < 2; ++k) {
+    const auto h = __builtin_amdgcn_permlane32_swap(x[k], y[k], false, false);
+    const auto f = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+    o[k] = f[0];
+    o[2 + k] = f[1];
   }
+  return o;
 }
 
 // Scales a wave's sums and stores them.  Register c of acc[i][j] of lane
 // 16 q + r: matrix row 16 j + 4 q + c, row 16 i + r of x.
 template <int DT, class C>
-__device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, int8_t* lds, int i0, int wm, int wn,
+__device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, const int8_t* lds, int i0, int wm, int wn,
                                            const i32x4 (&acc)[C::MF][C::NF]) {
-  constexpr int P = C::P, OB = Elem<DT>::bytes;
+  constexpr int P = C::P, OB = Elem<DT>::bytes, V = 16 / OB;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const float* sw = reinterpret_cast<const float*>(lds + C::LDS);
+  const float* sw = reinterpret_cast<const float*>(lds + C::RING);
   const float* sx = sw + C::BN;
   const int* yr = reinterpret_cast<const int*>(sx + C::BM);
-  auto make = [&](int i, int j) {
-    const float s = sx[wm * (C::BM / C::WGM) + 16 * i + r];
-    f32x4 v;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const f32x4 w = *reinterpret_cast<const f32x4*>(sw + (wn * C::NF + j + p) * 16 + 4 * q);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float u = (float)acc[i][j + p][c] * (s * w[c]);
-        v[c] = p ? swiglu_f(v[c], u) : u;
-      }
-    }
-    if constexpr (OB == 4) return __builtin_bit_cast(u32x4, v);
-    else return u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-  };
-  constexpr int V = 16 / OB;
   const bool whole = a.n % V == 0;  // 16-byte stores stay aligned, and a chunk is inside the row or outside
-  auto put = [&](int m, int c, const u32x4& d) {
-    const size_t at = (size_t)yr[m] * a.n + i0 + c;
-    if (whole) {
-      if (i0 + c < a.n) *reinterpret_cast<u32x4*>(static_cast<char*>(a.y) + at * OB) = d;
+  const int c0 = i0 + wn * (C::BN / C::WGN / P);
+#pragma unroll
+  for (int i = 0; i < C::MF; ++i) {
+    const int m = 16 * (C::WGM * i + wm) + r;
+    if (16 * (C::WGM * i + wm) >= t.rows) break;
+    const float s = sx[m];
+    const size_t row = (size_t)yr[m] * a.n;
+    auto values = [&](int j) {  // of output fragment j
+      f32x4 v;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const f32x4 w = *reinterpret_cast<const f32x4*>(sw + (wn * C::NF + j * P + p) * 16 + 4 * q);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float u = (float)acc[i][j * P + p][c] * (s * w[c]);
+          v[c] = p ? swiglu_f(v[c], u) : u;
+        }
+      }
+      return v;
+    };
+    auto put = [&](int c, const u32x4& d) {
+      if (m >= t.rows) return;
+      if (whole) {
+        if (c < a.n) *reinterpret_cast<u32x4*>(static_cast<char*>(a.y) + (row + c) * OB) = d;
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (c + k < a.n) {
+            if constexpr (OB == 4) static_cast<uint32_t*>(a.y)[row + c + k] = d[k];
+            else static_cast<uint16_t*>(a.y)[row + c + k] = (uint16_t)(d[k / 2] >> (k % 2 * 16));
+          }
+      }
+    };
+    if constexpr (OB == 4) {
+#pragma unroll
+      for (int j = 0; j < C::NF / P; ++j) put(c0 + 16 * j + 4 * q, __builtin_bit_cast(u32x4, values(j)));
     } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k)
-        if (i0 + c + k < a.n) {
-          if constexpr (OB == 4) static_cast<uint32_t*>(a.y)[at + k] = d[k];
-          else static_cast<uint16_t*>(a.y)[at + k] = (uint16_t)(d[k / 2] >> (k % 2 * 16));
+      for (int j = 0; j < C::NF / P; j += 2) {
+        if constexpr (C::NF / P > 1) {
+          const f32x4 v = values(j), w = values(j + 1);
+          put(c0 + 16 * j + 8 * q, join_fragments(u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])},
+                                                  u32x2{pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3])}));
+        } else {  // one fragment only: 8 bytes a lane
+          const f32x4 v = values(j);
+          if (m >= t.rows) continue;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c0 + 4 * q + k < a.n) store_y(a.y, DT, row + c0 + 4 * q + k, v[k]);
         }
+      }
     }
-  };
-  tile_out<C, C::BN / P, P, OB>(lds, wm, wn, t.rows, make, put);
+  }
 }
 
 // With K split over workgroups: the sums of one part, by position, in rows of
 // all tiles' columns (the matrices interleaved as in the tile).
 template <class C>
-__device__ __forceinline__ void tile_store_part(const I8Args& a, const Tile& t, int8_t* lds, int tn, int tiles_n,
-                                                int wm, int wn, int part, const i32x4 (&acc)[C::MF][C::NF]) {
-  int* dst = a.parts + ((size_t)part * a.rows + t.p0) * ((size_t)tiles_n * C::BN) + tn * C::BN;
-  tile_out<C, C::BN, 1, 4>(
-      lds, wm, wn, t.rows, [&](int i, int j) { return __builtin_bit_cast(u32x4, acc[i][j]); },
-      [&](int m, int c, const u32x4& d) {
-        *reinterpret_cast<u32x4*>(dst + (size_t)m * ((size_t)tiles_n * C::BN) + c) = d;
-      });
+__device__ __forceinline__ void tile_store_part(const I8Args& a, const Tile& t, int tn, int tiles_n, int wm, int wn,
+                                                int part, const i32x4 (&acc)[C::MF][C::NF]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const size_t width = (size_t)tiles_n * C::BN;
+  int* dst = a.parts + ((size_t)part * a.rows + t.p0) * width + tn * C::BN + wn * C::NF * 16 + 4 * q;
+#pragma unroll
+  for (int i = 0; i < C::MF; ++i) {
+    const int m = 16 * (C::WGM * i + wm) + r;
+    if (m >= t.rows) continue;
+#pragma unroll
+    for (int j = 0; j < C::NF; ++j) *reinterpret_cast<i32x4*>(dst + m * width + 16 * j) = acc[i][j];
+  }
 }
 
 // Workgroup -> tile.  Workgroups go to the 8 XCDs in turn; each XCD gets one
@@ -485,9 +493,9 @@ template <class C>
 __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int tiles_m, int parts, int band_rows) {
   constexpr int BM = C::BM, BN = C::BN, WGM = C::WGM, WGN = C::WGN, P = C::P, ST = C::ST, NW = C::NW, MF = C::MF,
                 NF = C::NF, GX = BM / 8, L = (BM + BN) / 8 / NW;  // L: loads of a wave and stage
-  static_assert(L * 8 * NW == BM + BN && NF % P == 0 && (ST == 2 || ST == 4), "tile");
-  // the ring (outputs later), then the tile's matrix scales, row scales and output rows
-  __shared__ __attribute__((aligned(1024))) int8_t lds[C::LDS + 4 * (BN + 2 * BM)];
+  static_assert(L * 8 * NW == BM + BN && NF % P == 0 && (ST == 2 || ST == 4) && GX == NW * MF, "tile");
+  // the ring, then the tile's matrix scales, row scales and output rows
+  __shared__ __attribute__((aligned(1024))) int8_t lds[C::RING + 4 * (BN + 2 * BM)];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wv % WGM, wn = wv / WGM;
   // a grouped product's grid is sized for the most tiles its slots can make: the
@@ -510,7 +518,7 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
         store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + m) * a.n + n, 0.0f);
     return;
   }
-  float* scales = reinterpret_cast<float*>(lds + C::LDS);
+  float* scales = reinterpret_cast<float*>(lds + C::RING);
   int* yr = reinterpret_cast<int*>(scales + BN + BM);
   for (int i = threadIdx.x; i < BM; i += C::T) yr[i] = y_row(a, t.p0 + min(i, t.rows - 1));
   __syncthreads();
@@ -532,120 +540,131 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
   }
   const int stages = (K + KS - 1) / KS;
   const int s0 = (int)((size_t)stages * part / parts), S = (int)((size_t)stages * (part + 1) / parts);
-  auto load_whole = [&](int st) {
-    int8_t* buf = lds + (st & (ST - 1)) * C::STAGE;
-#pragma unroll
-    for (int i = 0; i < L; ++i) load_to_lds(src[i] + (st * KS + 16 * chunk), buf + 1024 * (wv + NW * i));
-  };
-  auto load = [&](int st) {
-    if ((st + 1) * KS <= K) {
-      load_whole(st);
-    } else {  // the last stage of a K that is no multiple of 128: zeros past K on x's side
-      int8_t* buf = lds + (st & (ST - 1)) * C::STAGE;
-      const int k = st * KS + 16 * chunk;
-#pragma unroll
-      for (int i = 0; i < L; ++i)
-        load_to_lds(wv + NW * i < GX && k >= K ? kZeroCodes : src[i] + min(k, K - 16), buf + 1024 * (wv + NW * i));
-    }
-  };
   i32x4 acc[MF][NF];
 #pragma unroll
   for (int i = 0; i < MF; ++i)
 #pragma unroll
     for (int j = 0; j < NF; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  // With U of the MF fragment rows: a tile whose last rows are missing (the end of an
+  // expert) neither loads nor multiplies them.
+  auto run = [&](auto used) {
+    constexpr int U = decltype(used)::value, LU = L - MF + U;
+    auto load_whole = [&](int st) {
+      int8_t* buf = lds + (st & (ST - 1)) * C::STAGE;
 #pragma unroll
-  for (int i = 0; i < ST - 1; ++i)
-    if (s0 + i < S) load(s0 + i);
-  // the scales travel with the first stage; the loop's barriers stand before their use
-  for (int i = threadIdx.x; i < BN; i += C::T) {
-    const int n = min(i0 + (P == 2 ? i / 32 * 16 + i % 16 : i), a.n - 1);
-    scales[i] = a.w_scale[((size_t)t.e * P + (P == 2 ? i / 16 % 2 : 0)) * a.n + n];
-  }
-  for (int i = threadIdx.x; i < BM; i += C::T) scales[BN + i] = a.x_scale[x_row(a, yr[i])];
-  i32x4 fw[NF], fx[MF];
-  auto read = [&](int st, int half) {
-    const int at = 16 * ((4 * half + q) ^ (r & 7)) + r * KS;
-    const int8_t* bx = lds + (st & (ST - 1)) * C::STAGE + wm * (BM / WGM) * KS + at;
-    const int8_t* bw = lds + (st & (ST - 1)) * C::STAGE + BM * KS + wn * (BN / WGN) * KS + at;
-#pragma unroll
-    for (int j = 0; j < NF; ++j) fw[j] = *reinterpret_cast<const i32x4*>(bw + 16 * KS * j);
-#pragma unroll
-    for (int i = 0; i < MF; ++i) fx[i] = *reinterpret_cast<const i32x4*>(bx + 16 * KS * i);
-  };
-  auto multiply = [&]() {
-#pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-      for (int j = 0; j < NF; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fx[i], acc[i][j], 0, 0, 0);
-  };
-  // waits until all loads of this wave but those of the `later` newest stages have landed
-  auto landed = [&](int later) {
-    if (later >= 2) wait_vm<2 * L>();
-    else if (later == 1) wait_vm<L>();
-    else wait_vm<0>();
-  };
-  // Stages whose own load is a whole one go first, in a loop without a branch (each
-  // costs tens of clocks, and a stage of a small tile is a few hundred).
-  int st = s0;
-  if constexpr (NW == 8) {
-    // Two waves a SIMD, of two groups one step apart: while the waves of one
-    // group multiply, those of the other read the fragments of half a stage from
-    // LDS and issue loads, then they change places at a barrier.  A stage has
-    // landed for every wave when a group reads it: each wave waited for its own
-    // loads of stage st + 1 before the barrier that ends its reads of stage st.
-    const bool second = wv >= 4;
-    landed(min(ST - 2, S - 1 - s0));
-    meet();
-    if (second) meet();
-    auto turn = [&]() {
-      meet();
-      __builtin_amdgcn_s_setprio(1);
-      multiply();
-      __builtin_amdgcn_s_setprio(0);
-      meet();
+      for (int i = 0; i < L; ++i)
+        if (i < U || i >= MF) load_to_lds(src[i] + (st * KS + 16 * chunk), buf + 1024 * (wv + NW * i));
     };
-    for (; st < S - ST; ++st) {
-      read(st, 0);
-      load_whole(st + ST - 1);  // into the buffer of stage st - 1, which both groups have read
-      wait_lds();
-      turn();
-      read(st, 1);
-      wait_vm<(ST - 2) * L>();
-      turn();
-    }
-    for (; st < S; ++st) {
-      read(st, 0);
-      if (st + ST - 1 < S) load(st + ST - 1);
-      wait_lds();
-      turn();
-      read(st, 1);
-      landed(min(ST - 2, S - 2 - st));
-      turn();
-    }
-    if (!second) meet();
-  } else {
-    auto multiply_stage = [&](int st) {
-      read(st, 0);
-      multiply();
-      read(st, 1);
-      multiply();
+    auto load = [&](int st) {
+      if ((st + 1) * KS <= K) {
+        load_whole(st);
+      } else {  // the last stage of a K that is no multiple of 128: zeros past K on x's side
+        int8_t* buf = lds + (st & (ST - 1)) * C::STAGE;
+        const int k = st * KS + 16 * chunk;
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+          if (i < U || i >= MF) load_to_lds(i < MF && k >= K ? kZeroCodes : src[i] + min(k, K - 16), buf + 1024 * (wv + NW * i));
+      }
     };
-    for (; st < S - ST; ++st) {
-      wait_vm<(ST - 2) * L>();
-      meet();
-      load_whole(st + ST - 1);  // every wave is past stage st - 1: its buffer is free
-      multiply_stage(st);
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i)
+      if (s0 + i < S) load(s0 + i);
+    // the scales travel with the first stage; the loop's barriers stand before their use
+    for (int i = threadIdx.x; i < BN; i += C::T) {
+      const int n = min(i0 + (P == 2 ? i / 32 * 16 + i % 16 : i), a.n - 1);
+      scales[i] = a.w_scale[((size_t)t.e * P + (P == 2 ? i / 16 % 2 : 0)) * a.n + n];
     }
-    for (; st < S; ++st) {
-      landed(min(ST - 2, S - 1 - st));
+    for (int i = threadIdx.x; i < BM; i += C::T) scales[BN + i] = a.x_scale[x_row(a, yr[i])];
+    i32x4 fw[NF], fx[U];
+    auto read = [&](int st, int half) {
+      const int at = 16 * ((4 * half + q) ^ (r & 7)) + r * KS;
+      const int8_t* bx = lds + (st & (ST - 1)) * C::STAGE + 16 * wm * KS + at;
+      const int8_t* bw = lds + (st & (ST - 1)) * C::STAGE + BM * KS + wn * (BN / WGN) * KS + at;
+#pragma unroll
+      for (int j = 0; j < NF; ++j) fw[j] = *reinterpret_cast<const i32x4*>(bw + 16 * KS * j);
+#pragma unroll
+      for (int i = 0; i < U; ++i) fx[i] = *reinterpret_cast<const i32x4*>(bx + 16 * WGM * KS * i);
+    };
+    auto multiply = [&]() {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fx[i], acc[i][j], 0, 0, 0);
+    };
+    // waits until all loads of this wave but those of the `later` newest stages have landed
+    auto landed = [&](int later) {
+      if (later >= 2) wait_vm<2 * LU>();
+      else if (later == 1) wait_vm<LU>();
+      else wait_vm<0>();
+    };
+    // Stages whose own load is a whole one go first, in a loop without a branch (each
+    // costs tens of clocks, and a stage of a small tile is a few hundred).
+    int st = s0;
+    if constexpr (NW == 8) {
+      // Two waves a SIMD, of two groups one step apart: while the waves of one
+      // group multiply, those of the other read the fragments of half a stage from
+      // LDS and issue loads, then they change places at a barrier.  A stage has
+      // landed for every wave when a group reads it: each wave waited for its own
+      // loads of stage st + 1 before the barrier that ends its reads of stage st.
+      const bool second = wv >= 4;
+      landed(min(ST - 2, S - 1 - s0));
       meet();
-      if (st + ST - 1 < S) load(st + ST - 1);
-      multiply_stage(st);
+      if (second) meet();
+      auto turn = [&]() {
+        meet();
+        __builtin_amdgcn_s_setprio(1);
+        multiply();
+        __builtin_amdgcn_s_setprio(0);
+        meet();
+      };
+      for (; st < S - ST; ++st) {
+        read(st, 0);
+        load_whole(st + ST - 1);  // into the buffer of stage st - 1, which both groups have read
+        wait_lds();
+        turn();
+        read(st, 1);
+        wait_vm<(ST - 2) * LU>();
+        turn();
+      }
+      for (; st < S; ++st) {
+        read(st, 0);
+        if (st + ST - 1 < S) load(st + ST - 1);
+        wait_lds();
+        turn();
+        read(st, 1);
+        landed(min(ST - 2, S - 2 - st));
+        turn();
+      }
+      if (!second) meet();
+    } else {
+      auto multiply_stage = [&](int st) {
+        read(st, 0);
+        multiply();
+        read(st, 1);
+        multiply();
+      };
+      for (; st < S - ST; ++st) {
+        wait_vm<(ST - 2) * LU>();
+        meet();
+        load_whole(st + ST - 1);  // every wave is past stage st - 1: its buffer is free
+        multiply_stage(st);
+      }
+      for (; st < S; ++st) {
+        landed(min(ST - 2, S - 1 - st));
+        meet();
+        if (st + ST - 1 < S) load(st + ST - 1);
+        multiply_stage(st);
+      }
     }
-  }
+  };
+  const int need = (t.rows + 16 * WGM - 1) / (16 * WGM);
+  if (need >= MF) run(std::integral_constant<int, MF>{});
+  else if (MF == 4 && need == 3) run(std::integral_constant<int, MF == 4 ? 3 : 1>{});
+  else if (MF == 4 && need == 2) run(std::integral_constant<int, MF == 4 ? 2 : 1>{});
+  else run(std::integral_constant<int, 1>{});
   if constexpr (C::SPLIT) {
     if (parts > 1) {
-      tile_store_part<C>(a, t, lds, tn, tiles_n, wm, wn, part, acc);
+      tile_store_part<C>(a, t, tn, tiles_n, wm, wn, part, acc);
       return;
     }
   }
@@ -721,13 +740,20 @@ static void stream_launch(const I8Args& a, int max_tiles, hipStream_t s) {
 // x by 32 matrix rows; up to 32 (24): 32 by 32.  Measured at N 7168, K 7168:
 // 1 row 10.3 us, 8 rows 11.4, 32 rows 15.0 (64 x 64 tiles, K in two parts: 16.5);
 // at N 65536 8 rows 72 us (6.5 TB/s), 32 rows 90 (64 x 64 tiles: 88).
-// Above that the tile with the least estimated time for T workgroups per 56
-// stages (K 7168): c0 + c1 * T / 256, the larger tiles in whole rounds of 256,
-// since they run one or two to a CU; up to 256 workgroups, where each has a CU to
-// itself and a stage is a chain of latencies, `lone`.  Measured at N 7168, K 7168:
-// 64 x 64 23 us at 224 tiles, 34 at 448; 64 x 128 30 us at 224, 57 at 448; 128 x 128
-// 38 us at 224 (four buffers), 66 at 448 and 127 at 896 (two buffers, two
-// workgroups to a CU; four: 73, 141); 256 x 256 94 us at 224, 356 at 896.
+// Above that the tile with the least estimated time.
+// Dense, T workgroups: c0 + c1 * T / 256 per 56 stages (K 7168), the larger tiles
+// in whole rounds of 256, since they run one or two to a CU; up to 256 workgroups,
+// where each has a CU to itself and a stage is a chain of latencies, `lone`.
+// Measured at N 7168, K 7168: 64 x 64 23 us at 224 tiles, 34 at 448; 64 x 128 30 us
+// at 224, 57 at 448; 128 x 128 38 us at 224 (four buffers), 66 at 448 and 127 at 896
+// (two buffers, two workgroups to a CU; four: 73, 141); 256 x 256 88 us at 224, 356
+// at 896.
+// Grouped, where each expert's matrix comes from HBM and tiles end early: a round
+// of 256 tiles takes g1 us a stage and g3 once, and g2 us a stage go by the rows that
+// there are.  Fitted to 81 products of 4 to 128 experts with 28 to 500 rows each, K 768
+// to 7168: the choice costs 4% over the best tile on average.  16 experts, N 4096, K
+// 4096: 80 rows each 51 us with 128 rows a tile, 58 with 256, 81 with 64; 400 rows 125
+// us with 256, 174 with 128.
 // K is split over parts while 64 x 64 tiles leave CUs without work (64 rows of
 // N 7168: 18 us in 2 parts, 22 in one; 37 rows of N 1536: 11 us in 6 parts, 17 in
 // one).
@@ -737,35 +763,43 @@ I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
   if (per <= (grouped ? 8 : 16)) return {0, 16, 1, 0};
   if (per <= (grouped ? 24 : 32)) return {1, 32, 1, 0};
   struct Model {
-    int bm, bn;
-    double c0, c1, lone;
-    bool rounds;
+    int kind, bm, bn;
+    double c0, c1, lone;    // dense
+    double g0, g1, g2, g3;  // grouped
   };
-  static constexpr Model models[] = {{64, 64, 4.0, 16.0, 22.5, false},
-                                     {64, 128, 3.0, 27.0, 30.5, true},
-                                     {128, 128, 10.0, 28.0, 38.0, true},
-                                     {256, 256, 3.0, 89.0, 92.0, true}};
+  static constexpr Model models[] = {{2, 64, 64, 4.0, 16.0, 22.5, 5.1, 0.236, 0.0, 1.3},
+                                     {3, 64, 128, 3.0, 27.0, 30.5, 2.5, 0.188, 0.302, 3.5},
+                                     {4, 128, 128, 0.0, 0.0, 38.0, 0.0, 0.241, 0.331, 5.0},
+                                     {5, 128, 128, 10.0, 28.0, 0.0, 1.9, 0.255, 0.372, 2.5},
+                                     {6, 256, 256, 3.0, 89.0, 92.0, 0.0, 1.135, 0.0, 8.1}};
   const int P = swiglu ? 2 : 1, stages = (k + KS - 1) / KS;
   I8Plan best{};
   double least = 0.0;
-  for (int i = 0; i < 4; ++i) {
-    const Model& m = models[i];
+  for (const Model& m : models) {
     const int cols = (n * P + m.bn - 1) / m.bn;
-    // the rows of an expert end inside a tile: half a tile lost on average
-    const double down = grouped ? (double)rows / m.bm + 0.5 * used : (rows + m.bm - 1) / m.bm;
-    const double tiles = down * cols;
-    const double load = m.rounds ? ceil(tiles / 256.0) : tiles / 256.0;
-    const double time = tiles <= 256.0 ? m.lone * stages / 56.0 : m.c0 + m.c1 * load * stages / 56.0;
-    if (i && time >= least) continue;
+    double tiles, time;
+    if (grouped) {
+      // the rows of an expert end anywhere in a tile: half a tile more on average
+      tiles = (per / m.bm + 0.5 < 1.0 ? 1.0 : per / m.bm + 0.5) * used * cols;
+      const double work = (per / m.bm + 0.25) * used * cols / 256.0;
+      const double load = tiles <= 256.0 ? 1.0 : m.kind == 2 ? tiles / 256.0 : ceil(tiles / 256.0);
+      time = m.g0 + (m.g1 * load + m.g2 * (work < 1.0 ? 1.0 : work)) * stages + m.g3 * load;
+    } else {
+      tiles = (double)((rows + m.bm - 1) / m.bm) * cols;
+      if (tiles <= 256.0 ? m.kind == 5 : m.kind == 4) continue;
+      const double load = m.kind == 2 ? tiles / 256.0 : ceil(tiles / 256.0);
+      time = tiles <= 256.0 ? m.lone * stages / 56.0 : m.c0 + m.c1 * load * stages / 56.0;
+    }
+    if (best.kind && time >= least) continue;
     least = time;
     int parts = 1;
-    if (i == 0 && tiles < 150.0) {
+    if (m.kind == 2 && tiles < 150.0) {
       parts = (int)(224.0 / tiles);
       if (parts > kMaxParts) parts = kMaxParts;
       if (parts > stages / 6) parts = stages / 6;
       if (parts < 1) parts = 1;
     }
-    best.kind = i < 2 ? 2 + i : i == 2 && tiles <= 256.0 ? 4 : 3 + i;
+    best.kind = m.kind;
     best.tile_rows = m.bm;
     best.parts = parts;
     best.part_bytes = parts > 1 ? (size_t)parts * rows * cols * m.bn * 4 : 0;
