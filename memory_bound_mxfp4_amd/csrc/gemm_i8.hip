@@ -88,19 +88,19 @@ __device__ __forceinline__ void meet() {
 
 // ---- few rows -------------------------------------------------------------------
 //
-// 16 * NN matrix rows by up to 16 * NX rows of x a workgroup; bound by reading
+// 16 * NN matrix rows by up to 16 rows of x a workgroup; bound by reading
 // the matrix.  The NW waves take stages of K in turn, each through a ring of ST
 // buffers of its own: no barrier until their int32 sums meet at the end, and a
 // buffer is loaded again as soon as its fragments are in registers.
-template <int NX, int NN, int P, int NW, int ST>
+template <int NN, int P, int NW, int ST>
 __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
-  constexpr int STAGE = (NX + NN) * 16 * KS, L = 2 * (NX + NN), COLS = 16 * NN / P, T = 64 * NW;
-  static_assert(NN % P == 0 && NW * ST * STAGE >= NW * NX * NN * 1024, "stream");
+  constexpr int STAGE = (1 + NN) * 16 * KS, L = 2 * (1 + NN), COLS = 16 * NN / P, T = 64 * NW;
+  static_assert(NN % P == 0 && NW * ST * STAGE >= NW * NN * 1024, "stream");
   __shared__ __attribute__((aligned(1024))) int8_t lds[NW * ST * STAGE];
-  __shared__ float scales[16 * (NN + NX)];
-  __shared__ int yr[16 * NX];
+  __shared__ float scales[16 * (NN + 1)];
+  __shared__ int yr[16];
   Tile t;
-  if (!find_tile<16 * NX>(a, blockIdx.x / tiles_n, t)) return;
+  if (!find_tile<16>(a, blockIdx.x / tiles_n, t)) return;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i0 = blockIdx.x % tiles_n * COLS, K = a.k;
@@ -109,17 +109,17 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
       if (i0 + i % COLS < a.n) store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + i / COLS) * a.n + i0 + i % COLS, 0.0f);
     return;
   }
-  for (int i = threadIdx.x; i < 16 * NX; i += T) yr[i] = y_row(a, t.p0 + min(i, t.rows - 1));
+  if (threadIdx.x < 16) yr[threadIdx.x] = y_row(a, t.p0 + min((int)threadIdx.x, t.rows - 1));
   __syncthreads();
   // lane l of a load brings chunk (l ^ row) & 7 of row l >> 3, as in the tiles below
   const int lr = lane >> 3, chunk = (lane ^ lr) & 7;
   const int8_t* src[L];
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    if (i < 2 * NX) {
+    if (i < 2) {
       src[i] = a.x + (size_t)x_row(a, yr[8 * i + lr]) * a.x_stride;
     } else {
-      const int gw = 8 * (i - 2 * NX), n = min(i0 + (P == 2 ? gw / 32 * 16 + gw % 16 : gw) + lr, a.n - 1);
+      const int gw = 8 * (i - 2), n = min(i0 + (P == 2 ? gw / 32 * 16 + gw % 16 : gw) + lr, a.n - 1);
       src[i] = a.w + (((size_t)t.e * P + (P == 2 ? gw / 16 % 2 : 0)) * a.n + n) * K;
     }
   }
@@ -130,28 +130,25 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       const int8_t* p = src[j] + min(k, K - 16);
-      if (j < 2 * NX) load_to_lds(k < K ? p : kZeroCodes, buf + 1024 * j);
+      if (j < 2) load_to_lds(k < K ? p : kZeroCodes, buf + 1024 * j);
       else load_to_lds<true>(p, buf + 1024 * j);
     }
   };
 #pragma unroll
   for (int i = 0; i < ST; ++i)
     if (i < mine) load(i, ring + i * STAGE);
-  i32x4 acc[NX][NN];
+  i32x4 acc[NN];
 #pragma unroll
-  for (int i = 0; i < NX; ++i)
-#pragma unroll
-    for (int j = 0; j < NN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  for (int j = 0; j < NN; ++j) acc[j] = i32x4{0, 0, 0, 0};
   int8_t* buf = ring;
-  i32x4 fw[2][NN], fx[2][NX];
+  i32x4 fw[2][NN], fx[2];
   auto read = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int8_t* at = buf + 16 * ((4 * h + q) ^ (r & 7)) + r * KS;
+      fx[h] = *reinterpret_cast<const i32x4*>(at);
 #pragma unroll
-      for (int i = 0; i < NX; ++i) fx[h][i] = *reinterpret_cast<const i32x4*>(at + 16 * KS * i);
-#pragma unroll
-      for (int j = 0; j < NN; ++j) fw[h][j] = *reinterpret_cast<const i32x4*>(at + 16 * KS * (NX + j));
+      for (int j = 0; j < NN; ++j) fw[h][j] = *reinterpret_cast<const i32x4*>(at + 16 * KS * (1 + j));
     }
     wait_lds();
     asm volatile("" ::: "memory");
@@ -161,10 +158,7 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < NX; ++i)
-#pragma unroll
-        for (int j = 0; j < NN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h][j], fx[h][i], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < NN; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h][j], fx[h], acc[j], 0, 0, 0);
     buf = buf + STAGE == ring + ST * STAGE ? ring : buf + STAGE;
   };
   // no branch in this loop, as in the tiles below; then what is left in the ring
@@ -188,15 +182,12 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
     const int n = min(i0 + (P == 2 ? i / 32 * 16 + i % 16 : i), a.n - 1);
     scales[i] = a.w_scale[((size_t)t.e * P + (P == 2 ? i / 16 % 2 : 0)) * a.n + n];
   }
-  for (int i = threadIdx.x; i < 16 * NX; i += T) scales[16 * NN + i] = a.x_scale[x_row(a, yr[i])];
+  if (threadIdx.x < 16) scales[16 * NN + threadIdx.x] = a.x_scale[x_row(a, yr[threadIdx.x])];
   __syncthreads();
-  // accumulator register c of lane 16 q + r: matrix row 16 j + 4 q + c, row 16 i + r of x
+  // accumulator register c of lane 16 q + r: matrix row 16 j + 4 q + c, row r of x
   int* red = reinterpret_cast<int*>(lds);
 #pragma unroll
-  for (int i = 0; i < NX; ++i)
-#pragma unroll
-    for (int j = 0; j < NN; ++j)
-      *reinterpret_cast<i32x4*>(red + ((wv * NX + i) * 16 + r) * (16 * NN) + 16 * j + 4 * q) = acc[i][j];
+  for (int j = 0; j < NN; ++j) *reinterpret_cast<i32x4*>(red + (wv * 16 + r) * (16 * NN) + 16 * j + 4 * q) = acc[j];
   __syncthreads();
   for (int i = threadIdx.x; i < t.rows * COLS; i += T) {
     const int m = i / COLS, c = i % COLS;
@@ -207,7 +198,7 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
       const int tc = c / 16 * 16 * P + 16 * p + c % 16;  // column of the tile
       int sum = 0;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) sum += red[(w * 16 * NX + m) * (16 * NN) + tc];
+      for (int w = 0; w < NW; ++w) sum += red[(w * 16 + m) * (16 * NN) + tc];
       v[p] = (float)sum * (scales[16 * NN + m] * scales[tc]);
     }
     store_y(a.y, a.y_dtype, (size_t)yr[m] * a.n + i0 + c, P == 2 ? swiglu_f(v[0], v[P - 1]) : v[0]);
@@ -375,11 +366,13 @@ hipError_t launch_i8_token(const I8Args& a, const void* x, int dtype, int max_ti
 // into LDS, before stage k is computed.
 
 // One tile configuration: BM rows of x by BN matrix rows (P matrices
-// interleaved), WGM x WGN waves, ST buffers of a stage.
-template <int BM_, int BN_, int WGM_, int WGN_, int P_, int ST_>
+// interleaved), KG groups of WGM x WGN waves that take the stages in turn, ST
+// buffers of a stage.
+template <int BM_, int BN_, int WGM_, int WGN_, int KG_, int P_, int ST_>
 struct TileCfg {
-  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, P = P_, ST = ST_;
-  static constexpr int NW = WGM * WGN, T = 64 * NW, MF = BM / WGM / 16, NF = BN / WGN / 16;  // fragments of a wave
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, KG = KG_, P = P_, ST = ST_;
+  static constexpr int NW = WGM * WGN, T = 64 * NW * KG;                     // waves of a group, threads
+  static constexpr int MF = BM / WGM / 16, NF = BN / WGN / 16, MO = MF / KG;  // fragments of a wave, rows of them it stores
   static constexpr bool SPLIT = BM == 64 && BN == 64;  // K may be split over workgroups
   static constexpr int STAGE = (BM + BN) * KS, RING = ST * STAGE;
 };
@@ -399,11 +392,11 @@ __device__ __forceinline__ u32x4 join_fragments(const u32x2& x, const u32x2& y) 
   return o;
 }
 
-// Scales a wave's sums and stores them.  Register c of acc[i][j] of lane
-// 16 q + r: matrix row 16 j + 4 q + c, row 16 i + r of x.
+// Scales a wave's sums and stores them: its fragment rows from `first` on.  Register
+// c of acc[i][j] of lane 16 q + r: matrix row 16 j + 4 q + c, row 16 i + r of x.
 template <int DT, class C>
 __device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, const int8_t* lds, int i0, int wm, int wn,
-                                           const i32x4 (&acc)[C::MF][C::NF]) {
+                                           int first, const i32x4 (&acc)[C::MO][C::NF]) {
   constexpr int P = C::P, OB = Elem<DT>::bytes, V = 16 / OB;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const float* sw = reinterpret_cast<const float*>(lds + C::RING);
@@ -412,9 +405,9 @@ __device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, const
   const bool whole = a.n % V == 0;  // 16-byte stores stay aligned, and a chunk is inside the row or outside
   const int c0 = i0 + wn * (C::BN / C::WGN / P);
 #pragma unroll
-  for (int i = 0; i < C::MF; ++i) {
-    const int m = 16 * (C::WGM * i + wm) + r;
-    if (16 * (C::WGM * i + wm) >= t.rows) break;
+  for (int i = 0; i < C::MO; ++i) {
+    const int m = 16 * (C::WGM * (first + i) + wm) + r;
+    if (m - r >= t.rows) break;
     const float s = sx[m];
     const size_t row = (size_t)yr[m] * a.n;
     auto values = [&](int j) {  // of output fragment j
@@ -469,17 +462,32 @@ __device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, const
 // all tiles' columns (the matrices interleaved as in the tile).
 template <class C>
 __device__ __forceinline__ void tile_store_part(const I8Args& a, const Tile& t, int tn, int tiles_n, int wm, int wn,
-                                                int part, const i32x4 (&acc)[C::MF][C::NF]) {
+                                                int part, int first, const i32x4 (&acc)[C::MO][C::NF]) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const size_t width = (size_t)tiles_n * C::BN;
   int* dst = a.parts + ((size_t)part * a.rows + t.p0) * width + tn * C::BN + wn * C::NF * 16 + 4 * q;
 #pragma unroll
-  for (int i = 0; i < C::MF; ++i) {
-    const int m = 16 * (C::WGM * i + wm) + r;
+  for (int i = 0; i < C::MO; ++i) {
+    const int m = 16 * (C::WGM * (first + i) + wm) + r;
     if (m >= t.rows) continue;
 #pragma unroll
     for (int j = 0; j < C::NF; ++j) *reinterpret_cast<i32x4*>(dst + m * width + 16 * j) = acc[i][j];
   }
+}
+
+template <class C>
+__device__ __forceinline__ void tile_end(const I8Args& a, const Tile& t, const int8_t* lds, int i0, int tn, int tiles_n,
+                                         int wm, int wn, int parts, int part, int first,
+                                         const i32x4 (&acc)[C::MO][C::NF]) {
+  if constexpr (C::SPLIT) {
+    if (parts > 1) {
+      tile_store_part<C>(a, t, tn, tiles_n, wm, wn, part, first, acc);
+      return;
+    }
+  }
+  if (a.y_dtype == MOE_DTYPE_BF16) tile_store<MOE_DTYPE_BF16, C>(a, t, lds, i0, wm, wn, first, acc);
+  else if (a.y_dtype == MOE_DTYPE_F16) tile_store<MOE_DTYPE_F16, C>(a, t, lds, i0, wm, wn, first, acc);
+  else tile_store<MOE_DTYPE_F32, C>(a, t, lds, i0, wm, wn, first, acc);
 }
 
 // Workgroup -> tile.  Workgroups go to the 8 XCDs in turn; each XCD gets one
@@ -492,12 +500,14 @@ __device__ __forceinline__ void tile_store_part(const I8Args& a, const Tile& t, 
 template <class C>
 __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int tiles_m, int parts, int band_rows) {
   constexpr int BM = C::BM, BN = C::BN, WGM = C::WGM, WGN = C::WGN, P = C::P, ST = C::ST, NW = C::NW, MF = C::MF,
-                NF = C::NF, GX = BM / 8, L = (BM + BN) / 8 / NW;  // L: loads of a wave and stage
-  static_assert(L * 8 * NW == BM + BN && NF % P == 0 && (ST == 2 || ST == 4) && GX == NW * MF, "tile");
+                KG = C::KG, NF = C::NF, GX = BM / 8, L = (BM + BN) / 8 / NW;  // L: loads of a wave and stage
+  static_assert(L * 8 * NW == BM + BN && NF % P == 0 && ST % KG == 0 && GX == NW * MF &&
+                    (KG == 1 || NW == 4), "tile");
   // the ring, then the tile's matrix scales, row scales and output rows
   __shared__ __attribute__((aligned(1024))) int8_t lds[C::RING + 4 * (BN + 2 * BM)];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wv % WGM, wn = wv / WGM;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kg = wave / NW, wv = wave % NW;
+  const int wm = wv % WGM, wn = wv / WGM;
   // a grouped product's grid is sized for the most tiles its slots can make: the
   // XCDs share the ones there are
   if (a.order) tiles_m = min(tiles_m, a.num_tiles[0]);
@@ -512,8 +522,7 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
   if (!find_tile<BM>(a, tm, t)) return;
   const int K = a.k, i0 = tn * (BN / P);  // first output column
   if (t.e >= a.num_experts) {
-    if (part) return;
-    for (int m = threadIdx.x / 64; m < t.rows; m += NW)
+    for (int m = wave; m < t.rows; m += KG * NW)
       for (int n = i0 + lane; n < min(i0 + BN / P, a.n); n += 64)
         store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + m) * a.n + n, 0.0f);
     return;
@@ -549,17 +558,17 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
   // expert) neither loads nor multiplies them.
   auto run = [&](auto used) {
     constexpr int U = decltype(used)::value, LU = L - MF + U;
-    auto load_whole = [&](int st) {
-      int8_t* buf = lds + (st & (ST - 1)) * C::STAGE;
+    auto load_whole = [&](int st, int b) {
+      int8_t* buf = lds + b * C::STAGE;
 #pragma unroll
       for (int i = 0; i < L; ++i)
         if (i < U || i >= MF) load_to_lds(src[i] + (st * KS + 16 * chunk), buf + 1024 * (wv + NW * i));
     };
-    auto load = [&](int st) {
+    auto load = [&](int st, int b) {  // stage st to buffer b
       if ((st + 1) * KS <= K) {
-        load_whole(st);
+        load_whole(st, b);
       } else {  // the last stage of a K that is no multiple of 128: zeros past K on x's side
-        int8_t* buf = lds + (st & (ST - 1)) * C::STAGE;
+        int8_t* buf = lds + b * C::STAGE;
         const int k = st * KS + 16 * chunk;
 #pragma unroll
         for (int i = 0; i < L; ++i)
@@ -567,8 +576,8 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
       }
     };
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i)
-      if (s0 + i < S) load(s0 + i);
+    for (int i = 0; i < ST / KG - 1; ++i)
+      if (s0 + KG * i + kg < S) load(s0 + KG * i + kg, KG * i + kg);
     // the scales travel with the first stage; the loop's barriers stand before their use
     for (int i = threadIdx.x; i < BN; i += C::T) {
       const int n = min(i0 + (P == 2 ? i / 32 * 16 + i % 16 : i), a.n - 1);
@@ -576,10 +585,10 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
     }
     for (int i = threadIdx.x; i < BM; i += C::T) scales[BN + i] = a.x_scale[x_row(a, yr[i])];
     i32x4 fw[NF], fx[U];
-    auto read = [&](int st, int half) {
+    auto read = [&](int b, int half) {
       const int at = 16 * ((4 * half + q) ^ (r & 7)) + r * KS;
-      const int8_t* bx = lds + (st & (ST - 1)) * C::STAGE + 16 * wm * KS + at;
-      const int8_t* bw = lds + (st & (ST - 1)) * C::STAGE + BM * KS + wn * (BN / WGN) * KS + at;
+      const int8_t* bx = lds + b * C::STAGE + 16 * wm * KS + at;
+      const int8_t* bw = lds + b * C::STAGE + BM * KS + wn * (BN / WGN) * KS + at;
 #pragma unroll
       for (int j = 0; j < NF; ++j) fw[j] = *reinterpret_cast<const i32x4*>(bw + 16 * KS * j);
 #pragma unroll
@@ -593,13 +602,15 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
     };
     // waits until all loads of this wave but those of the `later` newest stages have landed
     auto landed = [&](int later) {
-      if (later >= 2) wait_vm<2 * LU>();
+      if (later >= 3) wait_vm<3 * LU>();
+      else if (later == 2) wait_vm<2 * LU>();
       else if (later == 1) wait_vm<LU>();
       else wait_vm<0>();
     };
     // Stages whose own load is a whole one go first, in a loop without a branch (each
     // costs tens of clocks, and a stage of a small tile is a few hundred).
-    int st = s0;
+    int i = 0;
+    const int n = S - s0;  // stage s0 + i is in buffer i
     if constexpr (NW == 8) {
       // Two waves a SIMD, of two groups one step apart: while the waves of one
       // group multiply, those of the other read the fragments of half a stage from
@@ -607,7 +618,7 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
       // landed for every wave when a group reads it: each wave waited for its own
       // loads of stage st + 1 before the barrier that ends its reads of stage st.
       const bool second = wv >= 4;
-      landed(min(ST - 2, S - 1 - s0));
+      landed(min(ST - 2, n - 1));
       meet();
       if (second) meet();
       auto turn = [&]() {
@@ -617,43 +628,53 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
         __builtin_amdgcn_s_setprio(0);
         meet();
       };
-      for (; st < S - ST; ++st) {
-        read(st, 0);
-        load_whole(st + ST - 1);  // into the buffer of stage st - 1, which both groups have read
+      for (; i < n - ST; ++i) {
+        read(i & (ST - 1), 0);
+        load_whole(s0 + i + ST - 1, (i + ST - 1) & (ST - 1));  // both groups have read stage i - 1
         wait_lds();
         turn();
-        read(st, 1);
+        read(i & (ST - 1), 1);
         wait_vm<(ST - 2) * LU>();
         turn();
       }
-      for (; st < S; ++st) {
-        read(st, 0);
-        if (st + ST - 1 < S) load(st + ST - 1);
+      for (; i < n; ++i) {
+        read(i & (ST - 1), 0);
+        if (i + ST - 1 < n) load(s0 + i + ST - 1, (i + ST - 1) & (ST - 1));
         wait_lds();
         turn();
-        read(st, 1);
-        landed(min(ST - 2, S - 2 - st));
+        read(i & (ST - 1), 1);
+        landed(min(ST - 2, n - 2 - i));
         turn();
       }
       if (!second) meet();
     } else {
-      auto multiply_stage = [&](int st) {
-        read(st, 0);
+      // One or two groups of four waves: while one reads fragments, the other multiplies.  Group kg
+      // has stages kg, kg + KG, ... and loads them itself; at the barrier of turn i every group has
+      // its stage of that turn, and has left the buffer of the turn before.
+      constexpr int R = ST / KG;
+      auto multiply_stage = [&](int b) {
+        read(b, 0);
         multiply();
-        read(st, 1);
+        read(b, 1);
         multiply();
       };
-      for (; st < S - ST; ++st) {
-        wait_vm<(ST - 2) * LU>();
-        meet();
-        load_whole(st + ST - 1);  // every wave is past stage st - 1: its buffer is free
-        multiply_stage(st);
+      const int mine = (n - kg + KG - 1) / KG, turns = (n + KG - 1) / KG;
+      for (; i <= turns - 2 * R; i += R) {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          wait_vm<(R - 2) * LU>();
+          meet();
+          load_whole(s0 + KG * (i + u + R - 1) + kg, KG * ((u + R - 1) % R) + kg);
+          multiply_stage(KG * u + kg);
+        }
       }
-      for (; st < S; ++st) {
-        landed(min(ST - 2, S - 1 - st));
+#pragma unroll
+      for (int u = 0; u < 2 * R - 1; ++u) {
+        if (i + u >= turns) break;
+        landed(min(R - 2, mine - 1 - i - u));
         meet();
-        if (st + ST - 1 < S) load(st + ST - 1);
-        multiply_stage(st);
+        if (i + u + R - 1 < mine) load(s0 + KG * (i + u + R - 1) + kg, KG * ((u + R - 1) % R) + kg);
+        if (i + u < mine) multiply_stage(KG * (u % R) + kg);
       }
     }
   };
@@ -662,34 +683,44 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
   else if (MF == 4 && need == 3) run(std::integral_constant<int, MF == 4 ? 3 : 1>{});
   else if (MF == 4 && need == 2) run(std::integral_constant<int, MF == 4 ? 2 : 1>{});
   else run(std::integral_constant<int, 1>{});
-  if constexpr (C::SPLIT) {
-    if (parts > 1) {
-      tile_store_part<C>(a, t, tn, tiles_n, wm, wn, part, acc);
-      return;
-    }
+  if constexpr (KG == 1) {
+    tile_end<C>(a, t, lds, i0, tn, tiles_n, wm, wn, parts, part, 0, acc);
+  } else {
+    // each group gives the other half of its fragment rows away and adds what it gets
+    i32x4* swap = reinterpret_cast<i32x4*>(lds) + (wv * C::MO * NF) * 64 + lane;
+    constexpr int HALF = NW * C::MO * NF * 64;
+    static_assert(2 * HALF * 16 <= C::RING, "sums");
+    i32x4 sum[C::MO][NF];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < C::MO; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        sum[i][j] = kg ? acc[C::MO + i][j] : acc[i][j];
+        swap[kg * HALF + (i * NF + j) * 64] = kg ? acc[i][j] : acc[C::MO + i][j];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < C::MO; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) sum[i][j] += swap[(1 - kg) * HALF + (i * NF + j) * 64];
+    tile_end<C>(a, t, lds, i0, tn, tiles_n, wm, wn, parts, part, kg * C::MO, sum);
   }
-  if (a.y_dtype == MOE_DTYPE_BF16) tile_store<MOE_DTYPE_BF16, C>(a, t, lds, i0, wm, wn, acc);
-  else if (a.y_dtype == MOE_DTYPE_F16) tile_store<MOE_DTYPE_F16, C>(a, t, lds, i0, wm, wn, acc);
-  else tile_store<MOE_DTYPE_F32, C>(a, t, lds, i0, wm, wn, acc);
 }
 
 constexpr int kMaxParts = 8;
 
-// The parts of a split K added up, scaled and stored: a workgroup takes 4 rows
-// (a wave each) by 256 columns of a tile.
+// The parts of a split K (of a dense product) added up, scaled and stored: a
+// workgroup takes 4 rows, a wave each, by 256 columns.
 template <class C>
-__global__ __launch_bounds__(256) void k_i8_parts(I8Args a, int parts, int tiles_n, int tiles_m, int cols) {
-  constexpr int P = C::P, BM = C::BM, BO = C::BN / P;
-  const int c = blockIdx.x % cols, u = blockIdx.x / cols, tm = u / (BM / 4), m = u % (BM / 4) * 4 + (threadIdx.x >> 6);
-  Tile t;
-  if (!find_tile<BM>(a, tm, t) || t.e >= a.num_experts || m >= t.rows) return;
-  const int n = c * 256 + (threadIdx.x & 63) * 4;
-  if (n >= a.n) return;
-  const int yr = y_row(a, t.p0 + m);
-  const float sx = a.x_scale[x_row(a, yr)];
-  const float* sw = a.w_scale + (size_t)t.e * P * a.n;
+__global__ __launch_bounds__(256) void k_i8_parts(I8Args a, int parts, int tiles_n, int cols) {
+  constexpr int P = C::P, BO = C::BN / P;
+  const int m = blockIdx.x / cols * 4 + (threadIdx.x >> 6), n = blockIdx.x % cols * 256 + (threadIdx.x & 63) * 4;
+  if (m >= a.rows || n >= a.n) return;
+  const float sx = a.x_scale[m];
+  const float* sw = a.w_scale;
   const size_t width = (size_t)tiles_n * C::BN, step = (size_t)a.rows * width;
-  const int* src = a.parts + (size_t)(t.p0 + m) * width + n / BO * C::BN + n % BO / 16 * 16 * P + n % 16;
+  const int* src = a.parts + (size_t)m * width + n / BO * C::BN + n % BO / 16 * 16 * P + n % 16;
   float v[P][4];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
@@ -705,7 +736,7 @@ __global__ __launch_bounds__(256) void k_i8_parts(I8Args a, int parts, int tiles
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (P == 2) v[0][k] = swiglu_f(v[0][k], v[P - 1][k]);
-    if (n + k < a.n) store_y(a.y, a.y_dtype, (size_t)yr * a.n + n + k, v[0][k]);
+    if (n + k < a.n) store_y(a.y, a.y_dtype, (size_t)m * a.n + n + k, v[0][k]);
   }
 }
 
@@ -722,109 +753,109 @@ static void tile_launch(const I8Args& a, int max_tiles, int parts, hipStream_t s
   if constexpr (C::SPLIT) {
     if (parts == 1) return;
     const int cols = (a.n + 255) / 256;
-    hipLaunchKernelGGL(k_i8_parts<C>, dim3(cols * max_tiles * (C::BM / 4)), dim3(256), 0, s, a, parts, tiles_n,
-                       max_tiles, cols);
+    hipLaunchKernelGGL(k_i8_parts<C>, dim3(cols * ((a.rows + 3) / 4)), dim3(256), 0, s, a, parts, tiles_n, cols);
   }
 }
 
-template <int NX, int NN, int NW, int ST>
 static void stream_launch(const I8Args& a, int max_tiles, hipStream_t s) {
-  const int P = a.swiglu ? 2 : 1, tiles_n = (a.n * P + 16 * NN - 1) / (16 * NN);
-  const dim3 grid(tiles_n * max_tiles), block(64 * NW);
-  if (a.swiglu) hipLaunchKernelGGL((k_i8_stream<NX, NN, 2, NW, ST>), grid, block, 0, s, a, tiles_n);
-  else hipLaunchKernelGGL((k_i8_stream<NX, NN, 1, NW, ST>), grid, block, 0, s, a, tiles_n);
+  const int tiles_n = (a.n * (a.swiglu ? 2 : 1) + 31) / 32;
+  const dim3 grid(tiles_n * max_tiles), block(256);
+  if (a.swiglu) hipLaunchKernelGGL((k_i8_stream<2, 2, 4, 3>), grid, block, 0, s, a, tiles_n);
+  else hipLaunchKernelGGL((k_i8_stream<2, 1, 4, 3>), grid, block, 0, s, a, tiles_n);
 }
 
-// Which kernel a product runs on.
-// Up to 16 rows (of an expert, on average 8: some have twice that): 16 rows of
-// x by 32 matrix rows; up to 32 (24): 32 by 32.  Measured at N 7168, K 7168:
-// 1 row 10.3 us, 8 rows 11.4, 32 rows 15.0 (64 x 64 tiles, K in two parts: 16.5);
-// at N 65536 8 rows 72 us (6.5 TB/s), 32 rows 90 (64 x 64 tiles: 88).
-// Above that the tile with the least estimated time.
-// Dense, T workgroups: c0 + c1 * T / 256 per 56 stages (K 7168), the larger tiles
-// in whole rounds of 256, since they run one or two to a CU; up to 256 workgroups,
-// where each has a CU to itself and a stage is a chain of latencies, `lone`.
-// Measured at N 7168, K 7168: 64 x 64 23 us at 224 tiles, 34 at 448; 64 x 128 30 us
-// at 224, 57 at 448; 128 x 128 38 us at 224 (four buffers), 66 at 448 and 127 at 896
-// (two buffers, two workgroups to a CU; four: 73, 141); 256 x 256 88 us at 224, 356
-// at 896.
-// Grouped, where each expert's matrix comes from HBM and tiles end early: a round
-// of 256 tiles takes g1 us a stage and g3 once, and g2 us a stage go by the rows that
-// there are.  Fitted to 81 products of 4 to 128 experts with 28 to 500 rows each, K 768
-// to 7168: the choice costs 4% over the best tile on average.  16 experts, N 4096, K
-// 4096: 80 rows each 51 us with 128 rows a tile, 58 with 256, 81 with 64; 400 rows 125
-// us with 256, 174 with 128.
-// K is split over parts while 64 x 64 tiles leave CUs without work (64 rows of
-// N 7168: 18 us in 2 parts, 22 in one; 37 rows of N 1536: 11 us in 6 parts, 17 in
-// one).
+// The kernels a product may run on, in the order of I8Plan::kind: 16 rows of x by 32
+// matrix rows as a stream, and the tiles.
+struct Tiling {
+  int bm, bn;
+  int resident;            // workgroups that the card holds at a time
+  bool rounds;             // time goes by whole rounds of them
+  double d0, d1;           // dense: us a round, and a round and stage
+  double g0, g1, g2, g3, g4;  // grouped, see below
+};
+constexpr Tiling kTilings[] = {{16, 32, 512, false, 3.3, 0.105, 3.3, 1.75, 0.235, 0.0, 0.114},
+                               {64, 64, 256, true, 3.0, 0.21, 0.4, 2.9, 0.118, 0.106, 0.422},
+                               {64, 128, 256, true, 4.0, 0.30, 0.0, 3.46, 0.173, 0.136, 0.549},
+                               {128, 128, 256, true, 4.5, 0.54, 0.0, 4.58, 0.118, 0.379, 0.354},
+                               {128, 128, 512, false, 6.1, 1.15, 0.0, 4.99, 0.569, 0.0, 0.49},
+                               {256, 256, 256, true, 7.0, 1.4, 0.0, 6.44, 0.869, 0.0, 0.453}};
+constexpr int kStream = 0, kSplit = 1, kTwoToACu = 4;
+
+// Which kernel a product runs on: the one with the least estimated time.
+// Dense: T workgroups in rounds of those that the card holds, each d0 + d1 * stages.  Up
+// to 16 rows always the stream; with more rows it reads the matrix again for every 16, and is
+// taken where all its workgroups get a CU to themselves.  Two 128 x 128 tiles to a CU (two
+// buffers of a stage each) are for more than one round of single ones (four buffers).
+// Measured at N 7168, K 7168: 8 rows 10.2 us (64 x 64 tiles 12.0), 24 rows 18.4 (12.4); 128 rows:
+// 64 x 64 15.8 us, 64 x 128 20.4, 128 x 128 30.8; 500 rows: 55, 41, 37, 256 x 256 68; 2048 rows: 191,
+// 145, 136 (two to a CU: 108), 86.
+// Grouped: each expert's matrix comes from HBM, an expert's rows end anywhere in a tile
+// (half a tile more on average, of which only the rows that there are cost anything).
+// g0 + rounds * (g1 + g2 * stages) + g3 * stages * rounds' worth of rows + g4 * the time to read
+// the matrices at 6.6 TB/s, fitted to 141 products of 4 to 256 experts with 4 to 500
+// rows each, K 768 to 7168: the choice costs 2% over the best kernel on average.  16
+// experts, N 4096, K 4096, 80 rows each: 64 x 64 96 us, 128 x 128 65 (two to a CU: 50), 256 x
+// 256 56; 320 rows: 236, 132, 127, 119.  128 experts of 12 rows, N 2048, K 768: the stream 69
+// us, 128 x 128 39; 32 experts of 8, 2 x 1536, K 7168: 112, 151.
+// K is split over parts where 64 x 64 tiles leave most CUs without work and the stages saved
+// are worth the 5 us of adding the parts up (64 rows of N 1536, K 7168: 10.4 us in 8
+// parts, 11.5 in one; of 2 x 1536 and 128 rows: 14.6 in 2 parts, 12.9 in one).
 I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
-  const int used = grouped ? (rows < experts ? rows : experts) : 1;
-  const double per = (double)rows / used;
-  if (per <= (grouped ? 8 : 16)) return {0, 16, 1, 0};
-  if (per <= (grouped ? 24 : 32)) return {1, 32, 1, 0};
-  struct Model {
-    int kind, bm, bn;
-    double c0, c1, lone;    // dense
-    double g0, g1, g2, g3;  // grouped
-  };
-  static constexpr Model models[] = {{2, 64, 64, 4.0, 16.0, 22.5, 5.1, 0.236, 0.0, 1.3},
-                                     {3, 64, 128, 3.0, 27.0, 30.5, 2.5, 0.188, 0.302, 3.5},
-                                     {4, 128, 128, 0.0, 0.0, 38.0, 0.0, 0.241, 0.331, 5.0},
-                                     {5, 128, 128, 10.0, 28.0, 0.0, 1.9, 0.255, 0.372, 2.5},
-                                     {6, 256, 256, 3.0, 89.0, 92.0, 0.0, 1.135, 0.0, 8.1}};
-  const int P = swiglu ? 2 : 1, stages = (k + KS - 1) / KS;
-  I8Plan best{};
+  const int P = swiglu ? 2 : 1, stages = (k + KS - 1) / KS, used = !grouped ? 1 : rows < experts ? rows : experts;
+  const double per = (double)rows / used, read = (double)used * n * P * k / 6.6e6;
+  I8Plan best{-1, 0, 1, 0};
   double least = 0.0;
-  for (const Model& m : models) {
+  for (int kind = 0; kind < (int)(sizeof(kTilings) / sizeof(kTilings[0])); ++kind) {
+    const Tiling& m = kTilings[kind];
     const int cols = (n * P + m.bn - 1) / m.bn;
-    double tiles, time;
-    if (grouped) {
-      // the rows of an expert end anywhere in a tile: half a tile more on average
-      tiles = (per / m.bm + 0.5 < 1.0 ? 1.0 : per / m.bm + 0.5) * used * cols;
-      const double work = (per / m.bm + 0.25) * used * cols / 256.0;
-      const double load = tiles <= 256.0 ? 1.0 : m.kind == 2 ? tiles / 256.0 : ceil(tiles / 256.0);
-      time = m.g0 + (m.g1 * load + m.g2 * (work < 1.0 ? 1.0 : work)) * stages + m.g3 * load;
-    } else {
-      tiles = (double)((rows + m.bm - 1) / m.bm) * cols;
-      if (tiles <= 256.0 ? m.kind == 5 : m.kind == 4) continue;
-      const double load = m.kind == 2 ? tiles / 256.0 : ceil(tiles / 256.0);
-      time = tiles <= 256.0 ? m.lone * stages / 56.0 : m.c0 + m.c1 * load * stages / 56.0;
-    }
-    if (best.kind && time >= least) continue;
-    least = time;
+    double time;
     int parts = 1;
-    if (m.kind == 2 && tiles < 150.0) {
-      parts = (int)(224.0 / tiles);
-      if (parts > kMaxParts) parts = kMaxParts;
-      if (parts > stages / 6) parts = stages / 6;
-      if (parts < 1) parts = 1;
+    if (grouped) {
+      const double down = per / m.bm + 0.5 < 1.0 ? 1.0 : per / m.bm + 0.5;
+      double load = down * used * cols / m.resident, work = (per / m.bm + 0.25) * used * cols / m.resident;
+      if (m.rounds || kind == kTwoToACu) load = ceil(load);
+      if (load < 1.0) load = 1.0;
+      if (work < 1.0) work = 1.0;
+      time = m.g0 + (m.g1 + m.g2 * stages) * load + m.g3 * stages * work + m.g4 * read;
+      if (kind != kStream && time < 1.2 * read) time = 1.2 * read;
+    } else {
+      const double tiles = (double)((rows + m.bm - 1) / m.bm) * cols;
+      if (kind == kStream ? rows > 16 && tiles > 256.0 : kind == kTwoToACu && tiles <= 256.0) continue;
+      double load = m.rounds ? ceil(tiles / m.resident) : tiles / m.resident;
+      if (load < 1.0) load = 1.0;
+      time = kind == kStream && rows <= 16 ? 0.0 : (m.d0 + m.d1 * stages) * load;
+      if (kind == kSplit) {
+        parts = (int)(224.0 / tiles);
+        if (parts > kMaxParts) parts = kMaxParts;
+        if (parts > stages / 6) parts = stages / 6;
+        const double saved = parts > 1 ? m.d1 * (stages - stages / parts) - 5.0 : 0.0;
+        if (saved <= 0.0) parts = 1;
+        else time -= saved;
+      }
     }
-    best.kind = m.kind;
-    best.tile_rows = m.bm;
-    best.parts = parts;
-    best.part_bytes = parts > 1 ? (size_t)parts * rows * cols * m.bn * 4 : 0;
+    if (best.kind >= 0 && time >= least) continue;
+    least = time;
+    best = I8Plan{kind, m.bm, parts, parts > 1 ? (size_t)parts * rows * cols * m.bn * 4 : 0};
   }
   return best;
 }
 
 template <int P>
 static void tiles_launch(const I8Args& a, const I8Plan& plan, int max_tiles, hipStream_t s) {
-  if (plan.kind == 2) tile_launch<TileCfg<64, 64, 2, 2, P, 4>>(a, max_tiles, plan.parts, s);
-  else if (plan.kind == 3) tile_launch<TileCfg<64, 128, 2, 2, P, 4>>(a, max_tiles, 1, s);
-  else if (plan.kind == 4) tile_launch<TileCfg<128, 128, 4, 2, P, 4>>(a, max_tiles, 1, s);
-  else if (plan.kind == 5) tile_launch<TileCfg<128, 128, 4, 2, P, 2>>(a, max_tiles, 1, s);
-  else tile_launch<TileCfg<256, 256, 4, 2, P, 2>>(a, max_tiles, 1, s);
+  if (plan.kind == 1) tile_launch<TileCfg<64, 64, 2, 2, 2, P, 8>>(a, max_tiles, plan.parts, s);
+  else if (plan.kind == 2) tile_launch<TileCfg<64, 128, 2, 2, 2, P, 6>>(a, max_tiles, 1, s);
+  else if (plan.kind == 3) tile_launch<TileCfg<128, 128, 4, 2, 1, P, 4>>(a, max_tiles, 1, s);
+  else if (plan.kind == 4) tile_launch<TileCfg<128, 128, 4, 2, 1, P, 2>>(a, max_tiles, 1, s);
+  else tile_launch<TileCfg<256, 256, 4, 2, 1, P, 2>>(a, max_tiles, 1, s);
 }
 
 bool i8_launchable(const I8Plan& plan, int n, bool swiglu, int max_tiles) {
-  const size_t bn = plan.kind <= 1 ? 32 : plan.kind == 2 ? 64 : plan.kind <= 5 ? 128 : 256;
-  const size_t cols = ((size_t)n * (swiglu ? 2 : 1) + bn - 1) / bn;
+  const size_t bn = kTilings[plan.kind].bn, cols = ((size_t)n * (swiglu ? 2 : 1) + bn - 1) / bn;
   return cols * max_tiles * plan.parts < ((size_t)1 << 31) / 512;  // threads of a launch, and ids in int
 }
 
 hipError_t launch_gemm_i8(const I8Args& a, const I8Plan& plan, int max_tiles, hipStream_t s) {
-  if (plan.kind == 0) stream_launch<1, 2, 4, 3>(a, max_tiles, s);
-  else if (plan.kind == 1) stream_launch<2, 2, 4, 2>(a, max_tiles, s);
+  if (plan.kind == 0) stream_launch(a, max_tiles, s);
   else if (a.swiglu) tiles_launch<2>(a, plan, max_tiles, s);
   else tiles_launch<1>(a, plan, max_tiles, s);
   return hipGetLastError();

@@ -115,8 +115,8 @@ hipError_t launch_route(const void* logits, int dtype, size_t row_stride, int ro
 // each map, and the maps.  Map i lists, for every expert that has slots (and
 // for the slots without one, as expert num_experts), the tiles of kTileRows[i]
 // of its positions: {expert | positions << 16, first position}.
-constexpr int kTileMaps = 5;
-constexpr int kTileRows[kTileMaps] = {16, 32, 64, 128, 256};
+constexpr int kTileMaps = 4;
+constexpr int kTileRows[kTileMaps] = {16, 64, 128, 256};
 struct TileMaps {
   int2* t[kTileMaps];
 };
@@ -148,7 +148,7 @@ struct I8Args {
   const int32_t *order, *num_tiles;
   const int2* tiles;
   int num_experts, x_div;
-  int32_t* parts;  // int32 sums of each part of a split K: [part][position][1 or 2][n]
+  int32_t* parts;  // int32 sums of each part of a split K: [part][position][columns of all tiles]
 };
 // How a product runs: kernel and tile (kind), rows of a tile, parts that K is
 // split into and the bytes of their sums.  rows: dense rows, or slots of

@@ -527,3 +527,77 @@ def test_memory_of_a_call_on_another_stream():
         for a, b in zip(want, got):
             assert torch.equal(a, b)
         assert all(bool((t == 0x55).all()) for t in trash)
+
+
+def _codes_case(rows, w_shape, k, seed):
+    """Codes and scales on the GPU, and the scaled products in float64 (of whole numbers, so exact before the scales)."""
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randint(-127, 128, (rows, k), generator=g, dtype=torch.int8).cuda()
+    w = torch.randint(-127, 128, w_shape + (k,), generator=g, dtype=torch.int8).cuda()
+    s = (torch.rand(rows, generator=g) * 1e-3 + 1e-4).cuda()
+    ws = (torch.rand(w_shape, generator=g) * 1e-3 + 1e-4).cuda()
+
+    def product(take, w, ws):
+        return (q[take].double() @ w.double().t()) * (s[take].double()[:, None] * ws.double()[None])
+
+    return q, s, w, ws, product
+
+
+@pytest.mark.parametrize("m,n,k,swiglu", [
+    # few rows of a narrow matrix, and 64 x 64 tiles with K in one and in several parts
+    (37, 520, 7184, False), (20, 4100, 272, False), (20, 2050, 1040, True), (70, 4100, 7184, False), (20, 4100, 7184, False),
+    (20, 2050, 7184, True), (33, 3000, 7184, False), (130, 520, 7184, True), (700, 100, 7184, True), (60, 200, 16400, False),
+    # 64 x 128
+    (200, 4100, 80, False), (200, 4100, 272, False), (200, 4100, 7184, False), (70, 4100, 2064, True), (70, 4104, 1152, True),
+    # 128 x 128, one and two to a CU
+    (1000, 2050, 272, False), (1000, 2050, 7184, False), (200, 4100, 1040, True), (513, 7000, 272, False),
+    (1000, 2050, 1040, True), (1000, 4100, 2064, False),
+    # 256 x 256
+    (1500, 7000, 80, False), (1500, 7000, 1040, False), (1500, 7000, 256, False), (700, 7000, 2064, True)])
+def test_gemm_tiles(m, n, k, swiglu):
+    """The sizes at which each kernel and tile is taken, with rows, columns and K that end inside one."""
+    import torch
+    q, s, w, ws, product = _codes_case(m, (2, n) if swiglu else (n,), k, m + n + k)
+    every = slice(None)
+    for out in ("f32", "bf16"):
+        y = moe.gemm_i8(q, w, ws, x_scale=s, swiglu=swiglu, out_dtype=ref.torch_dtype(out))
+        torch.cuda.synchronize()
+        if swiglu:
+            g, u = (product(every, w[i], ws[i]).cpu().numpy() for i in range(2))
+            _close(y, ref.silu(g) * u, ref.swiglu_bound(g, u, out))
+        else:
+            want = product(every, w, ws).cpu().numpy()
+            _close(y, want, ref.product_bound(want, out))
+
+
+@pytest.mark.parametrize("tokens,top_k,E,n,k,swiglu", [
+    (24, 2, 16, 1030, 1040, False), (20, 6, 40, 100, 7184, True), (3, 2, 2, 100, 7184, False), (60, 2, 40, 520, 1040, False),
+    (160, 2, 16, 1030, 7184, False), (1400, 2, 40, 520, 272, False), (175, 2, 5, 2050, 1040, True), (60, 2, 40, 2050, 2064, False),
+    (60, 2, 40, 1030, 1040, False), (800, 2, 40, 520, 7184, True), (3000, 2, 40, 1030, 272, False), (3000, 2, 40, 520, 1040, True),
+    (1500, 4, 40, 1030, 2064, False)])
+def test_experts_tiles(tokens, top_k, E, n, k, swiglu):
+    """The same for the experts: some with many rows, some with few or none, and slots without an expert."""
+    import torch
+    q, s, w, ws, product = _codes_case(tokens, (E, 2, n) if swiglu else (E, n), k, tokens + n + k)
+    g = torch.Generator().manual_seed(k)
+    idx = (torch.rand(tokens, top_k, generator=g) ** 2 * (E + 1)).to(torch.int32) - 1
+    idx[idx == E // 2] = 0
+    groups = moe.moe_group_slots(idx.cuda(), E)
+    for out in ("f32", "bf16"):
+        y = moe.experts_gemm_i8(q, groups, w, ws, x_scale=s, swiglu=swiglu, out_dtype=ref.torch_dtype(out))
+        torch.cuda.synchronize()
+        flat = idx.flatten()
+        assert bool((y[(flat < 0).nonzero()[:, 0].cuda()] == 0).all())
+        for e in range(E):
+            slots = (flat == e).nonzero()[:, 0]
+            if not len(slots):
+                continue
+            rows = (slots // top_k).cuda()
+            got = y[slots.cuda()]
+            if swiglu:
+                a, b = (product(rows, w[e, i], ws[e, i]).cpu().numpy() for i in range(2))
+                _close(got, ref.silu(a) * b, ref.swiglu_bound(a, b, out))
+            else:
+                want = product(rows, w[e], ws[e]).cpu().numpy()
+                _close(got, want, ref.product_bound(want, out))
