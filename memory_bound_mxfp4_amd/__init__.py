@@ -386,6 +386,8 @@ class RouteParamsC(ctypes.Structure):
 @functools.lru_cache(maxsize=256)
 def _route_params(*fields):
     """The C struct of a routing, by reference; a decode step routes the same way again and again."""
+    for v in fields[:-1]:
+        _int(v, "a parameter of the routing")
     return ctypes.byref(RouteParamsC(*fields))
 
 
@@ -393,11 +395,17 @@ _SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 _dtypes: dict = {}
 
 
+_module = None
+
+
 def _torch():
-    import torch
-    if not _dtypes:
+    """torch, imported when it is first needed; a statement in each call would cost as much as its checks."""
+    global _module
+    if _module is None:
+        import torch
         _dtypes.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16})
-    return torch
+        _module = torch
+    return _module
 
 
 def _dtype_code(dtype, what: str, int8: bool = False) -> int:
@@ -418,9 +426,12 @@ def _want(t, shape: tuple, dtype, device, what: str):
     return t
 
 
+_MAX_INT = 0x7FFFFFFF
+
+
 def _int(v: int, what: str) -> int:
     """Sizes go to the C interface as 32-bit integers, and a longer one would lose its upper bits on the way."""
-    if not -0x80000000 <= v <= 0x7FFFFFFF:
+    if not -_MAX_INT <= v <= _MAX_INT:
         raise ValueError(f"{what} is out of range: {v}")
     return v
 
@@ -430,8 +441,8 @@ def _rows(t, what: str):
     if t.dim() != 2:
         raise ValueError(f"{what} must be a matrix")
     rows, cols = t.shape
-    _int(rows, f"the rows of {what}")
-    _int(cols, f"the columns of {what}")
+    if rows > _MAX_INT or cols > _MAX_INT:
+        raise ValueError(f"{what} is out of range: {rows} x {cols}")
     if t.is_contiguous():
         return rows, cols, cols
     stride = t.stride(0) if rows > 1 else cols
@@ -454,20 +465,27 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+_current: tuple = ()  # torch's raw current stream of a device, and its current device
+
+
 def _launch(what: str, device, stream, *args):
     """Calls an entry point with `device` current, on the given stream or on that device's current one."""
-    import torch
+    global _current
     if device.type != "cuda":
         raise ValueError(f"{what} takes tensors on the GPU, not on {device}")
-    f = getattr(_lib or load(), what)
+    if not _current:
+        # as current_stream(device) and current_device(), without building a Stream
+        _current = (_torch()._C._cuda_getCurrentRawStream, _torch()._C._cuda_getDevice)
+    index = device.index
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(device.index)  # as current_stream(device), without building a Stream
+        s = _current[0](index)
     else:
         s = stream if isinstance(stream, int) else stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    f = getattr(_lib or load(), what)
+    if index == _current[1]():
         rc = f(*args, s)
     else:
-        with torch.cuda.device(device):
+        with _torch().cuda.device(device):
             rc = f(*args, s)
     if rc != MOE_OK:
         raise MoeError(rc, what)
@@ -485,8 +503,6 @@ def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int
     code = _dtype_code(logits.dtype, "logits")
     if bias is not None:
         _want(bias, (E,), torch.float32, dev, "bias")
-    for v, what in ((top_k, "top_k"), (groups, "groups"), (top_groups, "top_groups"), (group_top, "group_top")):
-        _int(v, what)
     p = _route_params(E, top_k, _SCORES[score], groups, top_groups, group_top, int(bool(renorm)), scale)
     shape = (rows, top_k)
     idx = _empty(shape, torch.int32, dev, stream) if idx is None else _want(idx, shape, torch.int32, dev, "idx")
@@ -516,7 +532,7 @@ def gemm_i8_workspace_size(m: int, n: int, k: int, swiglu: bool, x_dtype) -> int
 
 def _i8_operands(x, x_scale, w, w_scale, swiglu: bool, lead: tuple):
     """Shape checks shared by the two products; w is lead + [2][n][k] with swiglu, else lead + [n][k]."""
-    import torch
+    torch = _torch()
     rows, k, stride = _rows(x, "x")
     dev = x.device
     parts = (2,) if swiglu else ()
@@ -533,7 +549,7 @@ def _i8_operands(x, x_scale, w, w_scale, swiglu: bool, lead: tuple):
 
 
 def _out(out, shape, out_dtype, device, stream):
-    import torch
+    torch = _torch()
     if out is None:
         return _empty(shape, torch.bfloat16 if out_dtype is None else out_dtype, device, stream)
     if out_dtype is not None and out.dtype != out_dtype:
@@ -542,7 +558,7 @@ def _out(out, shape, out_dtype, device, stream):
 
 
 def _workspace(ws, need: int, device, stream):
-    import torch
+    torch = _torch()
     if ws is None:
         return _empty(need, torch.uint8, device, stream) if need else None
     return _want(ws, tuple(ws.shape), torch.uint8, device, "ws")
@@ -589,7 +605,7 @@ def alloc_slot_groups(tokens: int, top_k: int, num_experts: int, device=None, st
 
 def moe_group_slots(idx, num_experts: int, groups: Optional[SlotGroups] = None, stream=None) -> SlotGroups:
     """Sort the slots of idx (int32 [tokens][k]) by expert (moe_group_slots)."""
-    import torch
+    torch = _torch()
     if idx.dim() != 2:
         raise ValueError("idx must be a matrix")
     tokens, top_k = idx.shape
@@ -635,9 +651,11 @@ def experts_gemm_i8(x, groups: SlotGroups, w, w_scale, x_scale=None, swiglu: boo
 def moe_combine(y, gate, residual=None, out=None, stream=None):
     """out[t] = residual[t] + sum_j gate[t][j] * y[t * k + j] (moe_combine), fp32 [tokens][hidden]; out may be
     residual itself. Returns out."""
-    import torch
-    tokens, top_k, _ = _rows(gate, "gate")
-    hidden = _int(y.shape[-1], "hidden")
+    torch = _torch()
+    tokens, top_k = gate.shape
+    hidden = y.shape[-1]
+    if tokens > _MAX_INT or hidden > _MAX_INT:
+        raise ValueError(f"{tokens} tokens of {hidden} columns are out of range")
     dev = y.device
     _want(gate, (tokens, top_k), torch.float32, dev, "gate")
     _want(y, (tokens * top_k, hidden), y.dtype, dev, "y")

@@ -92,6 +92,9 @@ __device__ __forceinline__ void meet() {
 // the matrix.  The NW waves take stages of K in turn, each through a ring of ST
 // buffers of its own: no barrier until their int32 sums meet at the end, and a
 // buffer is loaded again as soon as its fragments are in registers.
+// N 7168, K 7168, 8 rows: 10.2 us (5 TB/s, 2.5 us of it start and end); N 65536: 72 us
+// (6.5 TB/s); 8 tokens with 16 of 128 experts each, 2 x 1024, K 7168: 91 us (6.4 TB/s).
+// (Waves that share a buffer and meet at every stage reached 5.2 TB/s.)
 template <int NN, int P, int NW, int ST>
 __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
   constexpr int STAGE = (1 + NN) * 16 * KS, L = 2 * (1 + NN), COLS = 16 * NN / P, T = 64 * NW;
@@ -207,13 +210,15 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
 
 // One float row of x, quantised on the way: each workgroup finds the row's scale
 // and codes itself (14 KB at K 7168, from L2) while the first stages of its 32
-// matrix rows travel, which costs less than a launch of its own.  Grouped: every
-// slot reads this row.
+// matrix rows travel, which costs less than a launch of its own: N 7168, K 7168 10 us
+// (5.1 TB/s) where the two launches took 12 and 3.  Grouped: every slot reads this
+// row.
 constexpr int kTokenChunks = 8;  // of 16 bytes of x a thread
 
 template <int DT, int P>
 __global__ __launch_bounds__(256) void k_i8_token(I8Args a, const u32x4* __restrict__ x, int tiles_n) {
-  constexpr int NW = 4, NN = 2, ST = 3, STAGE = NN * 16 * KS, L = 2 * NN, COLS = 16 * NN / P, N = Chunk<DT>::N, NC = kTokenChunks;
+  constexpr int NW = 4, NN = 2, ST = 3, STAGE = NN * 16 * KS, L = 2 * NN, COLS = 16 * NN / P;
+  constexpr int N = Chunk<DT>::N, NC = kTokenChunks;
   __shared__ __attribute__((aligned(1024))) int8_t lds[NW * ST * STAGE];
   __shared__ __attribute__((aligned(16))) int8_t row[256 * NC * N];  // the codes of x
   __shared__ uint32_t part[NW];
@@ -363,7 +368,16 @@ hipError_t launch_i8_token(const I8Args& a, const void* x, int dtype, int max_ti
 // A workgroup computes BM rows of x by BN rows of the matrix (with SwiGLU BN/2
 // gate rows and their BN/2 up rows, alternating by 16).  K runs in
 // stages kept in ST buffers: the loads of stage k + ST - 1 are issued, straight
-// into LDS, before stage k is computed.
+// into LDS, before stage k is computed.  (Loads through registers instead, of all or
+// of the matrix alone, took 12% to 20% longer.)
+//
+// 256 x 256 tiles are bound by the matrix units at the clock that the power limit leaves
+// them: 8192 rows, N 7168, K 7168 take 375 to 400 us (2.1 to 2.25 POP/s) with random
+// codes, 290 with zeros.  At K 1536 a tile takes 28 us: 19 for its 12 stages, 2 to start, 7 for the
+// outputs.  (One workgroup a CU that goes from tile to tile, loading the first
+// stage of the next one ahead: 8% slower, its waves wait for their own stores.)
+// The smaller tiles are bound by the latency of a stage, loads to LDS, barrier, LDS to
+// registers, multiplications: 509 rows, SwiGLU of 2 x 1536, K 7168 22 us (1.0 POP/s).
 
 // One tile configuration: BM rows of x by BN matrix rows (P matrices
 // interleaved), KG groups of WGM x WGN waves that take the stages in turn, ST
@@ -379,7 +393,8 @@ struct TileCfg {
 
 // Exchanges between the 16-lane groups of a wave so that of two neighbouring fragments
 // (x: columns 4 q .. of the first, y: of the second) lane 16 q + r gets 8 columns from
-// 8 q: a store then writes 64 bytes of a row.
+// 8 q: a store then writes 64 bytes of a row.  (Through LDS, whole rows at a time, the
+// outputs of a 256 x 256 tile took 2 us longer: two barriers with nothing beside them.)
 __device__ __forceinline__ u32x4 join_fragments(const u32x2& x, const u32x2& y) {
   u32x4 o;
 #pragma unroll
@@ -475,6 +490,7 @@ __device__ __forceinline__ void tile_store_part(const I8Args& a, const Tile& t, 
   }
 }
 
+// The end of a tile: its outputs, or its part of the sums.
 template <class C>
 __device__ __forceinline__ void tile_end(const I8Args& a, const Tile& t, const int8_t* lds, int i0, int tn, int tiles_n,
                                          int wm, int wn, int parts, int part, int first,
@@ -572,7 +588,8 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
         const int k = st * KS + 16 * chunk;
 #pragma unroll
         for (int i = 0; i < L; ++i)
-          if (i < U || i >= MF) load_to_lds(i < MF && k >= K ? kZeroCodes : src[i] + min(k, K - 16), buf + 1024 * (wv + NW * i));
+          if (i < U || i >= MF)
+            load_to_lds(i < MF && k >= K ? kZeroCodes : src[i] + min(k, K - 16), buf + 1024 * (wv + NW * i));
       }
     };
 #pragma unroll
@@ -602,8 +619,7 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
     };
     // waits until all loads of this wave but those of the `later` newest stages have landed
     auto landed = [&](int later) {
-      if (later >= 3) wait_vm<3 * LU>();
-      else if (later == 2) wait_vm<2 * LU>();
+      if (later >= 2) wait_vm<2 * LU>();
       else if (later == 1) wait_vm<LU>();
       else wait_vm<0>();
     };
@@ -616,7 +632,7 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
       // group multiply, those of the other read the fragments of half a stage from
       // LDS and issue loads, then they change places at a barrier.  A stage has
       // landed for every wave when a group reads it: each wave waited for its own
-      // loads of stage st + 1 before the barrier that ends its reads of stage st.
+      // loads of the next stage before the barrier that ends its reads of this one.
       const bool second = wv >= 4;
       landed(min(ST - 2, n - 1));
       meet();
@@ -650,7 +666,9 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
     } else {
       // One or two groups of four waves: while one reads fragments, the other multiplies.  Group kg
       // has stages kg, kg + KG, ... and loads them itself; at the barrier of turn i every group has
-      // its stage of that turn, and has left the buffer of the turn before.
+      // its stage of that turn, and has left the buffer of the turn before.  (One group of four
+      // waves: 19 us where two take 15.7, 128 rows, N 7168, K 7168.)  A ring is one body, so that
+      // its buffers are constants: with their numbers in registers 64 x 128 tiles took 30 us for 21.
       constexpr int R = ST / KG;
       auto multiply_stage = [&](int b) {
         read(b, 0);
@@ -769,9 +787,9 @@ static void stream_launch(const I8Args& a, int max_tiles, hipStream_t s) {
 struct Tiling {
   int bm, bn;
   int resident;            // workgroups that the card holds at a time
-  bool rounds;             // time goes by whole rounds of them
-  double d0, d1;           // dense: us a round, and a round and stage
-  double g0, g1, g2, g3, g4;  // grouped, see below
+  bool rounds;             // dense: time goes by whole rounds of them
+  double d0, d1;           // dense: us a round, and a stage of a round
+  double g0, g1, g2, g3, g4;  // grouped, see i8_plan
 };
 constexpr Tiling kTilings[] = {{16, 32, 512, false, 3.3, 0.105, 3.3, 1.75, 0.235, 0.0, 0.114},
                                {64, 64, 256, true, 3.0, 0.21, 0.4, 2.9, 0.118, 0.106, 0.422},
@@ -813,7 +831,7 @@ I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
     if (grouped) {
       const double down = per / m.bm + 0.5 < 1.0 ? 1.0 : per / m.bm + 0.5;
       double load = down * used * cols / m.resident, work = (per / m.bm + 0.25) * used * cols / m.resident;
-      if (m.rounds || kind == kTwoToACu) load = ceil(load);
+      if (kind > kSplit) load = ceil(load);
       if (load < 1.0) load = 1.0;
       if (work < 1.0) work = 1.0;
       time = m.g0 + (m.g1 + m.g2 * stages) * load + m.g3 * stages * work + m.g4 * read;
