@@ -94,11 +94,13 @@ __device__ __forceinline__ void meet() {
 // buffer is loaded again as soon as its fragments are in registers.
 // N 7168, K 7168, 8 rows: 10.2 us (5 TB/s, 2.5 us of it start and end); N 65536: 72 us
 // (6.5 TB/s); 8 tokens with 16 of 128 experts each, 2 x 1024, K 7168: 91 us (6.4 TB/s).
-// (Waves that share a buffer and meet at every stage reached 5.2 TB/s.)
+// (Waves that share a buffer and meet at every stage reached 5.2 TB/s.  Two buffers a
+// wave, three workgroups to a CU, are as fast as three for long K and better for
+// short: 128 experts, N 7168, K 1024, 72 us for 86.)
 template <int NN, int P, int NW, int ST>
 __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
   constexpr int STAGE = (1 + NN) * 16 * KS, L = 2 * (1 + NN), COLS = 16 * NN / P, T = 64 * NW;
-  static_assert(NN % P == 0 && NW * ST * STAGE >= NW * NN * 1024, "stream");
+  static_assert(NN <= 2 && NW * ST * STAGE >= NW * NN * 1024, "stream");
   __shared__ __attribute__((aligned(1024))) int8_t lds[NW * ST * STAGE];
   __shared__ float scales[16 * (NN + 1)];
   __shared__ int yr[16];
@@ -122,8 +124,8 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
     if (i < 2) {
       src[i] = a.x + (size_t)x_row(a, yr[8 * i + lr]) * a.x_stride;
     } else {
-      const int gw = 8 * (i - 2), n = min(i0 + (P == 2 ? gw / 32 * 16 + gw % 16 : gw) + lr, a.n - 1);
-      src[i] = a.w + (((size_t)t.e * P + (P == 2 ? gw / 16 % 2 : 0)) * a.n + n) * K;
+      const int gw = 8 * (i - 2), n = min(i0 + gw % COLS + lr, a.n - 1);  // P 2: COLS gate rows, then the up rows
+      src[i] = a.w + (((size_t)t.e * P + gw / COLS) * a.n + n) * K;
     }
   }
   const int stages = (K + KS - 1) / KS, mine = wv < stages ? (stages - wv + NW - 1) / NW : 0;
@@ -182,8 +184,8 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
     multiply();
   }
   for (int i = threadIdx.x; i < 16 * NN; i += T) {
-    const int n = min(i0 + (P == 2 ? i / 32 * 16 + i % 16 : i), a.n - 1);
-    scales[i] = a.w_scale[((size_t)t.e * P + (P == 2 ? i / 16 % 2 : 0)) * a.n + n];
+    const int n = min(i0 + i % COLS, a.n - 1);
+    scales[i] = a.w_scale[((size_t)t.e * P + i / COLS) * a.n + n];
   }
   if (threadIdx.x < 16) scales[16 * NN + threadIdx.x] = a.x_scale[x_row(a, yr[threadIdx.x])];
   __syncthreads();
@@ -198,7 +200,7 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
     float v[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int tc = c / 16 * 16 * P + 16 * p + c % 16;  // column of the tile
+      const int tc = COLS * p + c;  // column of the tile
       int sum = 0;
 #pragma unroll
       for (int w = 0; w < NW; ++w) sum += red[(w * 16 + m) * (16 * NN) + tc];
@@ -209,40 +211,40 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
 }
 
 // One float row of x, quantised on the way: each workgroup finds the row's scale
-// and codes itself (14 KB at K 7168, from L2) while the first stages of its 32
-// matrix rows travel, which costs less than a launch of its own: N 7168, K 7168 10 us
-// (5.1 TB/s) where the two launches took 12 and 3.  Grouped: every slot reads this
-// row.
-constexpr int kTokenChunks = 8;  // of 16 bytes of x a thread
+// and codes itself (14 KB at K 7168, from L2) while the first stages of its 16
+// matrix rows travel, which costs less than a launch of its own.  8 waves, so that
+// this is short and few stages follow: N 7168, K 7168 10.5 us back to back (4.9 TB/s;
+// 4 waves with 32 rows 12.0), N 1536 6.6 (8.7), N 65536 73 (6.4 TB/s).  Grouped: every
+// slot reads this row.
+constexpr int kTokenBytes = 32768;  // of x at most
 
-template <int DT, int P>
-__global__ __launch_bounds__(256) void k_i8_token(I8Args a, const u32x4* __restrict__ x, int tiles_n) {
-  constexpr int NW = 4, NN = 2, ST = 3, STAGE = NN * 16 * KS, L = 2 * NN, COLS = 16 * NN / P;
-  constexpr int N = Chunk<DT>::N, NC = kTokenChunks;
+template <int DT, int P, int NW, int ST>
+__global__ __launch_bounds__(64 * NW) void k_i8_token(I8Args a, const u32x4* __restrict__ x, int tiles_n) {
+  constexpr int T = 64 * NW, STAGE = 16 * KS, L = 2, COLS = 16 / P, N = Chunk<DT>::N, NC = kTokenBytes / 16 / T;
   __shared__ __attribute__((aligned(1024))) int8_t lds[NW * ST * STAGE];
-  __shared__ __attribute__((aligned(16))) int8_t row[256 * NC * N];  // the codes of x
+  __shared__ __attribute__((aligned(16))) int8_t row[kTokenBytes / 16 * N];  // the codes of x
   __shared__ uint32_t part[NW];
-  __shared__ int red[NW][16 * NN];
+  __shared__ __attribute__((aligned(16))) int red[NW][16];
   Tile t;
   if (!find_tile<16>(a, blockIdx.x / tiles_n, t)) return;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i0 = blockIdx.x % tiles_n * COLS, K = a.k, C = K / N;
   if (t.e >= a.num_experts) {  // slots without an expert: rows of zeros
-    for (int i = threadIdx.x; i < t.rows * COLS; i += 256)
+    for (int i = threadIdx.x; i < t.rows * COLS; i += T)
       if (i0 + i % COLS < a.n) store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + i / COLS) * a.n + i0 + i % COLS, 0.0f);
     return;
   }
   u32x4 c[NC];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) c[i] = (int)threadIdx.x + 256 * i < C ? x[threadIdx.x + 256 * i] : u32x4{0u, 0u, 0u, 0u};
+  for (int i = 0; i < NC; ++i) c[i] = (int)threadIdx.x + T * i < C ? x[threadIdx.x + T * i] : u32x4{0u, 0u, 0u, 0u};
   __builtin_amdgcn_sched_barrier(0);
   const int lr = lane >> 3, chunk = (lane ^ lr) & 7;
   const int8_t* src[L];
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    const int n = min(i0 + (P == 2 ? 8 * i % 16 : 8 * i) + lr, a.n - 1);
-    src[i] = a.w + (((size_t)t.e * P + (P == 2 ? i / 2 : 0)) * a.n + n) * K;
+    const int n = min(i0 + (P == 2 ? lr : 8 * i + lr), a.n - 1);  // P 2: 8 gate rows, 8 up rows
+    src[i] = a.w + (((size_t)t.e * P + (P == 2 ? i : 0)) * a.n + n) * K;
   }
   const int stages = (K + KS - 1) / KS, mine = wv < stages ? (stages - wv + NW - 1) / NW : 0;
   int8_t* ring = lds + wv * ST * STAGE;
@@ -267,11 +269,14 @@ __global__ __launch_bounds__(256) void k_i8_token(I8Args a, const u32x4* __restr
   if (lane == 0) part[wv] = m;
   wait_lds();
   meet();
-  const RowScale rs = row_scale(max(max(part[0], part[1]), max(part[2], part[3])));
+  m = part[0];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) m = max(m, part[i]);
+  const RowScale rs = row_scale(m);
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     // chunks past K, up to the end of its last stage, come out as zeros
-    const int at = threadIdx.x + 256 * i;
+    const int at = threadIdx.x + T * i;
     if (at >= stages * (KS / N)) break;
     float v[N];
     Chunk<DT>::widen(c[i], v);
@@ -282,18 +287,14 @@ __global__ __launch_bounds__(256) void k_i8_token(I8Args a, const u32x4* __restr
   }
   wait_lds();
   meet();
-  i32x4 acc[NN];
-#pragma unroll
-  for (int j = 0; j < NN; ++j) acc[j] = i32x4{0, 0, 0, 0};
+  i32x4 acc{0, 0, 0, 0};
   int8_t* buf = ring;
-  i32x4 fw[2][NN], fx[2];
+  i32x4 fw[2], fx[2];
   auto read = [&](int st) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       fx[h] = *reinterpret_cast<const i32x4*>(row + (wv + NW * st) * KS + 64 * h + 16 * q);  // the row in all 16 columns
-#pragma unroll
-      for (int j = 0; j < NN; ++j)
-        fw[h][j] = *reinterpret_cast<const i32x4*>(buf + 16 * ((4 * h + q) ^ (r & 7)) + r * KS + 16 * KS * j);
+      fw[h] = *reinterpret_cast<const i32x4*>(buf + 16 * ((4 * h + q) ^ (r & 7)) + r * KS);
     }
     wait_lds();
     asm volatile("" ::: "memory");
@@ -302,8 +303,7 @@ __global__ __launch_bounds__(256) void k_i8_token(I8Args a, const u32x4* __restr
   auto multiply = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < NN; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h][j], fx[h], acc[j], 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h], fx[h], acc, 0, 0, 0);
     buf = buf + STAGE == ring + ST * STAGE ? ring : buf + STAGE;
   };
   for (int st = 0; st < mine - ST; ++st) {
@@ -322,20 +322,17 @@ __global__ __launch_bounds__(256) void k_i8_token(I8Args a, const u32x4* __restr
     read(max(mine - ST, 0) + j);
     multiply();
   }
-  if (r == 0) {
-#pragma unroll
-    for (int j = 0; j < NN; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) red[wv][16 * j + 4 * q + k] = acc[j][k];
-  }
+  if (r == 0) *reinterpret_cast<i32x4*>(&red[wv][4 * q]) = acc;
   __syncthreads();
   const int n = i0 + (int)threadIdx.x;
   if ((int)threadIdx.x >= COLS || n >= a.n) return;
   float v[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int tc = threadIdx.x + 16 * p;
-    const int sum = (red[0][tc] + red[1][tc]) + (red[2][tc] + red[3][tc]);
+    const int tc = threadIdx.x + 8 * p;
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) sum += red[w][tc];
     v[p] = (float)sum * (rs.stored * a.w_scale[((size_t)t.e * P + p) * a.n + n]);
   }
   const float y = P == 2 ? swiglu_f(v[0], v[P - 1]) : v[0];
@@ -344,16 +341,16 @@ __global__ __launch_bounds__(256) void k_i8_token(I8Args a, const u32x4* __restr
 
 bool i8_token_ok(const void* x, int dtype, int k) {
   const int n = dtype == MOE_DTYPE_F32 ? 4 : 8;  // elements of 16 bytes
-  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && k <= 256 * kTokenChunks * n - KS;
+  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && k <= kTokenBytes / 16 * n - KS;
 }
 
 template <int DT>
 static void token_dt(const I8Args& a, const void* x, int max_tiles, hipStream_t s) {
-  const int tiles_n = (a.n * (a.swiglu ? 2 : 1) + 31) / 32;
-  const dim3 grid(tiles_n * max_tiles), block(256);
+  const int tiles_n = (a.n * (a.swiglu ? 2 : 1) + 15) / 16;
+  const dim3 grid(tiles_n * max_tiles), block(512);
   const u32x4* xv = static_cast<const u32x4*>(x);
-  if (a.swiglu) hipLaunchKernelGGL((k_i8_token<DT, 2>), grid, block, 0, s, a, xv, tiles_n);
-  else hipLaunchKernelGGL((k_i8_token<DT, 1>), grid, block, 0, s, a, xv, tiles_n);
+  if (a.swiglu) hipLaunchKernelGGL((k_i8_token<DT, 2, 8, 3>), grid, block, 0, s, a, xv, tiles_n);
+  else hipLaunchKernelGGL((k_i8_token<DT, 1, 8, 3>), grid, block, 0, s, a, xv, tiles_n);
 }
 
 hipError_t launch_i8_token(const I8Args& a, const void* x, int dtype, int max_tiles, hipStream_t s) {
@@ -775,11 +772,19 @@ static void tile_launch(const I8Args& a, int max_tiles, int parts, hipStream_t s
   }
 }
 
+// 32 matrix rows a workgroup, or 16 where all those have a CU to themselves (8 rows,
+// SwiGLU of 2 x 1536, K 7168: 6.7 us for 8.7; 37 rows, N 1536, 288 of them: 9.3 for 8.2).
 static void stream_launch(const I8Args& a, int max_tiles, hipStream_t s) {
-  const int tiles_n = (a.n * (a.swiglu ? 2 : 1) + 31) / 32;
-  const dim3 grid(tiles_n * max_tiles), block(256);
-  if (a.swiglu) hipLaunchKernelGGL((k_i8_stream<2, 2, 4, 3>), grid, block, 0, s, a, tiles_n);
-  else hipLaunchKernelGGL((k_i8_stream<2, 1, 4, 3>), grid, block, 0, s, a, tiles_n);
+  const int rows = a.n * (a.swiglu ? 2 : 1), halves = (rows + 15) / 16;
+  const dim3 block(256);
+  if (halves * max_tiles <= 256) {
+    if (a.swiglu) hipLaunchKernelGGL((k_i8_stream<1, 2, 4, 3>), dim3(halves * max_tiles), block, 0, s, a, halves);
+    else hipLaunchKernelGGL((k_i8_stream<1, 1, 4, 3>), dim3(halves * max_tiles), block, 0, s, a, halves);
+    return;
+  }
+  const int tiles_n = (rows + 31) / 32;
+  if (a.swiglu) hipLaunchKernelGGL((k_i8_stream<2, 2, 4, 2>), dim3(tiles_n * max_tiles), block, 0, s, a, tiles_n);
+  else hipLaunchKernelGGL((k_i8_stream<2, 1, 4, 2>), dim3(tiles_n * max_tiles), block, 0, s, a, tiles_n);
 }
 
 // The kernels a product may run on, in the order of I8Plan::kind: 16 rows of x by 32
@@ -791,7 +796,7 @@ struct Tiling {
   double d0, d1;           // dense: us a round, and a stage of a round
   double g0, g1, g2, g3, g4;  // grouped, see i8_plan
 };
-constexpr Tiling kTilings[] = {{16, 32, 512, false, 3.3, 0.105, 3.3, 1.75, 0.235, 0.0, 0.114},
+constexpr Tiling kTilings[] = {{16, 32, 512, false, 3.3, 0.105, 3.9, 0.88, 0.257, 0.0, 0.06},
                                {64, 64, 256, true, 3.0, 0.21, 0.4, 2.9, 0.118, 0.106, 0.422},
                                {64, 128, 256, true, 4.0, 0.30, 0.0, 3.46, 0.173, 0.136, 0.549},
                                {128, 128, 256, true, 4.5, 0.54, 0.0, 4.58, 0.118, 0.379, 0.354},
@@ -810,14 +815,14 @@ constexpr int kStream = 0, kSplit = 1, kTwoToACu = 4;
 // Grouped: each expert's matrix comes from HBM, an expert's rows end anywhere in a tile
 // (half a tile more on average, of which only the rows that there are cost anything).
 // g0 + rounds * (g1 + g2 * stages) + g3 * stages * rounds' worth of rows + g4 * the time to read
-// the matrices at 6.6 TB/s, fitted to 141 products of 4 to 256 experts with 4 to 500
-// rows each, K 768 to 7168: the choice costs 2% over the best kernel on average.  16
+// the matrices at 6.6 TB/s, fitted to 165 products of 4 to 256 experts with 2 to 500
+// rows each, K 768 to 7168: the choice costs 3% over the best kernel on average.  16
 // experts, N 4096, K 4096, 80 rows each: 64 x 64 96 us, 128 x 128 65 (two to a CU: 50), 256 x
-// 256 56; 320 rows: 236, 132, 127, 119.  128 experts of 12 rows, N 2048, K 768: the stream 69
-// us, 128 x 128 39; 32 experts of 8, 2 x 1536, K 7168: 112, 151.
+// 256 56; 320 rows: 236, 132, 127, 119.  128 experts of 12 rows, N 2048, K 768: the stream 53
+// us, 128 x 128 39; 32 experts of 8, 2 x 1536, K 7168: 111, 151.
 // K is split over parts where 64 x 64 tiles leave most CUs without work and the stages saved
-// are worth the 5 us of adding the parts up (64 rows of N 1536, K 7168: 10.4 us in 8
-// parts, 11.5 in one; of 2 x 1536 and 128 rows: 14.6 in 2 parts, 12.9 in one).
+// are worth adding the parts up, 5 us and more (64 rows of N 1536, K 7168: 10.4 us in 8
+// parts, 11.5 in one; 24 rows of N 7168: 14.6 in 2 parts, 12.2 in one).
 I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
   const int P = swiglu ? 2 : 1, stages = (k + KS - 1) / KS, used = !grouped ? 1 : rows < experts ? rows : experts;
   const double per = (double)rows / used, read = (double)used * n * P * k / 6.6e6;
@@ -846,7 +851,7 @@ I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu) {
         parts = (int)(224.0 / tiles);
         if (parts > kMaxParts) parts = kMaxParts;
         if (parts > stages / 6) parts = stages / 6;
-        const double saved = parts > 1 ? m.d1 * (stages - stages / parts) - 5.0 : 0.0;
+        const double saved = parts > 1 ? m.d1 * (stages - stages / parts) - 8.0 : 0.0;
         if (saved <= 0.0) parts = 1;
         else time -= saved;
       }
