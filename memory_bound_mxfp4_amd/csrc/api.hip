@@ -505,7 +505,7 @@ moe_status gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const floa
   a.y_dtype = y_dtype;
   a.num_experts = 1;
   a.x_div = 1;
-  if (m == 1 && x_dtype != MOE_DTYPE_I8 && i8_token_ok(x, x_dtype, k))
+  if (m == 1 && x_dtype != MOE_DTYPE_I8 && i8_token_ok(x, x_dtype, k, n, a.swiglu, 1))
     return launch_i8_token(a, x, x_dtype, 1, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
   st = i8_inputs(a, plan, x, x_dtype, x_stride, x_scale, m, k, ws, ws_bytes, s);
   if (st != MOE_OK) return st;
@@ -570,7 +570,7 @@ moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
   a.num_experts = num_experts;
   a.x_div = (size_t)x_rows == slots ? 1 : top_k;
   a.order = reinterpret_cast<const int32_t*>(gp);
-  if (x_rows == 1 && x_dtype != MOE_DTYPE_I8 && i8_token_ok(x, x_dtype, k)) {
+  if (x_rows == 1 && x_dtype != MOE_DTYPE_I8 && i8_token_ok(x, x_dtype, k, n, a.swiglu, g.max_tiles[0])) {
     a.num_tiles = reinterpret_cast<const int32_t*>(gp + g.counts);
     a.tiles = reinterpret_cast<const int2*>(gp + g.tiles[0]);
     return launch_i8_token(a, x, x_dtype, g.max_tiles[0], s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;

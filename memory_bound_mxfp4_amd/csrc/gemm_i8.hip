@@ -217,6 +217,7 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
 // 4 waves with 32 rows 12.0), N 1536 6.6 (8.7), N 65536 73 (6.4 TB/s).  Grouped: every
 // slot reads this row.
 constexpr int kTokenBytes = 32768;  // of x at most
+constexpr size_t kMaxGroups = ((size_t)1 << 31) / 512;  // workgroups of a launch: its threads, and numbers in int
 
 template <int DT, int P, int NW, int ST>
 __global__ __launch_bounds__(64 * NW) void k_i8_token(I8Args a, const u32x4* __restrict__ x, int tiles_n) {
@@ -339,9 +340,10 @@ __global__ __launch_bounds__(64 * NW) void k_i8_token(I8Args a, const u32x4* __r
   for (int i = 0; i < t.rows; ++i) store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + i) * a.n + n, y);
 }
 
-bool i8_token_ok(const void* x, int dtype, int k) {
-  const int n = dtype == MOE_DTYPE_F32 ? 4 : 8;  // elements of 16 bytes
-  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && k <= kTokenBytes / 16 * n - KS;
+bool i8_token_ok(const void* x, int dtype, int k, int n, bool swiglu, int max_tiles) {
+  const int per = dtype == MOE_DTYPE_F32 ? 4 : 8;  // elements of 16 bytes
+  const size_t groups = ((size_t)n * (swiglu ? 2 : 1) + 15) / 16 * max_tiles;
+  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && k <= kTokenBytes / 16 * per - KS && groups < kMaxGroups;
 }
 
 template <int DT>
@@ -874,7 +876,7 @@ static void tiles_launch(const I8Args& a, const I8Plan& plan, int max_tiles, hip
 
 bool i8_launchable(const I8Plan& plan, int n, bool swiglu, int max_tiles) {
   const size_t bn = kTilings[plan.kind].bn, cols = ((size_t)n * (swiglu ? 2 : 1) + bn - 1) / bn;
-  return cols * max_tiles * plan.parts < ((size_t)1 << 31) / 512;  // threads of a launch, and ids in int
+  return cols * max_tiles * plan.parts < kMaxGroups;
 }
 
 hipError_t launch_gemm_i8(const I8Args& a, const I8Plan& plan, int max_tiles, hipStream_t s) {

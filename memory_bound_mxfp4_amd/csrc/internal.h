@@ -160,7 +160,7 @@ struct I8Plan {
 I8Plan i8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu);
 // A product of one float row that the kernel quantises itself, on the tiles of
 // 16 positions; i8_token_ok: the rows it takes.
-bool i8_token_ok(const void* x, int dtype, int k);
+bool i8_token_ok(const void* x, int dtype, int k, int n, bool swiglu, int max_tiles);
 hipError_t launch_i8_token(const I8Args& a, const void* x, int dtype, int max_tiles, hipStream_t s);
 // Whether the launch of a plan stays inside the size of a grid.
 bool i8_launchable(const I8Plan& plan, int n, bool swiglu, int max_tiles);

@@ -601,3 +601,23 @@ def test_experts_tiles(tokens, top_k, E, n, k, swiglu):
             else:
                 want = product(rows, w[e], ws[e]).cpu().numpy()
                 _close(got, want, ref.product_bound(want, out))
+
+
+def test_experts_of_one_token_with_the_widest_matrices():
+    """More workgroups than the launch of a single row holds: the rows go the way of several."""
+    import torch
+    E, top_k, n, k = 40, 64, 1 << 20, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.randint(-127, 128, (E, 2, n, k), generator=g, dtype=torch.int8, device="cuda")
+    ws = torch.rand(E, 2, n, generator=g, device="cuda") * 1e-2 + 1e-3
+    x, v = _x(1, k, "bf16", 3)
+    idx = (torch.arange(top_k, dtype=torch.int32, device="cuda") * 7 % (E + 1) - 1)[None]
+    y = moe.experts_gemm_i8(x, moe.moe_group_slots(idx, E), w, ws, swiglu=True, out_dtype=torch.float32)
+    codes, scales = ref.quant(v)
+    at = torch.tensor([0, 1, 15, 16, 4095, n // 2 + 3, n - 17, n - 1], device="cuda")
+    for j, e in enumerate(idx[0].tolist()):
+        if e < 0:
+            assert bool((y[j] == 0).all())
+            continue
+        a, b = (ref.product(codes, scales, w[e, i, at].cpu().numpy(), ws[e, i, at].cpu().numpy()) for i in range(2))
+        _close(y[j, at][None], ref.silu(a) * b, ref.swiglu_bound(a, b, "f32"))
