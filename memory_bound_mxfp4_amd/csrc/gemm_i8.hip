@@ -93,7 +93,7 @@ __device__ __forceinline__ void meet() {
 // buffers of its own: no barrier until their int32 sums meet at the end, and a
 // buffer is loaded again as soon as its fragments are in registers.
 // N 7168, K 7168, 8 rows: 10.2 us (5 TB/s, 2.5 us of it start and end); N 65536: 72 us
-// (6.5 TB/s); 8 tokens with 16 of 128 experts each, 2 x 1024, K 7168: 91 us (6.4 TB/s).
+// (6.5 TB/s); 8 tokens with 16 of 128 experts each, 2 x 1024, K 7168: 91 to 95 us (6.4 TB/s).
 // (Waves that share a buffer and meet at every stage reached 5.2 TB/s.  Two buffers a
 // wave, three workgroups to a CU, are as fast as three for long K and better for
 // short: 128 experts, N 7168, K 1024, 72 us for 86.)

@@ -20,7 +20,7 @@
 // under a bias, or a large k) go the slow way: k rounds over all experts.
 //
 // A long call is bound by vector instructions (16384 rows of 896 experts, sigmoid
-// with a bias, top 16: 30 us, 2 TB/s; 766 of them a row, issuing 70% of the time, a
+// with a bias, top 16: 27 us, 2.2 TB/s; 706 of them a row, issuing 70% of the time, a
 // third for the 896 scores and a quarter for the survivors in fp64), a short one by
 // latency (one row of 896: 4.9 us; 4093 rows of 160 in 8 groups: 10 us).
 #include "i8_common.h"
