@@ -343,7 +343,9 @@ moe_status residual_add_rmsnorm_bf16(float* h, const uint16_t* t, int batch, int
  *           g * num_experts / groups on; its worth is the sum of the
  *           group_top (1 or 2; fewer if it has fewer) largest c of its
  *           candidates; the top_groups groups of the largest worth stay
- *           (ties: the lower group; a group without candidates never stays)
+ *           (ties: the lower group; a group without candidates never stays).
+ *           With group_top 1 and no bias the best logits are compared, the
+ *           same order where the scores are told apart
  *   S       = the top_k candidates of the remaining groups by (c descending,
  *             index ascending); without a bias by (l descending, index
  *             ascending), the same order where the scores are told apart

@@ -7,9 +7,9 @@
 //
 // What decides between two experts is compared as the formula's value in
 // fp64: two fp32 scores can tie, or turn round, where the formula does not.
-// But fp64 exponentials of all experts are only computed where a sum of all
-// of them enters the comparison (softmax with a bias) or every expert may
-// count for its group.  Otherwise the selection works on an fp32 key per
+// But fp64 exponentials of all experts are only computed where they enter a
+// comparison: softmax with a bias (their sum), and groups whose worth is more
+// than their best logit.  Otherwise the selection works on an fp32 key per
 // expert: the logit itself without a bias (the scores grow with it), the fp32
 // score + bias with one.  The k-th largest of the lanes' best keys, T, is no
 // better than the k-th best expert (the lanes are disjoint), so only experts
@@ -22,7 +22,8 @@
 // A long call is bound by vector instructions (16384 rows of 896 experts, sigmoid
 // with a bias, top 16: 27 us, 2.2 TB/s; 706 of them a row, issuing 70% of the time, a
 // third for the 896 scores and a quarter for the survivors in fp64), a short one by
-// latency (one row of 896: 4.9 us; 4093 rows of 160 in 8 groups: 10 us).
+// latency (one row of 896: 4.9 us; 4093 rows of 160 in 8 groups by
+// their best: 7.6 us, 9.5 with all exponentials).
 #include "i8_common.h"
 #include "moe_device.h"
 
@@ -125,16 +126,22 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
   }
   float best = LOWEST, top = 0.0f;
   double z = 1.0;
+  // a group's worth is its best score alone: then its best logit decides, and no score is needed
+  const bool by_logit = GROUPED && !bias && p.group_top == 1;
+  double ex[KPL <= 8 ? KPL : 1];  // softmax: the exponentials, where all of them are needed in fp64
   if (softmax) {
 #pragma unroll
     for (int i = 0; i < KPL; ++i) best = fmaxf(best, l[i]);
     const uint32_t m = wave_max_u32(best > LOWEST ? order_key(best) : 0u);
     top = m ? order_value(m) : 0.0f;
-    if (bias || GROUPED) {
+    if (bias || (GROUPED && !by_logit)) {
       double sum = 0.0;
       if constexpr (KPL <= 8) {
 #pragma unroll
-        for (int i = 0; i < KPL; ++i) sum += l[i] > LOWEST ? exp((double)l[i] - (double)top) : 0.0;
+        for (int i = 0; i < KPL; ++i) {
+          ex[i] = l[i] > LOWEST ? exp((double)l[i] - (double)top) : 0.0;
+          sum += ex[i];
+        }
       } else {  // one after the other: unrolled, the exponentials of 16 and more take all registers
 #pragma unroll 1
         for (int at = sub; at < mine; at += L) {
@@ -175,9 +182,14 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
       b2 = fmax(b2, fmin(b1, t));
       b1 = fmax(b1, t);
     };
-    if constexpr (KPL <= 8) {
+    if (by_logit) {
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) take(c[i] >= -__FLT_MAX__ ? score(l[i]) + (bias ? (double)b[i] : 0.0) : NONE);
+      for (int i = 0; i < KPL; ++i) b1 = fmax(b1, (double)c[i]);
+    } else if constexpr (KPL <= 8) {
+      const double rz = 1.0 / z;
+#pragma unroll
+      for (int i = 0; i < KPL; ++i)
+        take(c[i] >= -__FLT_MAX__ ? (softmax ? ex[i] * rz : score(l[i])) + (bias ? (double)b[i] : 0.0) : NONE);
     } else {
 #pragma unroll 1
       for (int at = sub; at < mine; at += L) {
