@@ -151,11 +151,16 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
       }
       z = sum_lanes_f64<64>(sum);
     } else if (!p.renorm) {
-      float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // chains of at most KPL / 4 additions
+      constexpr int CHAINS = KPL > 64 ? 8 : 4;  // of at most 16 additions: with 9 more and two roundings
+      float part[CHAINS] = {};                  // a score, 27 * 2^-24
 #pragma unroll
       for (int i = 0; i < KPL; ++i)
-        if (l[i] > LOWEST) s4[i & 3] += expf(l[i] - top);
-      z = (double)sum_lanes<64>((s4[0] + s4[1]) + (s4[2] + s4[3]));
+        if (l[i] > LOWEST) part[i % CHAINS] += expf(l[i] - top);
+#pragma unroll
+      for (int m = CHAINS / 2; m >= 1; m >>= 1)
+#pragma unroll
+        for (int i = 0; i < m; ++i) part[i] += part[i + m];
+      z = (double)sum_lanes<64>(part[0]);
     }
     if (z == 0.0) z = 1.0;
   }

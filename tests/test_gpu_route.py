@@ -164,3 +164,19 @@ def test_route_long_prompt():
     w = s.gather(1, want)
     w = w / w.sum(1, keepdim=True)
     assert ((gate.double() - w).abs() <= GATE_REL * w).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,groups,top_groups,top_k", [(160, 8, 3, 6), (64, 64, 5, 5), (4092, 33, 4, 16), (4096, 2, 1, 64), (96, 3, 3, 8),
+                                                       (2048, 16, 2, 7)])
+def test_route_groups_by_their_best(E, groups, top_groups, top_k, score, renorm):
+    """Groups ranked by their best logit alone, some of them alike, some without a candidate."""
+    l = _logits(40, E, E + groups)
+    size = E // groups
+    l[3, size:2 * size] = l[3, :size]                # two groups with the same logits
+    l[4, :(groups - 1) * size] = -np.inf             # one group left
+    l[5] = -np.inf                                   # none
+    l[6, ::2] = np.nan
+    l[7] = 1.5                                       # all alike
+    _check(l, top_k=top_k, score=score, groups=groups, top_groups=top_groups, group_top=1, renorm=renorm)
