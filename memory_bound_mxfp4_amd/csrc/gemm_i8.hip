@@ -5,6 +5,7 @@
 #include <type_traits>
 
 #include "i8_common.h"
+#include "tile_order.h"
 
 namespace moe {
 
@@ -505,13 +506,6 @@ __device__ __forceinline__ void tile_end(const I8Args& a, const Tile& t, const i
   else tile_store<MOE_DTYPE_F32, C>(a, t, lds, i0, wm, wn, first, acc);
 }
 
-// Workgroup -> tile.  Workgroups go to the 8 XCDs in turn; each XCD gets one
-// contiguous run of tiles, in bands of `band` tile rows walked column by column,
-// so that the tiles its CUs work on at a time share rows of x and of the
-// matrix in its L2.  A band of 8 in a dense product (both are read again and
-// again); in a grouped one about the tile rows of an expert, so that its rows
-// stay in L2 while its matrix, which nobody else needs, streams by once.
-
 template <class C>
 __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int tiles_m, int parts, int band_rows) {
   constexpr int BM = C::BM, BN = C::BN, WGM = C::WGM, WGN = C::WGN, P = C::P, ST = C::ST, NW = C::NW, MF = C::MF,
@@ -525,14 +519,9 @@ __global__ __launch_bounds__(C::T) void k_i8_tile(I8Args a, int tiles_n, int til
   const int wm = wv % WGM, wn = wv / WGM;
   // a grouped product's grid is sized for the most tiles its slots can make: the
   // XCDs share the ones there are
-  if (a.order) tiles_m = min(tiles_m, a.num_tiles[0]);
-  const int tiles = tiles_n * tiles_m, per_xcd = (tiles * parts + 7) / 8;
-  int id = (int)(blockIdx.x & 7) * per_xcd + (int)(blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per_xcd || id >= tiles * parts) return;
-  const int part = id / tiles;
-  id -= part * tiles;
-  const int band = id / (band_rows * tiles_n), in = id - band * band_rows * tiles_n;
-  const int high = min(band_rows, tiles_m - band * band_rows), tn = in / high, tm = band * band_rows + in - tn * high;
+  const TileAt at = tile_at(blockIdx.x, tiles_n, tiles_m, a.order ? a.num_tiles[0] : tiles_m, parts, band_rows);
+  if (!at.any) return;
+  const int tn = at.tn, tm = at.tm, part = at.part;
   Tile t;
   if (!find_tile<BM>(a, tm, t)) return;
   const int K = a.k, i0 = tn * (BN / P);  // first output column

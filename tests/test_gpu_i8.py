@@ -621,3 +621,29 @@ def test_experts_of_one_token_with_the_widest_matrices():
             continue
         a, b = (ref.product(codes, scales, w[e, i, at].cpu().numpy(), ws[e, i, at].cpu().numpy()) for i in range(2))
         _close(y[j, at][None], ref.silu(a) * b, ref.swiglu_bound(a, b, "f32"))
+
+
+@pytest.mark.parametrize("tokens,n,k", [(20, 1030, 1040), (800, 520, 272), (3000, 1030, 272)])
+def test_experts_of_a_groups_buffer_of_any_content(tokens, n, k):
+    """A buffer that was never filled: the outputs mean nothing, but no other memory is touched, and the next call
+    with slots in it is right."""
+    import torch
+    top_k, E = 2, 40
+    q, s, w, ws, product = _codes_case(tokens, (E, n), k, tokens + n)
+    groups = moe.alloc_slot_groups(tokens, top_k, E)
+    words = groups.buffer.view(torch.int32)
+    y = torch.full((tokens * top_k + 8, n), 5.0, device="cuda")
+    rng = torch.Generator(device="cuda").manual_seed(tokens)
+    for fill in (-1, 0, -1331422904, 0x7FFFFFFF, None):
+        if fill is None:
+            words.copy_(torch.randint(-2 ** 31, 2 ** 31, words.shape, generator=rng, device="cuda").to(torch.int32))
+        else:
+            words.fill_(fill)
+        moe.experts_gemm_i8(q, groups, w, ws, x_scale=s, out=y[4:-4])
+        torch.cuda.synchronize()
+        assert bool((y[:4] == 5).all()) and bool((y[-4:] == 5).all())
+    idx = torch.randint(0, E, (tokens, top_k), generator=rng, dtype=torch.int32, device="cuda")
+    got = moe.experts_gemm_i8(q, moe.moe_group_slots(idx, E, groups=groups), w, ws, x_scale=s, out_dtype=torch.float32)
+    slots = (idx.flatten() == 3).nonzero()[:, 0]
+    want = product(slots // top_k, w[3], ws[3]).cpu().numpy()
+    _close(got[slots], want, ref.product_bound(want, "f32"))
