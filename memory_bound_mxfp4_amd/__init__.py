@@ -12,6 +12,7 @@ import ctypes
 import functools
 import os
 from dataclasses import dataclass
+from operator import index as _index
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -385,7 +386,8 @@ class RouteParamsC(ctypes.Structure):
 
 @functools.lru_cache(maxsize=256)
 def _route_params(*fields):
-    """The C struct of a routing, by reference; a decode step routes the same way again and again."""
+    """The C struct of a routing, by reference; a decode step routes the same way again and again. The fields are
+    plain numbers: kept by value, not by the identity of what held them."""
     for v in fields[:-1]:
         _int(v, "a parameter of the routing")
     return ctypes.byref(RouteParamsC(*fields))
@@ -494,7 +496,8 @@ def _launch(what: str, device, stream, *args):
 def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int = 1, top_groups: int = 1,
               group_top: int = 1, renorm: bool = True, scale: float = 1.0, idx=None, gate=None, stream=None):
     """Router logits [rows][E] to experts and gates (moe_route): softmax or sigmoid scores, a bias for the
-    selection, groups of experts, renormalised gates. Returns (idx int32 [rows][k], gate fp32 [rows][k])."""
+    selection, groups of experts, renormalised gates. A scale held in a tensor is read in every call, which waits for
+    the GPU if it is there. Returns (idx int32 [rows][k], gate fp32 [rows][k])."""
     torch = _torch()
     rows, E, stride = _rows(logits, "logits")
     dev = logits.device
@@ -503,7 +506,9 @@ def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int
     code = _dtype_code(logits.dtype, "logits")
     if bias is not None:
         _want(bias, (E,), torch.float32, dev, "bias")
-    p = _route_params(E, top_k, _SCORES[score], groups, top_groups, group_top, int(bool(renorm)), scale)
+    top_k = _index(top_k)
+    p = _route_params(E, top_k, _SCORES[score], _index(groups), _index(top_groups), _index(group_top), int(bool(renorm)),
+                      ctypes.c_float(scale).value + 0.0)  # + 0.0: no -0.0, which is the same key as 0.0
     shape = (rows, top_k)
     idx = _empty(shape, torch.int32, dev, stream) if idx is None else _want(idx, shape, torch.int32, dev, "idx")
     gate = _empty(shape, torch.float32, dev, stream) if gate is None else _want(gate, shape, torch.float32, dev, "gate")

@@ -218,3 +218,49 @@ def test_sizes_past_32_bits():
     ):
         with pytest.raises(ValueError):
             call()
+
+
+def _routed(monkeypatch, **kw):
+    """The parameters that a call of the binding hands to the C interface."""
+    import torch
+    seen = []
+
+    def launch(what, device, stream, *args):
+        p = args[5]._obj
+        seen.append({name: getattr(p, name) for name, _ in p._fields_})
+
+    monkeypatch.setattr(moe, "_launch", launch)
+    args = dict(top_k=2)
+    args.update(kw)
+    moe.moe_route(torch.zeros(4, 16), **args)
+    return seen[0]
+
+
+def test_route_scale_is_read_in_every_call(monkeypatch):
+    """A routed scaling factor held in a tensor (a module's buffer) and changed in place between two calls."""
+    import torch
+    scale = torch.tensor(2.5)
+    assert _routed(monkeypatch, scale=scale)["scale"] == 2.5
+    scale.fill_(1.0)
+    assert _routed(monkeypatch, scale=scale)["scale"] == 1.0
+    assert _routed(monkeypatch, scale=2)["scale"] == 2.0
+    with pytest.raises((TypeError, ValueError)):
+        moe.moe_route(torch.zeros(4, 16), 2, scale="2")
+
+
+def test_route_sizes_are_whole_numbers(monkeypatch):
+    """A float is refused whether or not the same whole number was routed with before, a number of another integer
+    type is taken; a tensor's value is read in every call."""
+    import numpy as np
+    import torch
+    assert _routed(monkeypatch, groups=4, top_groups=2)["groups"] == 4
+    for over in (dict(groups=4.0, top_groups=2), dict(groups=4, top_groups=2.0), dict(groups=4, top_groups=2, group_top=1.0),
+                 dict(groups=4, top_groups=2, top_k=2.0)):
+        with pytest.raises(TypeError):
+            _routed(monkeypatch, **over)
+    got = _routed(monkeypatch, groups=np.int64(4), top_groups=np.int32(2), top_k=np.int64(3))
+    assert (got["groups"], got["top_groups"], got["top_k"]) == (4, 2, 3)
+    groups = torch.tensor(4)
+    assert _routed(monkeypatch, groups=groups, top_groups=2)["groups"] == 4
+    groups.fill_(2)
+    assert _routed(monkeypatch, groups=groups, top_groups=2)["groups"] == 2
