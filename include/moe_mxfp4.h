@@ -333,7 +333,8 @@ moe_status residual_add_rmsnorm_bf16(float* h, const uint16_t* t, int batch, int
  *               logits + r * row_stride elements (row_stride >= num_experts)
  *   bias        fp32 [num_experts] or NULL: added to the scores for the
  *               selection only, never to the gates (a balance bias)
- *   topk_idx    out int32 [rows][top_k]; topk_gate out fp32 [rows][top_k]
+ *   topk_idx    out int32 [rows][top_k]; topk_gate out fp32 [rows][top_k];
+ *               they overlap neither the logits' rows, nor bias, nor each other
  * For row r with logits l, over the candidates: the experts whose logit (and
  * bias) is neither NaN nor -inf (a logit of +inf counts as the largest fp32):
  *   s[e]    = exp(l[e]) / sum_i exp(l[i])  (MOE_SCORE_SOFTMAX)  or
@@ -383,7 +384,8 @@ moe_status moe_route(const void* logits, moe_dtype dtype, size_t row_stride, int
  *   q[m][k]  = the integer nearest to x[m][k] / scale[m] (the exact quotient,
  *              ties to even), within +-127
  *   x        [rows][k] bf16, fp16 or fp32, row m at x + m * x_stride elements
- *   q        out int8 [rows][k]; scale out fp32 [rows]; neither overlaps x
+ *   q        out int8 [rows][k]; scale out fp32 [rows]; neither overlaps the
+ *            rows of x, nor the other
  * A row of zeros (or so small that its scale rounds to 0) has scale 0 and
  * codes 0.  A row that holds a NaN or an infinity has scale NaN and codes 0,
  * so every product of it is NaN.  1 <= rows <= MOE_MAX_ROWS, 1 <= k <= 65536.
@@ -400,10 +402,12 @@ moe_status quant_rows_i8(const void* x, moe_dtype dtype, size_t x_stride, int ro
  *   w         int8 [n][k] codes, w_scale fp32 [n]
  *   swiglu    0, or 1: w is [2][n][k], gate then up, w_scale [2][n], and
  *             y[m][i] = silu(g) * u of the two products g and u
- *   y         out [m][n], bf16, fp16 or fp32 (y_dtype); must not overlap x
+ *   y         out [m][n], bf16, fp16 or fp32 (y_dtype)
  *   ws        workspace of >= gemm_i8_workspace_size(...) bytes, 256-byte
  *             aligned (may be NULL where that is 0).  It needs no
  *             initialisation and holds nothing between calls.
+ * Neither y nor the workspace's gemm_i8_workspace_size(...) bytes overlap the
+ * rows of x, w, either scale or each other.
  * The sum is exact; it is rounded to fp32, multiplied by the two scales and
  * rounded to y_dtype; SwiGLU runs in fp32 on the scaled sums.
  * 1 <= m <= MOE_MAX_ROWS, 1 <= n <= 2^20, k a multiple of 16 in 16 .. 65536;
@@ -429,7 +433,7 @@ moe_status gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const floa
  *                MOE_GROUPS_OFFSETS(tokens, top_k): expert e has order[
  *                offsets[e]] up to order[offsets[e + 1]] exclusive, and
  *                num_experts names the slots without an expert
- *            and lists that experts_gemm_i8 works through.
+ *            and lists that experts_gemm_i8 works through; it does not overlap idx
  * 1 <= tokens, 1 <= top_k <= 64, num_experts <= 4096, tokens * top_k < 2^27.
  * moe_slot_groups_size is 0 outside these limits.
  */
@@ -449,8 +453,8 @@ moe_status moe_group_slots(const int32_t* idx, int tokens, int top_k, int num_ex
  *   w        int8 [num_experts][n][k], w_scale fp32 [num_experts][n]; with
  *            swiglu int8 [num_experts][2][n][k], w_scale [num_experts][2][n]
  *   y        out [tokens * top_k][n]
- * Types, alignments, limits, sums and workspace as gemm_i8;
- * tokens, top_k and num_experts as moe_group_slots.
+ * Types, alignments, limits, overlaps (groups among the inputs), sums and
+ * workspace as gemm_i8; tokens, top_k and num_experts as moe_group_slots.
  */
 size_t experts_gemm_i8_workspace_size(int tokens, int top_k, int num_experts, int x_rows, int n, int k, int swiglu,
                                       moe_dtype x_dtype);
@@ -464,8 +468,8 @@ moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
  *   y         [tokens * top_k][hidden], bf16, fp16 or fp32 (`dtype`)
  *   gate      fp32 [tokens][top_k]
  *   residual  fp32 [tokens][hidden], or NULL for zeros; may be out itself
- *   out       fp32 [tokens][hidden]; overlaps neither y nor, otherwise,
- *             residual
+ *   out       fp32 [tokens][hidden]; overlaps neither y, nor gate, nor
+ *             otherwise residual
  * Summed in fp32, j ascending, then the residual.  1 <= tokens <=
  * MOE_MAX_ROWS, 1 <= top_k <= 64, 1 <= hidden <= 2^20.  Pointers aligned to
  * their element.

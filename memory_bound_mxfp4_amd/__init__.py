@@ -572,7 +572,7 @@ def _workspace(ws, need: int, device, stream):
 def gemm_i8(x, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dtype=None, ws=None, stream=None):
     """y = x w^T in 8-bit integers (gemm_i8): x [m][k] float rows, quantised on the way, or int8 codes with
     x_scale [m]; w int8 [n][k] with w_scale [n], or [2][n][k] and [2][n] with swiglu. Returns y [m][n] in out's
-    type, out_dtype or bfloat16; out must not overlap x."""
+    type, out_dtype or bfloat16; neither out nor ws overlaps an input."""
     m, k, stride, n, code = _i8_operands(x, x_scale, w, w_scale, swiglu, ())
     dev = x.device
     y = _out(out, (m, n), out_dtype, dev, stream)

@@ -381,9 +381,21 @@ static bool float_dtype(moe_dtype t) { return t == MOE_DTYPE_BF16 || t == MOE_DT
 static size_t dtype_bytes(moe_dtype t) { return t == MOE_DTYPE_F32 ? 4 : t == MOE_DTYPE_I8 ? 1 : 2; }
 static constexpr int kMaxI8K = 65536;  // 127 * 128 * k stays inside int32
 static constexpr int kMaxCols = 1 << 20;
+// What is written must not lie over what other workgroups still read.
 static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-  return p < q + b_bytes && q < p + a_bytes;
+  return a && b && p < q + b_bytes && q < p + a_bytes;
+}
+// The same for rows that may lie apart: whether the block touches one of them.
+struct Rows {
+  const void* base;
+  size_t count, bytes, stride;  // bytes of a row, and from one to the next
+};
+static bool overlap(const Rows& r, const void* block, size_t bytes) {
+  if (!overlap(r.base, (r.count - 1) * r.stride + r.bytes, block, bytes)) return false;
+  const uintptr_t b = reinterpret_cast<uintptr_t>(r.base), q = reinterpret_cast<uintptr_t>(block);
+  const size_t first = q < b + r.bytes ? 0 : (q - b - r.bytes) / r.stride + 1;  // row that ends behind the block's start
+  return first < r.count && b + first * r.stride < q + bytes;
 }
 
 moe_status moe_route(const void* logits, moe_dtype dtype, size_t row_stride, int rows, const float* bias,
@@ -400,6 +412,12 @@ moe_status moe_route(const void* logits, moe_dtype dtype, size_t row_stride, int
   if (!aligned(logits, dtype_bytes(dtype)) || !aligned(bias, 4) || !aligned(topk_idx, 4) || !aligned(topk_gate, 4))
     return MOE_ERR_INVALID_ARGUMENT;
   if (p.num_experts > MOE_MAX_EXPERTS || p.groups > 64 || rows > MOE_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+  const size_t es = dtype_bytes(dtype), places = 4 * (size_t)rows * p.top_k;
+  const Rows in{logits, (size_t)rows, p.num_experts * es, row_stride * es};
+  if (overlap(in, topk_idx, places) || overlap(in, topk_gate, places) || overlap(topk_idx, places, topk_gate, places) ||
+      overlap(bias, 4 * (size_t)p.num_experts, topk_idx, places) ||
+      overlap(bias, 4 * (size_t)p.num_experts, topk_gate, places))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (launch_route(logits, dtype, row_stride, rows, bias, p, topk_idx, topk_gate, static_cast<hipStream_t>(stream)) !=
       hipSuccess)
     return MOE_ERR_HIP;
@@ -412,8 +430,10 @@ moe_status quant_rows_i8(const void* x, moe_dtype dtype, size_t x_stride, int ro
     return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(x, dtype_bytes(dtype)) || !aligned(scale, 4)) return MOE_ERR_INVALID_ARGUMENT;
   if (k > kMaxI8K || rows > MOE_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
-  const size_t x_bytes = ((size_t)(rows - 1) * x_stride + k) * dtype_bytes(dtype);
-  if (overlap(x, x_bytes, q, (size_t)rows * k) || overlap(x, x_bytes, scale, 4 * (size_t)rows))
+  const size_t es = dtype_bytes(dtype);
+  const Rows in{x, (size_t)rows, k * es, x_stride * es};
+  if (overlap(in, q, (size_t)rows * k) || overlap(in, scale, 4 * (size_t)rows) ||
+      overlap(q, (size_t)rows * k, scale, 4 * (size_t)rows))
     return MOE_ERR_INVALID_ARGUMENT;
   if (launch_quant_rows(x, dtype, x_stride, rows, k, q, scale, static_cast<hipStream_t>(stream)) != hipSuccess)
     return MOE_ERR_HIP;
@@ -446,10 +466,20 @@ static moe_status check_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
     return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(w, 16) || !aligned(y, 16) || !aligned(w_scale, 4) || !aligned(x_scale, 4)) return MOE_ERR_INVALID_ARGUMENT;
   if (k > kMaxI8K || n > kMaxCols || x_rows > MOE_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
-  if (overlap(x, ((size_t)(x_rows - 1) * x_stride + k) * dtype_bytes(x_dtype), y, y_rows * n * dtype_bytes(y_dtype)))
+  const size_t es = dtype_bytes(x_dtype);
+  if (overlap(Rows{x, (size_t)x_rows, k * es, x_stride * es}, y, y_rows * n * dtype_bytes(y_dtype)))
     return MOE_ERR_INVALID_ARGUMENT;
   return MOE_OK;
 }
+
+// Whether a block that a product writes lies over its matrices, scales or groups.
+static bool over_operands(const I8Args& a, const float* x_scale, int x_rows, const void* groups, size_t groups_bytes,
+                          const void* block, size_t bytes) {
+  const size_t channels = (size_t)a.num_experts * (a.swiglu ? 2 : 1) * a.n;
+  return overlap(a.w, channels * a.k, block, bytes) || overlap(a.w_scale, 4 * channels, block, bytes) ||
+         overlap(x_scale, 4 * (size_t)x_rows, block, bytes) || overlap(groups, groups_bytes, block, bytes);
+}
+static size_t y_bytes(const I8Args& a) { return (size_t)a.rows * a.n * dtype_bytes((moe_dtype)a.y_dtype); }
 
 // Workspace of a product: the codes and scales of rows it quantises, then the
 // sums of a split K.
@@ -459,14 +489,20 @@ static size_t i8_ws_bytes(int x_rows, int k, moe_dtype x_dtype, const I8Plan& pl
 
 // Takes the workspace apart and quantises rows that are not codes already.
 static moe_status i8_inputs(I8Args& a, const I8Plan& plan, const void* x, moe_dtype x_dtype, size_t x_stride,
-                            const float* x_scale, int x_rows, int k, void* ws, size_t ws_bytes, hipStream_t s) {
+                            const float* x_scale, int x_rows, int k, const void* groups, size_t groups_bytes, void* ws,
+                            size_t ws_bytes, hipStream_t s) {
   a.x = static_cast<const int8_t*>(x);
   a.x_stride = x_stride;
   a.x_scale = x_scale;
   const size_t need = i8_ws_bytes(x_rows, k, x_dtype, plan);
-  if (!need) return MOE_OK;
-  if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARGUMENT;
+  if (need && (!ws || !aligned(ws, 256))) return MOE_ERR_INVALID_ARGUMENT;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (over_operands(a, x_scale, x_rows, groups, groups_bytes, a.y, y_bytes(a))) return MOE_ERR_INVALID_ARGUMENT;
+  if (!need) return MOE_OK;
+  const size_t es = dtype_bytes(x_dtype);
+  if (overlap(Rows{x, (size_t)x_rows, k * es, x_stride * es}, ws, need) || overlap(a.y, y_bytes(a), ws, need) ||
+      over_operands(a, x_scale, x_rows, groups, groups_bytes, ws, need))
+    return MOE_ERR_INVALID_ARGUMENT;
   char* p = static_cast<char*>(ws);
   if (x_dtype != MOE_DTYPE_I8) {
     const QuantWs w = quant_ws(p, x_rows, k);
@@ -505,9 +541,11 @@ moe_status gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const floa
   a.y_dtype = y_dtype;
   a.num_experts = 1;
   a.x_div = 1;
-  if (m == 1 && x_dtype != MOE_DTYPE_I8 && i8_token_ok(x, x_dtype, k, n, a.swiglu, 1))
+  if (m == 1 && x_dtype != MOE_DTYPE_I8 && i8_token_ok(x, x_dtype, k, n, a.swiglu, 1)) {
+    if (over_operands(a, nullptr, 1, nullptr, 0, y, y_bytes(a))) return MOE_ERR_INVALID_ARGUMENT;
     return launch_i8_token(a, x, x_dtype, 1, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
-  st = i8_inputs(a, plan, x, x_dtype, x_stride, x_scale, m, k, ws, ws_bytes, s);
+  }
+  st = i8_inputs(a, plan, x, x_dtype, x_stride, x_scale, m, k, nullptr, 0, ws, ws_bytes, s);
   if (st != MOE_OK) return st;
   if (launch_gemm_i8(a, plan, tiles, s) != hipSuccess) return MOE_ERR_HIP;
   return MOE_OK;
@@ -526,7 +564,9 @@ moe_status moe_group_slots(const int32_t* idx, int tokens, int top_k, int num_ex
                            size_t groups_bytes, void* stream) {
   if (!idx || !groups || !aligned(idx, 4) || !aligned(groups, 256) || !slots_ok(tokens, top_k, num_experts))
     return MOE_ERR_INVALID_ARGUMENT;
-  if (groups_bytes < groups_layout(tokens, top_k, num_experts).bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = groups_layout(tokens, top_k, num_experts).bytes;
+  if (groups_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (overlap(idx, 4 * (size_t)tokens * top_k, groups, need)) return MOE_ERR_INVALID_ARGUMENT;
   if (launch_group_slots(idx, tokens, top_k, num_experts, groups, static_cast<hipStream_t>(stream)) != hipSuccess)
     return MOE_ERR_HIP;
   return MOE_OK;
@@ -571,13 +611,14 @@ moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
   a.x_div = (size_t)x_rows == slots ? 1 : top_k;
   a.order = reinterpret_cast<const int32_t*>(gp);
   if (x_rows == 1 && x_dtype != MOE_DTYPE_I8 && i8_token_ok(x, x_dtype, k, n, a.swiglu, g.max_tiles[0])) {
+    if (over_operands(a, nullptr, 1, groups, g.bytes, y, y_bytes(a))) return MOE_ERR_INVALID_ARGUMENT;
     a.num_tiles = reinterpret_cast<const int32_t*>(gp + g.counts);
     a.tiles = reinterpret_cast<const int2*>(gp + g.tiles[0]);
     return launch_i8_token(a, x, x_dtype, g.max_tiles[0], s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
   }
   a.num_tiles = reinterpret_cast<const int32_t*>(gp + g.counts) + map;
   a.tiles = reinterpret_cast<const int2*>(gp + g.tiles[map]);
-  st = i8_inputs(a, plan, x, x_dtype, x_stride, x_scale, x_rows, k, ws, ws_bytes, s);
+  st = i8_inputs(a, plan, x, x_dtype, x_stride, x_scale, x_rows, k, groups, g.bytes, ws, ws_bytes, s);
   if (st != MOE_OK) return st;
   if (launch_gemm_i8(a, plan, g.max_tiles[map], s) != hipSuccess) return MOE_ERR_HIP;
   return MOE_OK;
@@ -592,7 +633,8 @@ moe_status moe_combine(const void* y, moe_dtype dtype, const float* gate, int to
   if (tokens > MOE_MAX_ROWS || hidden > kMaxCols) return MOE_ERR_UNSUPPORTED;
   const size_t bytes = (size_t)tokens * hidden * 4;
   if (overlap(y, (size_t)tokens * top_k * hidden * dtype_bytes(dtype), out, bytes) ||
-      (residual && residual != out && overlap(residual, bytes, out, bytes)))
+      overlap(gate, 4 * (size_t)tokens * top_k, out, bytes) ||
+      (residual != out && overlap(residual, bytes, out, bytes)))
     return MOE_ERR_INVALID_ARGUMENT;
   if (launch_combine(y, dtype, gate, tokens, top_k, hidden, residual, out, static_cast<hipStream_t>(stream)) !=
       hipSuccess)

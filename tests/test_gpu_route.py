@@ -180,3 +180,19 @@ def test_route_groups_by_their_best(E, groups, top_groups, top_k, score, renorm)
     l[6, ::2] = np.nan
     l[7] = 1.5                                       # all alike
     _check(l, top_k=top_k, score=score, groups=groups, top_groups=top_groups, group_top=1, renorm=renorm)
+
+
+def test_route_outputs_between_the_rows():
+    """Outputs that lie in the gap between two rows of logits overlap neither."""
+    import torch
+    l = _logits(2, 64, 8)
+    wide = torch.zeros(2, 100, device="cuda")
+    wide[:, :64] = torch.from_numpy(l).cuda()
+    idx, gate = wide[0, 64:72].view(torch.int32).view(2, 4), wide[0, 72:80].view(2, 4)
+    moe.moe_route(wide[:, :64], 4, idx=idx, gate=gate)
+    want_idx, want_gate = ref.route(l, top_k=4)
+    assert np.array_equal(idx.cpu().numpy(), want_idx)
+    assert np.allclose(gate.cpu().numpy(), want_gate, rtol=GATE_REL, atol=0)
+    assert torch.equal(wide[:, :64].cpu(), torch.from_numpy(l)) and not bool(wide[1, 64:].any())
+    with pytest.raises(moe.MoeError):
+        moe.moe_route(wide[:, :64], 4, idx=wide[0, 60:68].view(torch.int32).view(2, 4), gate=gate)

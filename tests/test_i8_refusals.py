@@ -264,3 +264,62 @@ def test_route_sizes_are_whole_numbers(monkeypatch):
     assert _routed(monkeypatch, groups=groups, top_groups=2)["groups"] == 4
     groups.fill_(2)
     assert _routed(monkeypatch, groups=groups, top_groups=2)["groups"] == 2
+
+
+FAR = dict(x=P(0x100000), w=P(0x200000), ws=P(0x300000), y=P(0x400000), work=P(0x500000))
+
+
+def test_route_outputs_over_inputs():
+    """Rows are read and written by different workgroups."""
+    a = dict(logits=P(0x10000), idx=P(0x20000), gate=P(0x30000), bias=P(0x40000), rows=4, stride=300)  # rows of 1024 bytes
+    end = 0x10000 + 3 * 1200 + 1024
+    for name in ("idx", "gate"):                                            # 4 rows of 8: 128 bytes
+        for at in (0x10000, 0x10000 - 124, end - 4, 0x10000 + 1200 + 512, 0x40000, 0x40000 + 1020, 0x40000 - 124):
+            assert _route(**{**a, name: P(at)}) == INVALID, (name, hex(at))
+    assert _route(**{**a, "idx": P(0x30000 + 124)}) == INVALID
+    assert _route(**{**a, "gate": P(0x20000)}) == INVALID
+
+
+def test_product_outputs_over_inputs():
+    """The output over the matrix, the scales, the workspace or the groups; the workspace over any of them."""
+    need = moe.load().gemm_i8_workspace_size(4, 32, 64, 0, BF16)
+    w_end, s_end = 0x200000 + 32 * 64, 0x300000 + 32 * 4
+    for at in (0x200000, w_end - 16, 0x200000 - 240, 0x300000, s_end - 16, 0x500000, 0x500000 + need - 16, 0x500000 - 240):
+        assert _gemm(**{**FAR, "y": P(at)}) == INVALID, hex(at)
+    for at in (0x100000, 0x100200 - 256, 0x200000, w_end - 256, 0x300000, 0x400000):
+        assert _gemm(**{**FAR, "work": P(at)}) == INVALID, hex(at)
+    codes = {**FAR, "xd": I8, "xs": P(0x600000)}
+    assert _gemm(**{**codes, "y": P(0x600000)}) == INVALID
+    assert _gemm(**{**codes, "y": P(0x600000 - 240)}) == INVALID
+    two = {**FAR, "swiglu": 1}
+    assert _gemm(**{**two, "y": P(w_end + 32 * 64 - 16)}) == INVALID
+    assert _gemm(**{**two, "y": P(s_end + 32 * 4 - 16)}) == INVALID
+    # one row, which needs no workspace
+    assert _gemm(**{**FAR, "m": 1, "y": P(0x200000)}) == INVALID
+    assert _gemm(**{**FAR, "m": 1, "y": P(0x300000)}) == INVALID
+
+    lib = moe.load()
+    need = lib.experts_gemm_i8_workspace_size(4, 2, 8, 4, 32, 64, 0, BF16)
+    groups = lib.moe_slot_groups_size(4, 2, 8)
+    far = {**FAR, "g": P(0x700000), "gb": groups}
+    for at in (0x200000 + 8 * 32 * 64 - 16, 0x300000 + 8 * 32 * 4 - 16, 0x500000 + need - 16, 0x700000, 0x700000 + groups - 16):
+        assert _experts(**{**far, "y": P(at)}) == INVALID, hex(at)
+    for at in (0x200000 + 8 * 32 * 64 - 256, 0x300000 + 8 * 32 * 4 - 256, 0x700000, 0x700000 + groups - 256):
+        assert _experts(**{**far, "work": P(at)}) == INVALID, hex(at)
+    one = {**far, "rows": 1, "tokens": 1}
+    for at in (0x200000, 0x300000, 0x700000):
+        assert _experts(**{**one, "y": P(at)}) == INVALID, hex(at)
+
+
+def test_other_outputs_over_inputs():
+    lib = moe.load()
+    x, q, s = P(0x10000), P(0x20000), P(0x30000)
+    assert lib.quant_rows_i8(x, F32, 64, 4, 64, q, P(0x20000 + 252), None) == INVALID    # 256 codes
+    assert lib.quant_rows_i8(x, F32, 64, 4, 64, q, P(0x20000 - 12), None) == INVALID
+    need = lib.moe_slot_groups_size(4, 2, 8)
+    for at in (0x10000, 0x10000 + need - 4, 0x10000 - 28):                                # 8 slots
+        assert lib.moe_group_slots(P(at), 4, 2, 8, P(0x10000), need, None) == INVALID, hex(at)
+    y, g, r, o = P(0x10000), P(0x20000), P(0x30000), P(0x40000)
+    for at in (0x40000, 0x40000 + 508, 0x40000 - 12):                                     # 2 tokens of 64, gates of 16 bytes
+        assert lib.moe_combine(y, F32, P(at), 2, 2, 64, r, o, None) == INVALID, hex(at)
+        assert lib.moe_combine(y, F32, P(at), 2, 2, 64, o, o, None) == INVALID, hex(at)
