@@ -205,7 +205,7 @@ __global__ __launch_bounds__(64 * NW) void k_i8_stream(I8Args a, int tiles_n) {
       int sum = 0;
 #pragma unroll
       for (int w = 0; w < NW; ++w) sum += red[(w * 16 + m) * (16 * NN) + tc];
-      v[p] = (float)sum * (scales[16 * NN + m] * scales[tc]);
+      v[p] = scaled(sum, scales[16 * NN + m], scales[tc]);
     }
     store_y(a.y, a.y_dtype, (size_t)yr[m] * a.n + i0 + c, P == 2 ? swiglu_f(v[0], v[P - 1]) : v[0]);
   }
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(64 * NW) void k_i8_token(I8Args a, const u32x4* __r
     int sum = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) sum += red[w][tc];
-    v[p] = (float)sum * (rs.stored * a.w_scale[((size_t)t.e * P + p) * a.n + n]);
+    v[p] = scaled(sum, rs.stored, a.w_scale[((size_t)t.e * P + p) * a.n + n]);
   }
   const float y = P == 2 ? swiglu_f(v[0], v[P - 1]) : v[0];
   for (int i = 0; i < t.rows; ++i) store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + i) * a.n + n, y);
@@ -432,7 +432,7 @@ __device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, const
         const f32x4 w = *reinterpret_cast<const f32x4*>(sw + (wn * C::NF + j * P + p) * 16 + 4 * q);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float u = (float)acc[i][j * P + p][c] * (s * w[c]);
+          const float u = scaled(acc[i][j * P + p][c], s, w[c]);
           v[c] = p ? swiglu_f(v[c], u) : u;
         }
       }
@@ -737,7 +737,7 @@ __global__ __launch_bounds__(256) void k_i8_parts(I8Args a, int parts, int tiles
 #pragma unroll
     for (int i = 0; i < kMaxParts; ++i) sum += i < parts ? part[i] : i32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[p][k] = (float)sum[k] * (sx * sw[p * a.n + min(n + k, a.n - 1)]);
+    for (int k = 0; k < 4; ++k) v[p][k] = scaled(sum[k], sx, sw[p * a.n + min(n + k, a.n - 1)]);
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {

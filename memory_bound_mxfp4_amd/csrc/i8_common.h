@@ -76,6 +76,15 @@ __device__ __forceinline__ void store_y(void* y, int dtype, size_t i, float v) {
   else static_cast<float*>(y)[i] = v;
 }
 
+// A sum with its two scales, three roundings.  The scales are not multiplied with each
+// other first: their product may leave fp32's normal numbers where the result does not (a
+// sum of 0 would become NaN, small rows would lose bits).  A sum is a whole number, so
+// sum * w_scale, a multiple of the last bit of w_scale, is exact where it is subnormal, and
+// as |sum| <= 2^30 it overflows for no w_scale up to 2^97.
+__device__ __forceinline__ float scaled(int sum, float x_scale, float w_scale) {
+  return (float)sum * w_scale * x_scale;
+}
+
 // silu(g) * u with the accurate exponential: the result is within a few fp32
 // roundings of the formula for every finite g (exp overflows to inf and the
 // quotient to -0 for very negative g).

@@ -647,3 +647,54 @@ def test_experts_of_a_groups_buffer_of_any_content(tokens, n, k):
     slots = (idx.flatten() == 3).nonzero()[:, 0]
     want = product(slots // top_k, w[3], ws[3]).cpu().numpy()
     _close(got[slots], want, ref.product_bound(want, "f32"))
+
+
+# Sizes of each kernel: one row, few rows, K in parts, 64 x 128, 128 x 128 and 256 x 256 tiles.
+ALL_KERNELS = [(1, 520, 272), (9, 520, 272), (37, 520, 7184), (200, 4100, 272), (1000, 2050, 272), (1500, 7000, 80)]
+
+
+@pytest.mark.parametrize("size", [1e-37, 1e-36, 1e-34, 1e-20, 1e33, 1e36])
+@pytest.mark.parametrize("m,n,k", ALL_KERNELS)
+def test_gemm_of_small_and_large_rows(m, n, k, size):
+    """Rows whose scale times a matrix scale is no normal fp32 number, or whose sums times their scale are none: the
+    outputs are, and stay within the three roundings."""
+    x, v = _x(m, k, "f32", m + n, sigma=size)
+    w, ws = _w((n, k), k)
+    at = np.unique(np.linspace(0, m - 1, 40).astype(int))
+    codes, scales = ref.quant(v[at])
+    want = ref.product(codes, scales, w, ws)
+    y = moe.gemm_i8(x, _dev(w), _dev(ws), out_dtype=ref.torch_dtype("f32"))
+    _close(y[at], want, ref.product_bound(want, "f32"))
+
+
+@pytest.mark.parametrize("m,n,k", ALL_KERNELS)
+def test_gemm_sum_of_zero_under_large_scales(m, n, k):
+    """0 times two finite scales is 0, also where the scales' product overflows."""
+    import torch
+    w, _ = _w((n, k), 5)
+    q = torch.zeros(m, k, dtype=torch.int8, device="cuda")
+    q[-1] = 1
+    for a, b in ((8e35, 500.0), (500.0, 8e35)):
+        xs, ws = torch.full((m,), a, device="cuda"), torch.full((n,), b, device="cuda")
+        y = moe.gemm_i8(q, _dev(w), ws, x_scale=xs, out_dtype=torch.float32)
+        assert not bool(y[:-1].any()) and not bool(y.isnan().any())
+    # the same within a float row: a 1 and a -1 meet matrix rows of ones
+    x = torch.zeros(m, k, device="cuda")
+    x[:, 0], x[:, 1] = 1e38, -1e38
+    y = moe.gemm_i8(x, torch.ones(n, k, dtype=torch.int8, device="cuda"), torch.full((n,), 1e4, device="cuda"),
+                    out_dtype=torch.float32)
+    assert not bool(y.any()) and not bool(y.isnan().any())
+
+
+@pytest.mark.parametrize("size", [1e-36, 1e33])
+@pytest.mark.parametrize("tokens,top_k,E,n,k", [(1, 4, 6, 48, 272), (20, 2, 40, 130, 1040), (3000, 2, 40, 520, 80)])
+def test_experts_of_small_and_large_rows(tokens, top_k, E, n, k, size):
+    x, v = _x(tokens, k, "f32", tokens, sigma=size)
+    w, ws = _w((E, n, k), k)
+    idx = np.random.default_rng(tokens).integers(0, E, (tokens, top_k)).astype(np.int32)
+    y = moe.experts_gemm_i8(x, moe.moe_group_slots(_dev(idx), E), _dev(w), _dev(ws), out_dtype=ref.torch_dtype("f32"))
+    for s in np.unique(np.linspace(0, tokens * top_k - 1, 60).astype(int)):
+        codes, scales = ref.quant(v[s // top_k][None])
+        e = idx.reshape(-1)[s]
+        want = ref.product(codes, scales, w[e], ws[e])
+        _close(y[int(s)][None], want, ref.product_bound(want, "f32"), s)
