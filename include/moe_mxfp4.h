@@ -410,7 +410,8 @@ moe_status quant_rows_i8(const void* x, moe_dtype dtype, size_t x_stride, int ro
  * rows of x, w, either scale or each other.
  * The sum is exact; it is rounded to fp32, multiplied by w_scale, then by
  * x_scale, a rounding each (so a w_scale up to 2^97 overflows only where the
- * result does), and rounded to y_dtype; SwiGLU runs in fp32 on the scaled sums.
+ * result does), and rounded to y_dtype; SwiGLU runs in fp32 on the scaled sums,
+ * within 11 roundings for every gate, also where exp(-gate) overflows.
  * 1 <= m <= MOE_MAX_ROWS, 1 <= n <= 2^20, k a multiple of 16 in 16 .. 65536;
  * MOE_ERR_UNSUPPORTED also where its tiles make 2^22 workgroups or more (an
  * output of some 10^11 elements, fewer with few rows an expert).  16-byte aligned x

@@ -425,7 +425,11 @@ __device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, const
     if (m - r >= t.rows) break;
     const float s = sx[m];
     const size_t row = (size_t)yr[m] * a.n;
-    auto values = [&](int j) {  // of output fragment j
+    // Gates below -80 are rare: the row is stored as if there were none, and once more if
+    // there are.  (A branch for each value took 8192 rows of 2 x 3584, K 1536 from 122 to
+    // 127.5 us, one for each fragment to 123.4.)
+    float lowest = 0.0f;
+    auto values = [&](int j, auto low) {  // of output fragment j
       f32x4 v;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
@@ -433,7 +437,8 @@ __device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, const
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float u = scaled(acc[i][j * P + p][c], s, w[c]);
-          v[c] = p ? swiglu_f(v[c], u) : u;
+          if (p) lowest = fminf(lowest, v[c]);
+          v[c] = !p ? u : decltype(low)::value ? swiglu_f(v[c], u) : swiglu_rest(v[c], u);
         }
       }
       return v;
@@ -451,25 +456,30 @@ __device__ __forceinline__ void tile_store(const I8Args& a, const Tile& t, const
           }
       }
     };
-    if constexpr (OB == 4) {
+    auto store = [&](auto low) {
+      if constexpr (OB == 4) {
 #pragma unroll
-      for (int j = 0; j < C::NF / P; ++j) put(c0 + 16 * j + 4 * q, __builtin_bit_cast(u32x4, values(j)));
-    } else {
+        for (int j = 0; j < C::NF / P; ++j) put(c0 + 16 * j + 4 * q, __builtin_bit_cast(u32x4, values(j, low)));
+      } else {
 #pragma unroll
-      for (int j = 0; j < C::NF / P; j += 2) {
-        if constexpr (C::NF / P > 1) {
-          const f32x4 v = values(j), w = values(j + 1);
-          put(c0 + 16 * j + 8 * q, join_fragments(u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])},
-                                                  u32x2{pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3])}));
-        } else {  // one fragment only: 8 bytes a lane
-          const f32x4 v = values(j);
-          if (m >= t.rows) continue;
+        for (int j = 0; j < C::NF / P; j += 2) {
+          if constexpr (C::NF / P > 1) {
+            const f32x4 v = values(j, low), w = values(j + 1, low);
+            put(c0 + 16 * j + 8 * q, join_fragments(u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])},
+                                                    u32x2{pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3])}));
+          } else {  // one fragment only: 8 bytes a lane
+            const f32x4 v = values(j, low);
+            if (m >= t.rows) continue;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (c0 + 4 * q + k < a.n) store_y(a.y, DT, row + c0 + 4 * q + k, v[k]);
+            for (int k = 0; k < 4; ++k)
+              if (c0 + 4 * q + k < a.n) store_y(a.y, DT, row + c0 + 4 * q + k, v[k]);
+          }
         }
       }
-    }
+    };
+    store(std::false_type{});
+    if constexpr (P == 2)
+      if (__any(lowest < -80.0f)) store(std::true_type{});
   }
 }
 

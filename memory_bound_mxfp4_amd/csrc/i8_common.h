@@ -86,9 +86,18 @@ __device__ __forceinline__ float scaled(int sum, float x_scale, float w_scale) {
 }
 
 // silu(g) * u with the accurate exponential: the result is within a few fp32
-// roundings of the formula for every finite g (exp overflows to inf and the
-// quotient to -0 for very negative g).
-__device__ __forceinline__ float swiglu_f(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// roundings of the formula for every g and finite u.  Below -80, where exp(-g) may
+// overflow although the result does not vanish, 1 + exp(-g) is exp(-g) to fp32 and
+// g exp(g) is taken in factors: exp(-80), and twice exp((g + 80) / 2), which is a normal
+// number down to -254.  From there on no u leaves more than 0.
+__device__ __forceinline__ float swiglu_low(float g, float u) {
+  g = fmaxf(g, -300.0f);
+  const float t = expf(0.5f * (g + 80.0f));
+  return g * 1.8048513878454153e-35f * u * t * t;
+}
+// Above that.
+__device__ __forceinline__ float swiglu_rest(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+__device__ __forceinline__ float swiglu_f(float g, float u) { return g < -80.0f ? swiglu_low(g, u) : swiglu_rest(g, u); }
 
 // ---- rows to 8-bit codes ---------------------------------------------------------
 //

@@ -649,8 +649,9 @@ def test_experts_of_a_groups_buffer_of_any_content(tokens, n, k):
     _close(got[slots], want, ref.product_bound(want, "f32"))
 
 
-# Sizes of each kernel: one row, few rows, K in parts, 64 x 128, 128 x 128 and 256 x 256 tiles.
-ALL_KERNELS = [(1, 520, 272), (9, 520, 272), (37, 520, 7184), (200, 4100, 272), (1000, 2050, 272), (1500, 7000, 80)]
+# Sizes of each kernel: one row, few rows, 64 x 64 tiles with K in one and in parts, 64 x 128, 128 x 128 and 256 x 256.
+ALL_KERNELS = [(1, 520, 272), (9, 520, 272), (20, 4100, 272), (60, 200, 16400), (200, 4100, 272), (1000, 2050, 272),
+               (1500, 7000, 80)]
 
 
 @pytest.mark.parametrize("size", [1e-37, 1e-36, 1e-34, 1e-20, 1e33, 1e36])
@@ -698,3 +699,33 @@ def test_experts_of_small_and_large_rows(tokens, top_k, E, n, k, size):
         e = idx.reshape(-1)[s]
         want = ref.product(codes, scales, w[e], ws[e])
         _close(y[int(s)][None], want, ref.product_bound(want, "f32"), s)
+
+
+@pytest.mark.parametrize("m,n,k", ALL_KERNELS)
+def test_gemm_swiglu_of_very_negative_gates(m, n, k):
+    """silu(g) * u where exp(-g) overflows fp32 but silu(g), or its product with a large u, does not vanish.  The sums
+    are 1 and the gates and ups the matrix scales themselves, exactly.  Below -80 the kernel takes two factors
+    exp((g + 80) / 2) (2 roundings each, as any exponential), a constant and four products, so 9 roundings; above, an
+    exponential, a sum, a quotient and a product, 5.  Products that end below fp32's normal numbers: half a step each."""
+    import torch
+    g = -np.concatenate([np.linspace(70, 104, 137), [80, 88.7, 88.75, 89, 120, 150, 174, 175, 200, 254, 300, 301, 1e4, 1e38]])
+    u = np.array([1.0, -0.3, 1e-8, 1e10, -1e25, 3e38])
+    g, u = (a.ravel().astype(np.float32) for a in np.meshgrid(g, u))
+    at = np.resize(np.random.default_rng(1).permutation(len(g)), n)
+    g, u = g[at], u[at]
+    w = np.zeros((2, n, k), np.int8)
+    w[0, :, 3], w[1, :, 3] = -1, 1
+    q = torch.zeros(m, k, dtype=torch.int8, device="cuda")
+    q[:, 3] = 1
+    y = moe.gemm_i8(q, _dev(w), _dev(np.stack([-g, u])), x_scale=torch.ones(m, device="cuda"), swiglu=True,
+                    out_dtype=torch.float32)
+    assert torch.equal(y, y[:1].expand(m, n))
+    want = ref.silu(g.astype(np.float64)) * u.astype(np.float64)
+    _close(y[:1], want[None], np.abs(want)[None] * 9 * 2.0 ** -24 * 1.001 + 4 * 2.0 ** -150)
+    # one float row that the kernel quantises itself, and as one expert's row
+    x = torch.zeros(1, k, device="cuda")
+    x[0, 3] = 127.0
+    one = moe.gemm_i8(x, _dev(w), _dev(np.stack([-g, u]) / np.float32(128)), swiglu=True, out_dtype=torch.float32)
+    g, u = (127.0 * (a / np.float32(128)).astype(np.float64) for a in (g, u))
+    want, turn = ref.silu(g) * u, 2 * 2.0 ** -24 * (2 + np.abs(np.minimum(-g, 400)))  # g and u with one rounding each
+    _close(one, want[None], np.abs(want)[None] * (9 * 2.0 ** -24 + turn) * 1.01 + 4 * 2.0 ** -150)
