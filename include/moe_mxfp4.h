@@ -355,8 +355,8 @@ moe_status residual_add_rmsnorm_bf16(float* h, const uint16_t* t, int batch, int
  * index -1, gate 0.  Scores, sums and c are compared in fp64 (or so that the
  * comparison has the same result), so two experts are in the order of the
  * formula also where their fp32 scores would tie.  Gates are rounded once; of a
- * softmax without bias and renormalisation they are within 2^-19, since the
- * sum over all its scores is taken in fp32.
+ * softmax without bias and renormalisation the sum over all its scores is
+ * within 2^-29 of itself before that.
  * 1 <= rows <= MOE_MAX_ROWS, 1 <= top_k <= min(64, top_groups * num_experts / groups),
  * num_experts <= 4096 and a multiple of groups, 1 <= top_groups <= groups <=
  * 64, group_top 1 or 2; groups == 1 needs top_groups == 1; scale finite.  bias

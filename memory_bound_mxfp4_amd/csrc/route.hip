@@ -78,6 +78,27 @@ __device__ __forceinline__ uint32_t kth_largest(uint32_t v, int k, int slack, bo
   return t;
 }
 
+// exp(v - top) for v <= top, a term of a softmax's sum: within 2^-29 of itself down to
+// e^-100, and that instead of anything smaller (also for -inf), which no sum that holds
+// exp(0) can tell.  In fp64, 2^(n + f) with f in -1/2 .. 1/2 and a polynomial of degree 6
+// for 2^f (least largest relative error, fitted in fp64); n goes into the exponent.  The
+// sum in fp32, of accurate fp32 exponentials, left gates twice as far off (5.4e-8 for
+// 2.5e-8 on average) and took up to 8% less (4093 rows of 160: 7.5 us for 7.6; 16384 of 896:
+// 28.6 for 31.1; 4096 of 4096: 58.6 for 57.1).
+__device__ __forceinline__ double exp_below(float v, double top) {
+  constexpr double LOG2E = 1.4426950408889634, MAGIC = 6755399441055744.0;  // 1.5 * 2^52: n in the low bits
+  constexpr double C[7] = {1.0000000005541678,  0.6931472057372635,   0.24022646890631455,   0.05550328776970911,
+                           0.009618488957365078, 0.001339993121735204, 0.00015345811939447112};
+  const double d = fmax((double)v - top, -100.0);
+  const double t = fma(d, LOG2E, MAGIC), f = fma(d, LOG2E, MAGIC - t);
+  double p = C[6];
+#pragma unroll
+  for (int k = 5; k >= 0; --k) p = fma(p, f, C[k]);
+  const uint64_t bits = __builtin_bit_cast(uint64_t, p);
+  const uint32_t hi = (uint32_t)(bits >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, t) << 20);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | (uint32_t)bits);
+}
+
 // GROUPED: L lanes a group; else the row is one group of 64 lanes.
 template <int DT, int KPL, bool GROUPED>
 __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, size_t row_stride, int rows,
@@ -151,16 +172,10 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
       }
       z = sum_lanes_f64<64>(sum);
     } else if (!p.renorm) {
-      constexpr int CHAINS = KPL > 64 ? 8 : 4;  // of at most 16 additions: with 9 more and two roundings
-      float part[CHAINS] = {};                  // a score, 27 * 2^-24
+      double part[4] = {};
 #pragma unroll
-      for (int i = 0; i < KPL; ++i)
-        if (l[i] > LOWEST) part[i % CHAINS] += expf(l[i] - top);
-#pragma unroll
-      for (int m = CHAINS / 2; m >= 1; m >>= 1)
-#pragma unroll
-        for (int i = 0; i < m; ++i) part[i] += part[i + m];
-      z = (double)sum_lanes<64>(part[0]);
+      for (int i = 0; i < KPL; ++i) part[i % 4] += exp_below(l[i], (double)top);
+      z = sum_lanes_f64<64>((part[0] + part[1]) + (part[2] + part[3]));
     }
     if (z == 0.0) z = 1.0;
   }

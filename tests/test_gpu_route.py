@@ -196,3 +196,31 @@ def test_route_outputs_between_the_rows():
     assert torch.equal(wide[:, :64].cpu(), torch.from_numpy(l)) and not bool(wide[1, 64:].any())
     with pytest.raises(moe.MoeError):
         moe.moe_route(wide[:, :64], 4, idx=wide[0, 60:68].view(torch.int32).view(2, 4), gate=gate)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(scale=16.0), dict(groups=8, top_groups=3, group_top=1), dict(groups=8, top_groups=3, group_top=2),
+    dict(bias=True), dict(renorm=True), dict(score="sigmoid")], ids=str)
+@pytest.mark.parametrize("E,dtype", [(160, "bf16"), (896, "f32"), (2048, "f16"), (4096, "f32")])
+def test_route_gates_are_rounded_once(E, dtype, kw):
+    """Scores, their sum and the quotient are taken in 64 bits or close to it (a term of the sum is within 2^-29 of
+    itself): a gate is half a step of fp32 off, and 2^-28 more at most."""
+    import torch
+    kw = dict(kw)
+    kw.setdefault("renorm", False)
+    l = _logits(50, E, E)
+    l[1] = 0.25                             # a sum of E equal terms
+    l[2, ::3] = -np.inf
+    l[3, :] = np.finfo(np.float32).min if dtype == "f32" else -6e4
+    l[4, :5] = 300.0, 299.5, 150.0, 80.0, 0.0
+    l[5, 1:] = -90.0
+    if kw.pop("bias", False):
+        kw["bias"] = _bias(E, 2)
+    lt = torch.from_numpy(l).to(ref.torch_dtype(dtype))
+    want_idx, want = ref.route(lt.float().numpy(), top_k=8, **kw)
+    args = {**kw, "bias": torch.from_numpy(kw["bias"]).cuda()} if "bias" in kw else kw
+    idx, gate = moe.moe_route(lt.cuda(), 8, **args)
+    assert np.array_equal(idx.cpu().numpy(), want_idx)
+    off = np.abs(gate.cpu().numpy().astype(np.float64) - want)
+    bound = (2.0 ** -24 + 2.0 ** -28) * np.abs(want) + 2.0 ** -150
+    assert (off <= bound).all(), (off / bound).max()
