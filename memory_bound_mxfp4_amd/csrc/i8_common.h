@@ -12,6 +12,15 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 namespace moe {
 
+// Between LDS writes of one lane and reads of another lane of the same wave: orders them
+// for the compiler too (the hardware keeps a wave's LDS accesses in order, so this becomes
+// no instruction beyond waits that the reads' results need anyway).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Element i of a bf16, fp16 or fp32 array, widened to fp32 (exact).
 template <int DT>
 __device__ __forceinline__ float load_f32(const void* p, size_t i) {

@@ -286,7 +286,7 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
     list_lb[wv][place] = float2{l[i], bias ? b[i] : 0.0f};
     ++at;
   }
-  __builtin_amdgcn_wave_barrier();
+  wave_sync();
   int e = -1, place = lane;  // without an expert: places from n on stay empty
   double s = 0.0;
   if (n <= 64) {
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
       k64 = bias ? (exact & ~0xFFFull) | (uint64_t)(0xFFF - e) : (exact << 32) | (uint64_t)(0xFFF - e);
     }
     list_k[wv][lane] = k64;
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     int ahead = 0;
     for (int j = 0; j < n; j += 2) {
       typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
@@ -310,9 +310,9 @@ __global__ __launch_bounds__(256) void k_route(const void* __restrict__ logits, 
     }
     if (bias) {
       // two neighbours with the same 52 bits: all of them, then the index, decide
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       if (lane < n) list_k[wv][ahead] = k64;
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       const bool close = lane < n && ahead + 1 < n && (list_k[wv][ahead + 1] >> 12) == (k64 >> 12);
       if (__ballot(close)) {
         ahead = 0;

@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * W) void k_group_slots(const int32_t* __restric
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (b + 64 * i + lane < s1 && (same[i] & ((1ull << lane) - 1)) == 0) mine[key[i]] += __popcll(same[i]);
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
     }
   }
   __syncthreads();
@@ -207,12 +207,12 @@ __global__ __launch_bounds__(64 * W) void k_group_slots(const int32_t* __restric
       const bool in = s < s1;
       const int rank = __popcll(same[i] & ((1ull << lane) - 1));
       const int base = in ? mine[key[i]] : 0;
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       if (in) {
         order[base + rank] = s;
         if (rank == 0) mine[key[i]] = base + __popcll(same[i]);
       }
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
     }
   }
 }
