@@ -649,9 +649,10 @@ def test_experts_of_a_groups_buffer_of_any_content(tokens, n, k):
     _close(got[slots], want, ref.product_bound(want, "f32"))
 
 
-# Sizes of each kernel: one row, few rows, 64 x 64 tiles with K in one and in parts, 64 x 128, 128 x 128 and 256 x 256.
-ALL_KERNELS = [(1, 520, 272), (9, 520, 272), (20, 4100, 272), (60, 200, 16400), (200, 4100, 272), (1000, 2050, 272),
-               (1500, 7000, 80)]
+# Sizes of each kernel, without and with SwiGLU: one row, few rows, 64 x 64 tiles with K in one and in parts, 64 x 128,
+# 128 x 128 (one and two to a CU) and 256 x 256.
+ALL_KERNELS = [(1, 520, 272), (9, 520, 272), (20, 4100, 272), (60, 200, 16400), (200, 4100, 272), (70, 4104, 1152),
+               (1000, 2050, 272), (513, 7000, 272), (1500, 7000, 80)]
 
 
 @pytest.mark.parametrize("size", [1e-37, 1e-36, 1e-34, 1e-20, 1e33, 1e36])
@@ -729,3 +730,36 @@ def test_gemm_swiglu_of_very_negative_gates(m, n, k):
     g, u = (127.0 * (a / np.float32(128)).astype(np.float64) for a in (g, u))
     want, turn = ref.silu(g) * u, 2 * 2.0 ** -24 * (2 + np.abs(np.minimum(-g, 400)))  # g and u with one rounding each
     _close(one, want[None], np.abs(want)[None] * (9 * 2.0 ** -24 + turn) * 1.01 + 4 * 2.0 ** -150)
+
+
+@pytest.mark.parametrize("tokens,hidden,inter", [(1, 512, 256), (7, 256, 128), (150, 256, 144), (700, 256, 272)])
+def test_layer_stage_by_stage(tokens, hidden, inter):
+    """The operators in a row, each against its definition in 64 bits on what the one before it left: every element
+    within the roundings of its own step."""
+    import torch
+    E, k = 16, 4
+    layer = _Layer(tokens, hidden, inter, E, k)
+    logits, x, v, residual = _layer_inputs(tokens, hidden, E, tokens)
+    out = torch.empty(tokens, hidden, device="cuda")
+    layer(_dev(logits), x, _dev(residual), out)
+    idx, gate = ref.route(logits, k, bias=layer.bias.cpu().numpy(), score="sigmoid", groups=4, top_groups=2, group_top=2,
+                          scale=2.5)
+    assert np.array_equal(layer.idx.cpu().numpy(), idx)
+    _close(layer.gate, gate, np.abs(gate) * (2.0 ** -24 + 2.0 ** -40))
+    flat, codes, scales = idx.reshape(-1), *ref.quant(v)
+    h, y = layer.h.double().cpu().numpy(), layer.y.double().cpu().numpy()
+    hc, hs = ref.quant(h)
+    w1, s1, w2, s2 = (t.cpu().numpy() for t in (layer.w1, layer.s1, layer.w2, layer.s2))
+    none = flat < 0
+    assert not h[none].any() and not y[none].any()
+    for e in range(E):
+        slots = np.flatnonzero(flat == e)
+        if not len(slots):
+            continue
+        g, u = (ref.product(codes[slots // k], scales[slots // k], w1[e, p], s1[e, p]) for p in (0, 1))
+        _close(layer.h[torch.from_numpy(slots).cuda()], ref.silu(g) * u, ref.swiglu_bound(g, u, "bf16"), ("h", e))
+        want = ref.product(hc[slots], hs[slots], w2[e], s2[e])
+        _close(layer.y[torch.from_numpy(slots).cuda()], want, ref.product_bound(want, "bf16"), ("y", e))
+    terms = layer.gate.double().cpu().numpy()[:, :, None] * y.reshape(tokens, k, hidden)
+    # k multiplications with an addition, each rounded once, and the residual's addition
+    _close(out, residual + terms.sum(1), (k + 1) * 2.0 ** -24 * 1.01 * (np.abs(terms).sum(1) + np.abs(residual)))
