@@ -94,7 +94,7 @@ __device__ __forceinline__ void meet() {
 // buffers of its own: no barrier until their int32 sums meet at the end, and a
 // buffer is loaded again as soon as its fragments are in registers.
 // N 7168, K 7168, 8 rows: 10.2 us (5 TB/s, 2.5 us of it start and end); N 65536: 72 us
-// (6.5 TB/s); 8 tokens with 16 of 128 experts each, 2 x 1024, K 7168: 91 to 95 us (6.4 TB/s).
+// (6.5 TB/s); 8 tokens with 16 of 128 experts each, 2 x 1024, K 7168: 91 to 97 us (6.4 TB/s).
 // (Waves that share a buffer and meet at every stage reached 5.2 TB/s.  Two buffers a
 // wave, three workgroups to a CU, are as fast as three for long K and better for
 // short: 128 experts, N 7168, K 1024, 72 us for 86.)
@@ -371,9 +371,13 @@ hipError_t launch_i8_token(const I8Args& a, const void* x, int dtype, int max_ti
 // into LDS, before stage k is computed.  (Loads through registers instead, of all or
 // of the matrix alone, took 12% to 20% longer.)
 //
-// 256 x 256 tiles are bound by the matrix units at the clock that the power limit leaves
-// them: 8192 rows, N 7168, K 7168 take 375 to 400 us (2.1 to 2.25 POP/s) with random
-// codes, 290 with zeros.  At K 1536 a tile takes 28 us: 19 for its 12 stages, 2 to start, 7 for the
+// 256 x 256 tiles: 8192 rows, N 7168, K 7168 take 338 us back to back on the same random
+// codes (2.5 POP/s), about 370 behind a quantiser with changing inputs, up to 420 under a profiler,
+// and 266 with zeros.  Two bounds lie together, the multiplications of a stage (2048 clocks of the
+// matrix units) and its LDS
+// traffic (192 KB out and 64 KB in, 2048 clocks at 128 bytes); the counters show the matrix
+// units busy for 167 us at 2.4 GHz, and what random codes take more than zeros is the clock
+// that the power limit leaves.  At K 1536 a tile takes 28 us: 19 for its 12 stages, 2 to start, 7 for the
 // outputs.  (One workgroup a CU that goes from tile to tile, loading the first
 // stage of the next one ahead: 8% slower, its waves wait for their own stores.)
 // The smaller tiles are bound by the latency of a stage, loads to LDS, barrier, LDS to
@@ -812,7 +816,9 @@ constexpr int kStream = 0, kSplit = 1, kTwoToACu = 4;
 // buffers of a stage each) are for more than one round of single ones (four buffers).
 // Measured at N 7168, K 7168: 8 rows 10.2 us (64 x 64 tiles 12.0), 24 rows 18.4 (12.4); 128 rows:
 // 64 x 64 15.8 us, 64 x 128 20.4, 128 x 128 30.8; 500 rows: 55, 41, 37, 256 x 256 68; 2048 rows: 191,
-// 145, 136 (two to a CU: 108), 86.
+// 145, 136 (two to a CU: 108), 86.  Over 110 products of 17 to 4096 rows, N 128 to 8192, K 128 to
+// 8192 the choice costs 1.6% over the best kernel on average and 9% in the worst tenth: short K
+// with some 30 to 200 rows, where the stream would take 1 to 2 us less (97 rows, 2 x 268, K 176: 6.0 us, 4.0).
 // Grouped: each expert's matrix comes from HBM, an expert's rows end anywhere in a tile
 // (half a tile more on average, of which only the rows that there are cost anything).
 // g0 + rounds * (g1 + g2 * stages) + g3 * stages * rounds' worth of rows + g4 * the time to read

@@ -8,7 +8,8 @@
 // What decides between two experts is compared as the formula's value in
 // fp64: two fp32 scores can tie, or turn round, where the formula does not.
 // But fp64 exponentials of all experts are only computed where they enter a
-// comparison: softmax with a bias (their sum), and groups whose worth is more
+// comparison or a gate: softmax with a bias or without renormalisation (their sum; a short
+// form of them in the latter), and groups whose worth is more
 // than their best logit.  Otherwise the selection works on an fp32 key per
 // expert: the logit itself without a bias (the scores grow with it), the fp32
 // score + bias with one.  The k-th largest of the lanes' best keys, T, is no
@@ -16,14 +17,17 @@
 // with keys >= T (with a bias: T less what fp32 may be off) can be among the
 // best k: about 20 of 896 at k 16.  They move to one lane each, get their
 // exact 64-bit key there, and are ranked against each other.  Ties in a
-// logit are cut by index already at T.  More than 64 survivors (equal scores
-// under a bias, or a large k) go the slow way: k rounds over all experts.
+// logit are cut by index already at T.  More than 64 survivors go the slow way: k rounds
+// over all experts, with a bias an exponential of each in every round.  That takes equal
+// scores under a bias, a top_k above about 36, or groups that leave fewer lanes than top_k
+// (then T is 0).  4096 rows of 896: top 48 255 us, 557 with a bias and sigmoid, top 64 338 us; of
+// 1024 in 8 groups, 4 kept, top 32: 192 and 427 us (16384 rows of 896, top 16: 26 us).
 //
-// A long call is bound by vector instructions (16384 rows of 896 experts, sigmoid
-// with a bias, top 16: 27 us, 2.2 TB/s; 706 of them a row, issuing 70% of the time, a
+// A long call of the usual kind is bound by vector instructions (16384 rows of 896 experts,
+// sigmoid with a bias, top 16: 26 us, 2.3 TB/s; 706 of them a row, issuing 70% of the time, a
 // third for the 896 scores and a quarter for the survivors in fp64), a short one by
-// latency (one row of 896: 4.9 us; 4093 rows of 160 in 8 groups by
-// their best: 7.6 us, 9.5 with all exponentials).
+// latency (one row of 896: 5.0 us; 4093 rows of 160 in 8 groups by
+// their best: 7.3 us).
 #include "i8_common.h"
 #include "moe_device.h"
 
