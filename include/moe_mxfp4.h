@@ -72,7 +72,7 @@ typedef enum {
   MOE_ERR_HIP = -4                  /* a HIP runtime call or launch failed     */
 } moe_status;
 
-typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_I8 = 3 } moe_dtype;
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_I8 = 3, MOE_DTYPE_F8 = 4 } moe_dtype;
 
 /* Largest batch (activation rows) of the decode-layer, router_topk, MXFP4,
  * norm and bf16 entry points.  moe_route and the 8-bit entry points below
@@ -81,8 +81,8 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1, MOE_DTYPE_F16 = 2, MOE_DTY
 /* Largest top_k and number of experts the router/top-k kernels accept. */
 #define MOE_MAX_TOPK 64
 #define MOE_MAX_EXPERTS 4096
-/* Largest number of rows (tokens) moe_route, quant_rows_i8, gemm_i8 and
- * moe_combine accept: 2^24 - 1. */
+/* Largest number of rows (tokens) moe_route, the 8-bit entry points, the norms
+ * with an output in 8 bits and moe_combine accept: 2^24 - 1. */
 #define MOE_MAX_ROWS 0xFFFFFF
 
 /* Layout of the experts buffer (moe_layer_weights.expert_layout). */
@@ -464,6 +464,112 @@ moe_status experts_gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, co
                            const void* groups, size_t groups_bytes, int tokens, int top_k, int num_experts,
                            const int8_t* w, const float* w_scale, int n, int swiglu, void* y, moe_dtype y_dtype,
                            void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 8-bit floating-point products.  Codes are E4M3 (OCP 8-bit floating point: 4 exponent bits,
+ * 3 behind the leading one, largest 448, no infinities, 0x7F and 0xFF NaN).
+ * Activations have an fp32 scale for each row and block of 128 consecutive k,
+ * weights one for each block of 128 rows by 128 k; the last block of a row,
+ * or of a matrix's rows, may be shorter.
+ *
+ * quant_rows_f8 -- rows to E4M3 codes with a scale for each block:
+ *   scale[b][m] = fp32( max_{k in block b} |x[m][k]| / 448 )
+ *   q[m][k]     = the E4M3 number nearest to x[m][k] / scale[b][m] (the exact
+ *                 quotient, ties to even), within +-448
+ *   x        [rows][k] bf16, fp16 or fp32, row m at x + m * x_stride elements
+ *   q        out E4M3 [rows][k]; scale out fp32 [ceil(k / 128)][rows], the
+ *            blocks outermost; neither overlaps the rows of x, nor the other
+ * A block of zeros (or so small that its scale rounds to 0) has scale 0 and
+ * codes 0.  A block that holds a NaN or an infinity has scale NaN and codes
+ * 0, so every product of its row is NaN.
+ * 1 <= rows <= MOE_MAX_ROWS, 1 <= k <= 65536.
+ */
+moe_status quant_rows_f8(const void* x, moe_dtype dtype, size_t x_stride, int rows, int k, uint8_t* q, float* scale,
+                         void* stream);
+
+/*
+ * gemm_f8 -- y[m][n] = sum_b (x_scale[b][m] * w_scale[n / 128][b]) *
+ *                            sum_{k in block b} xq[m][k] * w[n][k]
+ *   x         x_dtype MOE_DTYPE_F8: the codes xq, with x_scale fp32
+ *             [ceil(k / 128)][m]; bf16, fp16 or fp32: rows that the call
+ *             quantises as quant_rows_f8 does, x_scale NULL
+ *             row i at x + i * x_stride elements, x_stride >= k
+ *   w         E4M3 [n][k] codes, w_scale fp32 [ceil(n / 128)][ceil(k / 128)]
+ *   swiglu    0, or 1: w is [2][n][k], gate then up, w_scale [2][..][..], and
+ *             y[m][i] = silu(g) * u of the two products g and u
+ *   y         out [m][n], bf16, fp16 or fp32 (y_dtype)
+ *   ws        workspace of >= gemm_f8_workspace_size(...) bytes, 256-byte
+ *             aligned (may be NULL where that is 0).  It needs no
+ *             initialisation and holds nothing between calls.
+ * Neither y nor the workspace's gemm_f8_workspace_size(...) bytes overlap the
+ * rows of x, w, either scale or each other.
+ * The products of a block are summed in fp32 by the matrix units, each block's
+ * sum is multiplied by fp32(x_scale * w_scale) and added in fp32; SwiGLU runs in
+ * fp32 on the two sums.  The order of the blocks is fixed for given sizes and
+ * types.  A block's two scales should have a product among fp32's normal
+ * numbers (that of two scales above 2^-63 has); below that it loses bits.
+ * 1 <= m <= MOE_MAX_ROWS, 1 <= n <= 2^20, k a multiple of 16 in 16 .. 65536;
+ * MOE_ERR_UNSUPPORTED also where its tiles make 2^22 workgroups or more (an
+ * output of some 10^10 elements, fewer with few rows an expert).  16-byte aligned x
+ * (x_stride a multiple of 16) if it is E4M3, else aligned to its element; w
+ * and y 16-byte aligned.
+ */
+size_t gemm_f8_workspace_size(int m, int n, int k, int swiglu, moe_dtype x_dtype);
+moe_status gemm_f8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int m, int k,
+                   const uint8_t* w, const float* w_scale, int n, int swiglu, void* y, moe_dtype y_dtype, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * experts_gemm_f8 -- gemm_f8 of every slot with its own expert's matrix:
+ *   y[s] = product of x[r] with w[expert of slot s];  zeros for a slot
+ *   without an expert
+ *   x_rows   tokens (row r = s / top_k: FC1) or tokens * top_k (row r = s:
+ *            FC2); with top_k 1 the two are the same
+ *   groups   as moe_group_slots left it for the same tokens, top_k and
+ *            num_experts
+ *   w        E4M3 [num_experts][n][k], w_scale fp32 [num_experts][ceil(n / 128)]
+ *            [ceil(k / 128)]; with swiglu [num_experts][2][...] both
+ *   x_scale  fp32 [ceil(k / 128)][x_rows]
+ *   y        out [tokens * top_k][n]
+ * Types, alignments, limits, overlaps (groups among the inputs), sums and
+ * workspace as gemm_f8; tokens, top_k and num_experts as moe_group_slots.
+ */
+size_t experts_gemm_f8_workspace_size(int tokens, int top_k, int num_experts, int x_rows, int n, int k, int swiglu,
+                                      moe_dtype x_dtype);
+moe_status experts_gemm_f8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int x_rows, int k,
+                           const void* groups, size_t groups_bytes, int tokens, int top_k, int num_experts,
+                           const uint8_t* w, const float* w_scale, int n, int swiglu, void* y, moe_dtype y_dtype,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * residual_add_rmsnorm_f8, residual_add_rmsnorm_i8 -- the residual's addition
+ * and the norm in front of the 8-bit products, as one launch:
+ *   g[m][i] = fp32( h[m][i] + t[m][i] )
+ *   v[m][i] = g[m][i] / sqrt( mean_i(g[m][i]^2) + eps ) * gain[i]
+ *   q, scale = codes and scales of v as quant_rows_f8 (quant_rows_i8) defines them
+ *   h        fp32 [rows][hidden], row m at h + m * h_stride elements
+ *   t        [rows][hidden] bf16, fp16 or fp32 (t_dtype), row m at t + m *
+ *            t_stride elements; NULL: g = h (t_dtype and t_stride are not read)
+ *   gain     fp32 [hidden], or NULL for ones
+ *   h_out    out fp32 [rows][hidden], g; may be h itself (its rows one after
+ *            another); NULL with t, and only then
+ *   out      out bf16 [rows][hidden], v rounded to fp32 and then to bf16, or NULL
+ *   q        out E4M3 (int8) [rows][hidden]
+ *   scale    out fp32 [ceil(hidden / 128)][rows] (i8: [rows])
+ * v is not rounded before it is quantised: the mean and v are computed in
+ * fp64.  A row that holds a NaN or an infinity, or is zero where eps is 0,
+ * has every scale NaN, codes 0 and out NaN; so has a block (i8: a row) whose
+ * gain is not finite or whose scale is beyond fp32, where out is as the formula has it.
+ * What is written overlaps neither what is read nor one another, but for h_out.
+ * 1 <= rows <= MOE_MAX_ROWS, 1 <= hidden <= 65536, eps finite and not
+ * negative.  Pointers aligned to their element.
+ */
+moe_status residual_add_rmsnorm_f8(const float* h, size_t h_stride, const void* t, moe_dtype t_dtype, size_t t_stride,
+                                   const float* gain, int rows, int hidden, float eps, float* h_out, uint16_t* out,
+                                   uint8_t* q, float* scale, void* stream);
+moe_status residual_add_rmsnorm_i8(const float* h, size_t h_stride, const void* t, moe_dtype t_dtype, size_t t_stride,
+                                   const float* gain, int rows, int hidden, float eps, float* h_out, uint16_t* out,
+                                   int8_t* q, float* scale, void* stream);
 
 /*
  * moe_combine -- out[t][h] = residual[t][h] + sum_j gate[t][j] * y[t*top_k + j][h]

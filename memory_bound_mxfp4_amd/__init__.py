@@ -19,7 +19,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_mxfp4.so")
 
 MOE_OK, MOE_ERR_INVALID_ARGUMENT, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_HIP = 0, -1, -2, -3, -4
-MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_DTYPE_F16, MOE_DTYPE_I8 = 0, 1, 2, 3
+MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_DTYPE_F16, MOE_DTYPE_I8, MOE_DTYPE_F8 = 0, 1, 2, 3, 4
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_EXPERTS_CANONICAL, MOE_EXPERTS_PACKED = 0, 1
 MAX_BATCH = 64
@@ -32,7 +32,9 @@ EXPORTS = ("moe_expert_bytes", "moe_workspace_size", "moe_router_workspace_size"
            "moe_workspace_status", "moe_stream_read_probe", "moe_decode_layer_noalloc", "moe_decode_layer_mxfp8",
            "moe_prefetch", "moe_set_max_workgroups", "moe_status_string", "moe_route", "quant_rows_i8",
            "gemm_i8_workspace_size", "gemm_i8", "moe_slot_groups_size", "moe_group_slots",
-           "experts_gemm_i8_workspace_size", "experts_gemm_i8", "moe_combine")
+           "experts_gemm_i8_workspace_size", "experts_gemm_i8", "moe_combine", "quant_rows_f8", "gemm_f8_workspace_size",
+           "gemm_f8", "experts_gemm_f8_workspace_size", "experts_gemm_f8", "residual_add_rmsnorm_f8",
+           "residual_add_rmsnorm_i8")
 
 
 class MoeError(RuntimeError):
@@ -95,6 +97,13 @@ def load():
         "experts_gemm_i8_workspace_size": (Z, [I, I, I, I, I, I, I, I]),
         "experts_gemm_i8": (I, [P, I, Z, P, I, I, P, Z, I, I, I, P, P, I, I, P, I, P, Z, P]),
         "moe_combine": (I, [P, I, P, I, I, I, P, P, P]),
+        "quant_rows_f8": (I, [P, I, Z, I, I, P, P, P]),
+        "gemm_f8_workspace_size": (Z, [I, I, I, I, I]),
+        "gemm_f8": (I, [P, I, Z, P, I, I, P, P, I, I, P, I, P, Z, P]),
+        "experts_gemm_f8_workspace_size": (Z, [I, I, I, I, I, I, I, I]),
+        "experts_gemm_f8": (I, [P, I, Z, P, I, I, P, Z, I, I, I, P, P, I, I, P, I, P, Z, P]),
+        "residual_add_rmsnorm_f8": (I, [P, Z, P, I, Z, P, I, I, F, P, P, P, P, P]),
+        "residual_add_rmsnorm_i8": (I, [P, Z, P, I, Z, P, I, I, F, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -671,3 +680,143 @@ def moe_combine(y, gate, residual=None, out=None, stream=None):
     _launch("moe_combine", dev, stream, _addr(y), _dtype_code(y.dtype, "y"), _addr(gate), tokens, top_k, hidden,
             _addr(residual), _addr(out))
     return out
+
+
+# ---- 8-bit floating point: e4m3 codes with a scale for each block of 128 -----------------------------------------------
+
+BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _f8_code(dtype) -> int:
+    return MOE_DTYPE_F8 if dtype == _torch().float8_e4m3fn else _dtype_code(dtype, "x")
+
+
+def quant_rows_f8(x, q=None, scale=None, stream=None):
+    """Rows of x [rows][k] to e4m3 codes with a scale for each block of 128 (quant_rows_f8). Returns (q float8_e4m3fn
+    [rows][k], scale fp32 [ceil(k / 128)][rows])."""
+    rows, k, stride = _rows(x, "x")
+    dev = x.device
+    code = _dtype_code(x.dtype, "x")
+    q, scale = _codes_out(q, scale, rows, k, True, dev, stream)
+    _launch("quant_rows_f8", dev, stream, _addr(x), code, stride, rows, k, _addr(q), _addr(scale))
+    return q, scale
+
+
+def _codes_out(q, scale, rows: int, k: int, f8: bool, device, stream):
+    torch = _torch()
+    dtype = torch.float8_e4m3fn if f8 else torch.int8
+    shape = (_blocks(k), rows) if f8 else (rows,)
+    q = _empty((rows, k), dtype, device, stream) if q is None else _want(q, (rows, k), dtype, device, "q")
+    scale = _empty(shape, torch.float32, device, stream) if scale is None else \
+        _want(scale, shape, torch.float32, device, "scale")
+    return q, scale
+
+
+def _norm_q(what: str, f8: bool, h, t, gain, eps, h_out, out, q, scale, stream):
+    torch = _torch()
+    rows, hidden, stride = _rows(h, "h")
+    dev = h.device
+    if h.dtype != torch.float32:
+        raise ValueError(f"h must be float32, not {h.dtype}")
+    code = t_stride = 0
+    if t is not None:
+        t_rows, t_cols, t_stride = _rows(t, "t")
+        if (t_rows, t_cols) != (rows, hidden) or t.device != dev:
+            raise ValueError(f"t must have the shape of h on its device, not {(t_rows, t_cols)} on {t.device}")
+        code = _dtype_code(t.dtype, "t")
+        h_out = _want(h if h_out is None else h_out, (rows, hidden), torch.float32, dev, "h_out")
+    elif h_out is not None:
+        raise ValueError("h_out goes with t, and only with it")
+    if gain is not None:
+        _want(gain, (hidden,), torch.float32, dev, "gain")
+    if out is not None:
+        _want(out, (rows, hidden), torch.bfloat16, dev, "out")
+    q, scale = _codes_out(q, scale, rows, hidden, f8, dev, stream)
+    _launch(what, dev, stream, _addr(h), stride, _addr(t), code, t_stride, _addr(gain), rows, hidden, float(eps),
+            _addr(h_out), _addr(out), _addr(q), _addr(scale))
+    return q, scale
+
+
+def residual_add_rmsnorm_f8(h, t=None, gain=None, eps: float = 1e-6, h_out=None, out=None, q=None, scale=None,
+                            stream=None):
+    """h + t to h_out (h itself if none is given; without t nothing is added), then RMSNorm of it times gain as e4m3
+    codes with a scale for each block of 128, as one launch (residual_add_rmsnorm_f8); the normalised rows also in
+    bfloat16 to out, if given. Returns (q float8_e4m3fn [rows][hidden], scale fp32 [ceil(hidden / 128)][rows])."""
+    return _norm_q("residual_add_rmsnorm_f8", True, h, t, gain, eps, h_out, out, q, scale, stream)
+
+
+def residual_add_rmsnorm_i8(h, t=None, gain=None, eps: float = 1e-6, h_out=None, out=None, q=None, scale=None,
+                            stream=None):
+    """residual_add_rmsnorm_f8 with int8 codes and one scale a row, as gemm_i8 takes them. Returns (q int8
+    [rows][hidden], scale fp32 [rows])."""
+    return _norm_q("residual_add_rmsnorm_i8", False, h, t, gain, eps, h_out, out, q, scale, stream)
+
+
+def gemm_f8_workspace_size(m: int, n: int, k: int, swiglu: bool, x_dtype) -> int:
+    for v, what in ((m, "m"), (n, "n"), (k, "k")):
+        _int(v, what)
+    return int(load().gemm_f8_workspace_size(m, n, k, int(bool(swiglu)), _f8_code(x_dtype)))
+
+
+def _f8_operands(x, x_scale, w, w_scale, swiglu: bool, lead: tuple):
+    """Shape checks shared by the two products; w is lead + [2][n][k] with swiglu, else lead + [n][k]."""
+    torch = _torch()
+    rows, k, stride = _rows(x, "x")
+    dev = x.device
+    parts = (2,) if swiglu else ()
+    if w.dim() != len(lead) + len(parts) + 2:
+        raise ValueError(f"w has {w.dim()} dimensions, not {len(lead) + len(parts) + 2}")
+    n = _int(w.shape[-2], "the rows of w")
+    _want(w, lead + parts + (n, k), torch.float8_e4m3fn, dev, "w")
+    _want(w_scale, lead + parts + (_blocks(n), _blocks(k)), torch.float32, dev, "w_scale")
+    code = _f8_code(x.dtype)
+    if (x_scale is not None) != (code == MOE_DTYPE_F8):
+        raise ValueError("x_scale goes with float8_e4m3fn rows, and only with them")
+    if x_scale is not None:
+        _want(x_scale, (_blocks(k), rows), torch.float32, dev, "x_scale")
+    return rows, k, stride, n, code
+
+
+def gemm_f8(x, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dtype=None, ws=None, stream=None):
+    """y = x w^T in 8-bit floating point (gemm_f8): x [m][k] float rows, quantised on the way, or float8_e4m3fn codes
+    with x_scale [ceil(k / 128)][m]; w float8_e4m3fn [n][k] with w_scale [ceil(n / 128)][ceil(k / 128)], or [2][..][..]
+    both with swiglu. Returns y [m][n] in out's type, out_dtype or bfloat16; neither out nor ws overlaps an input."""
+    m, k, stride, n, code = _f8_operands(x, x_scale, w, w_scale, swiglu, ())
+    dev = x.device
+    y = _out(out, (m, n), out_dtype, dev, stream)
+    ws = _workspace(ws, 0 if ws is not None else load().gemm_f8_workspace_size(m, n, k, int(bool(swiglu)), code), dev, stream)
+    _launch("gemm_f8", dev, stream, _addr(x), code, stride, _addr(x_scale), m, k, _addr(w), _addr(w_scale), n, int(bool(swiglu)),
+            _addr(y), _dtype_code(y.dtype, "out"), _addr(ws), 0 if ws is None else ws.numel())
+    return y
+
+
+def experts_gemm_f8_workspace_size(groups: SlotGroups, x_rows: int, n: int, k: int, swiglu: bool, x_dtype) -> int:
+    for v, what in ((x_rows, "x_rows"), (n, "n"), (k, "k")):
+        _int(v, what)
+    return int(load().experts_gemm_f8_workspace_size(groups.tokens, groups.top_k, groups.num_experts, x_rows, n, k,
+                                                     int(bool(swiglu)), _f8_code(x_dtype)))
+
+
+def experts_gemm_f8(x, groups: SlotGroups, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dtype=None,
+                    ws=None, stream=None):
+    """gemm_f8 of every slot with its expert's matrix (experts_gemm_f8): x has a row per token or per slot, w is
+    float8_e4m3fn [num_experts][n][k] (or [num_experts][2][n][k] with swiglu). Returns y [tokens * top_k][n]."""
+    E = groups.num_experts
+    rows, k, stride, n, code = _f8_operands(x, x_scale, w, w_scale, swiglu, (E,))
+    dev = x.device
+    if rows != groups.tokens and rows != groups.tokens * groups.top_k:
+        raise ValueError(f"x has {rows} rows, neither the tokens nor the slots of the groups")
+    if groups.buffer.device != dev:
+        raise ValueError("groups are on another device")
+    y = _out(out, (groups.tokens * groups.top_k, n), out_dtype, dev, stream)
+    need = 0 if ws is not None else load().experts_gemm_f8_workspace_size(groups.tokens, groups.top_k, E, rows, n, k,
+                                                                          int(bool(swiglu)), code)
+    ws = _workspace(ws, need, dev, stream)
+    _launch("experts_gemm_f8", dev, stream, _addr(x), code, stride, _addr(x_scale), rows, k, _addr(groups.buffer),
+            groups.buffer.numel(), groups.tokens, groups.top_k, E, _addr(w), _addr(w_scale), n, int(bool(swiglu)), _addr(y),
+            _dtype_code(y.dtype, "out"), _addr(ws), 0 if ws is None else ws.numel())
+    return y

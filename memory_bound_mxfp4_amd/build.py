@@ -8,7 +8,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SO = os.path.join(PKG, "libmoe_mxfp4.so")
 SOURCES = ["api.hip", "router.hip", "experts.hip", "dense.hip", "pack.hip", "layer.hip", "probe.hip",
-           "route.hip", "slots.hip", "quant.hip", "gemm_i8.hip"]
+           "route.hip", "slots.hip", "quant.hip", "gemm_i8.hip", "api_f8.hip", "quant_f8.hip", "norm_q.hip", "gemm_f8.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # Packed fp32 VALU ops are disabled for all device code.  The atomic
 # optimizer is off: it rewrites a one-lane atomic into a wave-wide pattern

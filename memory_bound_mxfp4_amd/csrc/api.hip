@@ -7,6 +7,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "api_common.h"
 #include "internal.h"
 #include "moe_mxfp4.h"
 
@@ -71,8 +72,6 @@ int num_cus() {
 }  // namespace moe
 
 using namespace moe;
-
-static inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 static moe_status check_layer(const moe_layer_weights* w, int batch) {
   if (!w) return MOE_ERR_INVALID_ARGUMENT;
@@ -377,27 +376,6 @@ moe_status residual_add_rmsnorm_bf16(float* h, const uint16_t* t, int batch, int
 
 // ---- routing, slots by expert, 8-bit products -------------------------------
 
-static bool float_dtype(moe_dtype t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32 || t == MOE_DTYPE_F16; }
-static size_t dtype_bytes(moe_dtype t) { return t == MOE_DTYPE_F32 ? 4 : t == MOE_DTYPE_I8 ? 1 : 2; }
-static constexpr int kMaxI8K = 65536;  // 127 * 128 * k stays inside int32
-static constexpr int kMaxCols = 1 << 20;
-// What is written must not lie over what other workgroups still read.
-static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-  return a && b && p < q + b_bytes && q < p + a_bytes;
-}
-// The same for rows that may lie apart: whether the block touches one of them.
-struct Rows {
-  const void* base;
-  size_t count, bytes, stride;  // bytes of a row, and from one to the next
-};
-static bool overlap(const Rows& r, const void* block, size_t bytes) {
-  if (!overlap(r.base, (r.count - 1) * r.stride + r.bytes, block, bytes)) return false;
-  const uintptr_t b = reinterpret_cast<uintptr_t>(r.base), q = reinterpret_cast<uintptr_t>(block);
-  const size_t first = q < b + r.bytes ? 0 : (q - b - r.bytes) / r.stride + 1;  // row that ends behind the block's start
-  return first < r.count && b + first * r.stride < q + bytes;
-}
-
 moe_status moe_route(const void* logits, moe_dtype dtype, size_t row_stride, int rows, const float* bias,
                      const moe_route_params* params, int32_t* topk_idx, float* topk_gate, void* stream) {
   if (!logits || !params || !topk_idx || !topk_gate || !float_dtype(dtype) || rows < 1) return MOE_ERR_INVALID_ARGUMENT;
@@ -549,11 +527,6 @@ moe_status gemm_i8(const void* x, moe_dtype x_dtype, size_t x_stride, const floa
   if (st != MOE_OK) return st;
   if (launch_gemm_i8(a, plan, tiles, s) != hipSuccess) return MOE_ERR_HIP;
   return MOE_OK;
-}
-
-static bool slots_ok(int tokens, int top_k, int num_experts) {
-  return tokens >= 1 && top_k >= 1 && top_k <= MOE_MAX_TOPK && num_experts >= 1 && num_experts <= MOE_MAX_EXPERTS &&
-         (size_t)tokens * top_k < ((size_t)1 << 27);
 }
 
 size_t moe_slot_groups_size(int tokens, int top_k, int num_experts) {

@@ -166,6 +166,48 @@ hipError_t launch_i8_token(const I8Args& a, const void* x, int dtype, int max_ti
 bool i8_launchable(const I8Plan& plan, int n, bool swiglu, int max_tiles);
 hipError_t launch_gemm_i8(const I8Args& a, const I8Plan& plan, int max_tiles, hipStream_t s);
 
+// ---- 8-bit floating point ----
+hipError_t launch_quant_f8(const void* x, int dtype, size_t x_stride, int rows, int K, uint8_t* q, float* scale,
+                           hipStream_t s);
+
+struct NormArgs {
+  const float* h;
+  size_t h_stride;
+  const void* t;  // NULL: nothing is added, and h_out is not written
+  size_t t_stride;
+  const float* gain;  // NULL: ones
+  int rows, row0, hidden;
+  float eps;
+  float* h_out;
+  uint16_t* out;  // the normalised rows in bf16, or NULL
+  void* q;
+  float* scale;
+};
+hipError_t launch_norm_q(const NormArgs& a, int t_dtype, bool f8, hipStream_t s);
+
+struct F8Args {
+  const int8_t* x;
+  size_t x_stride;
+  const float* x_scale;  // [blocks of K][x_rows]
+  int x_rows;
+  int rows, k, n;  // rows: positions of the product (dense rows, or slots)
+  const int8_t* w;
+  const float* w_scale;  // of each matrix [blocks of n][blocks of K]
+  bool swiglu;
+  void* y;
+  int y_dtype;
+  // grouped products; order NULL: dense
+  const int32_t *order, *num_tiles;
+  const int2* tiles;
+  int num_experts, x_div;
+};
+struct F8Plan {
+  int kind, tile_rows;
+};
+F8Plan f8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu);
+bool f8_launchable(const F8Plan& plan, int n, bool swiglu, int max_tiles);
+hipError_t launch_gemm_f8(const F8Args& a, const F8Plan& plan, int max_tiles, hipStream_t s);
+
 int num_cus();
 
 }  // namespace moe
