@@ -104,8 +104,19 @@ static bool over_operands(const F8Args& a, const float* x_scale, int x_rows, con
 }
 static size_t y_bytes(const F8Args& a) { return (size_t)a.rows * a.n * dtype_bytes((moe_dtype)a.y_dtype); }
 
-static size_t f8_ws_bytes(int x_rows, int k, moe_dtype x_dtype, const F8Plan&) {
-  return x_dtype == MOE_DTYPE_F8 ? 0 : quant_ws(nullptr, x_rows, k).bytes;
+// Workspace of a product: the codes and scales of rows it quantises, then the
+// sums of a split K.
+static size_t f8_ws_bytes(int x_rows, int k, moe_dtype x_dtype, const F8Plan& plan) {
+  return (x_dtype == MOE_DTYPE_F8 ? 0 : quant_ws(nullptr, x_rows, k).bytes) + align256(plan.part_bytes);
+}
+// For outputs of any type.
+static size_t f8_ws_size(int rows, int experts, bool grouped, int x_rows, int n, int k, int swiglu, moe_dtype x_dtype) {
+  size_t most = 0;
+  for (int wide = 0; wide < 2; ++wide) {
+    const size_t b = f8_ws_bytes(x_rows, k, x_dtype, f8_plan(rows, experts, grouped, n, k, swiglu != 0, wide != 0));
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 // Takes the workspace apart and quantises rows that are not codes already.
@@ -125,13 +136,16 @@ static moe_status f8_inputs(F8Args& a, const F8Plan& plan, const void* x, moe_dt
   if (overlap(Rows{x, (size_t)x_rows, k * es, x_stride * es}, ws, need) || overlap(a.y, y_bytes(a), ws, need) ||
       over_operands(a, x_scale, x_rows, groups, groups_bytes, ws, need))
     return MOE_ERR_INVALID_ARGUMENT;
+  char* p = static_cast<char*>(ws);
   if (x_dtype != MOE_DTYPE_F8) {
-    const QuantWs w = quant_ws(ws, x_rows, k);
+    const QuantWs w = quant_ws(p, x_rows, k);
     if (launch_quant_f8(x, x_dtype, x_stride, x_rows, k, w.q, w.scale, s) != hipSuccess) return MOE_ERR_HIP;
     a.x = reinterpret_cast<const int8_t*>(w.q);
     a.x_stride = (size_t)k;
     a.x_scale = w.scale;
+    p += w.bytes;
   }
+  a.parts = reinterpret_cast<float*>(p);
   return MOE_OK;
 }
 
@@ -166,7 +180,7 @@ moe_status residual_add_rmsnorm_i8(const float* h, size_t h_stride, const void* 
 
 size_t gemm_f8_workspace_size(int m, int n, int k, int swiglu, moe_dtype x_dtype) {
   if (m < 1 || n < 1 || k < 1 || m > MOE_MAX_ROWS || n > kMaxCols || k > kMaxK) return 0;
-  return f8_ws_bytes(m, k, x_dtype, f8_plan(m, 1, false, n, k, swiglu != 0));
+  return f8_ws_size(m, 1, false, m, n, k, swiglu, x_dtype);
 }
 
 moe_status gemm_f8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int m, int k,
@@ -175,7 +189,7 @@ moe_status gemm_f8(const void* x, moe_dtype x_dtype, size_t x_stride, const floa
   moe_status st = check_f8(x, x_dtype, x_stride, x_scale, m, k, w, w_scale, n, swiglu, y, y_dtype, m);
   if (st != MOE_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const F8Plan plan = f8_plan(m, 1, false, n, k, swiglu != 0);
+  const F8Plan plan = f8_plan(m, 1, false, n, k, swiglu != 0, y_dtype == MOE_DTYPE_F32);
   const int tiles = (m + plan.tile_rows - 1) / plan.tile_rows;
   if (!f8_launchable(plan, n, swiglu != 0, tiles)) return MOE_ERR_UNSUPPORTED;
   F8Args a{};
@@ -189,6 +203,10 @@ moe_status gemm_f8(const void* x, moe_dtype x_dtype, size_t x_stride, const floa
   a.y_dtype = y_dtype;
   a.num_experts = 1;
   a.x_div = 1;
+  if (m == 1 && x_dtype != MOE_DTYPE_F8 && f8_token_ok(x, k, n, a.swiglu, 1)) {
+    if (over_operands(a, nullptr, 1, nullptr, 0, y, y_bytes(a))) return MOE_ERR_INVALID_ARGUMENT;
+    return launch_f8_token(a, x, x_dtype, 1, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  }
   st = f8_inputs(a, plan, x, x_dtype, x_stride, x_scale, m, k, nullptr, 0, ws, ws_bytes, s);
   if (st != MOE_OK) return st;
   return launch_gemm_f8(a, plan, tiles, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
@@ -199,7 +217,7 @@ size_t experts_gemm_f8_workspace_size(int tokens, int top_k, int num_experts, in
   if (!slots_ok(tokens, top_k, num_experts) || x_rows < 1 || n < 1 || k < 1 || x_rows > MOE_MAX_ROWS ||
       n > kMaxCols || k > kMaxK)
     return 0;
-  return f8_ws_bytes(x_rows, k, x_dtype, f8_plan(tokens * top_k, num_experts, true, n, k, swiglu != 0));
+  return f8_ws_size(tokens * top_k, num_experts, true, x_rows, n, k, swiglu, x_dtype);
 }
 
 moe_status experts_gemm_f8(const void* x, moe_dtype x_dtype, size_t x_stride, const float* x_scale, int x_rows, int k,
@@ -215,7 +233,7 @@ moe_status experts_gemm_f8(const void* x, moe_dtype x_dtype, size_t x_stride, co
   const GroupsLayout g = groups_layout(tokens, top_k, num_experts);
   if (groups_bytes < g.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const F8Plan plan = f8_plan((int)slots, num_experts, true, n, k, swiglu != 0);
+  const F8Plan plan = f8_plan((int)slots, num_experts, true, n, k, swiglu != 0, y_dtype == MOE_DTYPE_F32);
   int map = 0;
   while (map + 1 < kTileMaps && kTileRows[map] != plan.tile_rows) ++map;
   if (!f8_launchable(plan, n, swiglu != 0, g.max_tiles[map])) return MOE_ERR_UNSUPPORTED;
@@ -232,6 +250,12 @@ moe_status experts_gemm_f8(const void* x, moe_dtype x_dtype, size_t x_stride, co
   a.num_experts = num_experts;
   a.x_div = (size_t)x_rows == slots ? 1 : top_k;
   a.order = reinterpret_cast<const int32_t*>(gp);
+  if (x_rows == 1 && x_dtype != MOE_DTYPE_F8 && f8_token_ok(x, k, n, a.swiglu, g.max_tiles[0])) {
+    if (over_operands(a, nullptr, 1, groups, g.bytes, y, y_bytes(a))) return MOE_ERR_INVALID_ARGUMENT;
+    a.num_tiles = reinterpret_cast<const int32_t*>(gp + g.counts);
+    a.tiles = reinterpret_cast<const int2*>(gp + g.tiles[0]);
+    return launch_f8_token(a, x, x_dtype, g.max_tiles[0], s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  }
   a.num_tiles = reinterpret_cast<const int32_t*>(gp + g.counts) + map;
   a.tiles = reinterpret_cast<const int2*>(gp + g.tiles[map]);
   st = f8_inputs(a, plan, x, x_dtype, x_stride, x_scale, x_rows, k, groups, g.bytes, ws, ws_bytes, s);

@@ -97,11 +97,12 @@ __device__ __forceinline__ u32x2 f8_quant8(const float* v, const F8Scale& r) {
   return r.zero ? u32x2{0u, 0u} : o;
 }
 
-// The largest over the 16 lanes that hold a block.
+// The largest over the 16 lanes that hold a block, in all of them (rotations within 16 lanes).
 __device__ __forceinline__ uint32_t block_max_bits(uint32_t m) {
-#pragma unroll
-  for (int d = kLanes / 2; d >= 1; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, WAVE));
-  return m;
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x128, 0xF, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x124, 0xF, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x122, 0xF, 0xF, false));
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x121, 0xF, 0xF, false));
 }
 
 // 8 elements of a row from `at` on, fp32; VEC: aligned to 16 bytes and inside the row,

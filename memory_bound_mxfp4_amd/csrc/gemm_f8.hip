@@ -1,25 +1,38 @@
 // gemm_f8.hip -- the 8-bit floating-point products with a scale for each block
 // of 128: y = sum over blocks b of (x_scale[b] * w_scale[b]) * (xq wq^T)_b, for
 // one matrix or for the rows of each expert, with SwiGLU on pairs of matrices.
+//
+// A block of K is a stage of every kernel here: its products are summed by the matrix
+// units from zero, and the sum is scaled and added in fp32 (4 multiply-adds for each matrix
+// instruction, which take half of its time on the vector units).
+#include <type_traits>
+
 #include "f8_common.h"
 #include "tile_device.h"
 #include "tile_order.h"
 
+typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 namespace moe {
 
-// 16 codes to fp16, which holds every e4m3 number.
-struct Wide16 {
-  f16x8 h[2];
+static_assert(KS == kBlock, "a stage is a block");
+
+// 32 codes of a lane, from two 16-byte chunks of a block.
+struct Codes {
+  i32x4 c[2];
 };
-__device__ __forceinline__ Wide16 widen(const i32x4& c) {
-  Wide16 o;
+// The same in fp16, which holds every e4m3 number.
+struct Wide {
+  f16x8 h[4];
+};
+__device__ __forceinline__ Wide widen(const Codes& v) {
+  Wide o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i], 1.0f, false);
-    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i], 1.0f, true);
+  for (int i = 0; i < 8; ++i) {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v.c[i / 4][i % 4], 1.0f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v.c[i / 4][i % 4], 1.0f, true);
     o.h[i / 2][i % 2 * 4] = a[0];
     o.h[i / 2][i % 2 * 4 + 1] = a[1];
     o.h[i / 2][i % 2 * 4 + 2] = b[0];
@@ -28,107 +41,819 @@ __device__ __forceinline__ Wide16 widen(const i32x4& c) {
   return o;
 }
 
-// The products of one block: 16 matrix rows by 16 rows of x over 128 codes of K, summed in
-// fp32.  Both operands hold the same 32 codes of K in a lane, so their order within the
-// block does not matter.  (The matrix units' own 8-bit products are twice as fast, but align the
-// products of 8 neighbouring codes to the largest of them and cut off what is below 2^-13 of it.)
-__device__ __forceinline__ f32x4 mfma_block(const i32x4 (&w)[2], const i32x4 (&x)[2]) {
+// The products of one block: 16 matrix rows by 16 rows of x over 128 codes of K.  Both
+// operands hold the same 32 codes of K in a lane, so their order within the block does
+// not matter.  In fp16 the sum is one of fp32.  The matrix units' own 8-bit products are twice
+// as fast, but align the products of 8 neighbouring codes to the one with the largest exponent and
+// cut off what is below 2^-13 of that (measured: 256 * 256 + 30 gives 65536 + 24), some
+// 3e-5 of a sum of normal values; sums across those groups are fp32's.  So outputs of
+// fp32 are made from fp16, those of 16 bits, whose own rounding is 2^-9 (bf16) or 2^-12
+// (fp16) at least, from codes where time goes by the matrix units.
+__device__ __forceinline__ f32x4 mfma_wide(const Wide& w, const Wide& x) {
   f32x4 c{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const Wide16 a = widen(w[h]), b = widen(x[h]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.h[i], b.h[i], c, 0, 0, 0);
-  }
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.h[i], x.h[i], c, 0, 0, 0);
   return c;
 }
+__device__ __forceinline__ f32x4 mfma_codes(const Codes& w, const Codes& x) {
+  const i32x8 a = __builtin_shufflevector(w.c[0], w.c[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  const i32x8 b = __builtin_shufflevector(x.c[0], x.c[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ void add_scaled(f32x4& acc, float s, const f32x4& v) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) acc[c] = fmaf(s, v[c], acc[c]);
+}
 
-constexpr size_t kMaxGroups = ((size_t)1 << 31) / 512;  // workgroups of a launch: its threads, and numbers in int
+// Lane (row, 16-byte column q) of a fragment in a stage of 128-byte rows: chunks q and
+// 4 + q, each moved to place (chunk ^ row) & 7.
+__device__ __forceinline__ Codes read_codes(const int8_t* rows, int r, int q) {
+  Codes o;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) o.c[h] = *reinterpret_cast<const i32x4*>(rows + r * KS + 16 * ((4 * h + q) ^ (r & 7)));
+  return o;
+}
 
-// 64 rows of x by 64 matrix rows a workgroup of 2 x 2 waves; a block of K at a time through
-// one buffer in LDS.
-template <int P>
-__global__ __launch_bounds__(256) void k_f8_simple(F8Args a, int tiles_n) {
-  constexpr int LD = KS + 16;  // rows apart by 36 banks
-  __shared__ __attribute__((aligned(16))) int8_t lx[64 * LD], lw[64 * LD];
-  __shared__ int yr[64];
+// One wave copies a float from each lane's address to 256 bytes of LDS.
+__device__ __forceinline__ void load_floats_to_lds(const float* src, float* dst) {
+  __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)dst, 4, 0, 0);
+}
+
+// Where the scales of a matrix lie: of expert e, part p (gate, up), block `nb` of its rows.
+__device__ __forceinline__ const float* w_scales(const F8Args& a, int e, int P, int p, int nb) {
+  const int kb = (a.k + kBlock - 1) / kBlock, blocks = (a.n + kBlock - 1) / kBlock;
+  return a.w_scale + (((size_t)e * P + p) * blocks + min(nb, blocks - 1)) * kb;
+}
+
+template <class A>
+__device__ __forceinline__ void zero_rows(const A& a, const Tile& t, int i0, int cols, int threads) {
+  for (int i = threadIdx.x; i < t.rows * cols; i += threads)
+    if (i0 + i % cols < a.n) store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + i / cols) * a.n + i0 + i % cols, 0.0f);
+}
+
+// ---- few rows -------------------------------------------------------------------
+//
+// 16 * NN matrix rows by up to 16 rows of x a workgroup; bound by reading the matrix.  The
+// NW waves take the stages in turn, each through a ring of ST buffers of its own: no
+// barrier until their fp32 sums meet at the end, in the order of the waves.  The codes are
+// widened to fp16: the vector units have the time.  A stage's scales come in one load: lane
+// r brings that of row r of x, lane 16 + p that of part p of the matrix.
+template <int NN, int P, int NW, int ST>
+__global__ __launch_bounds__(64 * NW, 2) void k_f8_stream(F8Args a, int tiles_n) {
+  constexpr int STAGE = (1 + NN) * 16 * KS, D = 2 * (1 + NN), L = D + 1, COLS = 16 * NN / P, T = 64 * NW;
+  static_assert(NN <= 2 && NW * ST * STAGE >= NW * NN * 1024, "stream");
+  __shared__ __attribute__((aligned(1024))) int8_t lds[NW * ST * STAGE];
+  __shared__ __attribute__((aligned(256))) float scales[NW * ST * 64];
+  __shared__ int yr[16];
   Tile t;
-  if (!find_tile<64>(a, blockIdx.x / tiles_n, t)) return;
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4, wv = threadIdx.x >> 6, wm = wv & 1, wn = wv >> 1;
-  const int i0 = blockIdx.x % tiles_n * (64 / P), K = a.k, kb = (K + kBlock - 1) / kBlock, nb = (a.n + kBlock - 1) / kBlock;
+  if (!find_tile<16>(a, blockIdx.x / tiles_n, t)) return;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i0 = blockIdx.x % tiles_n * COLS, K = a.k;
   if (t.e >= a.num_experts) {  // slots without an expert: rows of zeros
-    for (int i = threadIdx.x; i < t.rows * (64 / P); i += 256)
-      if (i0 + i % (64 / P) < a.n) store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + i / (64 / P)) * a.n + i0 + i % (64 / P), 0.0f);
+    zero_rows(a, t, i0, COLS, T);
     return;
   }
-  if (threadIdx.x < 64) yr[threadIdx.x] = y_row(a, t.p0 + min((int)threadIdx.x, t.rows - 1));
+  if (threadIdx.x < 16) yr[threadIdx.x] = y_row(a, t.p0 + min((int)threadIdx.x, t.rows - 1));
   __syncthreads();
-  f32x4 acc[2][2];
+  const int lr = lane >> 3, chunk = (lane ^ lr) & 7;  // lane l of a load brings chunk (l ^ row) & 7 of row l >> 3
+  const int8_t* src[D];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int b = 0; b < kb; ++b) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = threadIdx.x + 256 * i, row = c / 8, k = b * KS + c % 8 * 16;
-      const int p = P == 2 ? row / 16 % 2 : 0, n = min(i0 + (P == 2 ? row / 32 * 16 + row % 16 : row), a.n - 1);
-      i32x4 vx{0, 0, 0, 0}, vw{0, 0, 0, 0};
-      if (k < K) {
-        vx = *reinterpret_cast<const i32x4*>(a.x + (size_t)x_row(a, yr[row]) * a.x_stride + k);
-        vw = *reinterpret_cast<const i32x4*>(a.w + (((size_t)t.e * P + p) * a.n + n) * K + k);
-      }
-      *reinterpret_cast<i32x4*>(lx + row * LD + c % 8 * 16) = vx;
-      *reinterpret_cast<i32x4*>(lw + row * LD + c % 8 * 16) = vw;
+  for (int i = 0; i < D; ++i) {
+    if (i < 2) {
+      src[i] = a.x + (size_t)x_row(a, yr[8 * i + lr]) * a.x_stride;
+    } else {
+      const int gw = 8 * (i - 2), n = min(i0 + gw % COLS + lr, a.n - 1);  // P 2: COLS gate rows, then the up rows
+      src[i] = a.w + (((size_t)t.e * P + gw / COLS) * a.n + n) * K;
     }
-    __syncthreads();
-    i32x4 fx[2][2], fw[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        fx[i][h] = *reinterpret_cast<const i32x4*>(lx + (16 * (2 * wm + i) + r) * LD + 16 * (4 * h + q));
-        fw[i][h] = *reinterpret_cast<const i32x4*>(lw + (16 * (2 * wn + i) + r) * LD + 16 * (4 * h + q));
-      }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float sx = a.x_scale[(size_t)b * a.x_rows + x_row(a, yr[16 * (2 * wm + i) + r])];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float s = sx * a.w_scale[(((size_t)t.e * P + (P == 2 ? j : 0)) * nb + i0 / kBlock) * kb + b];
-        const f32x4 v = mfma_block(fw[j], fx[i]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(s, v[c], acc[i][j][c]);
-      }
-    }
-    __syncthreads();
   }
-  // register c of lane 16 q + r: matrix row 4 q + c of the fragment, row r of x
+  const bool of_x = lane < 16;
+  const float* scale0 = of_x ? a.x_scale + x_row(a, yr[r]) : w_scales(a, t.e, P, min(lane - 16, P - 1), i0 / kBlock);
+  const uint32_t scale_step = of_x ? (uint32_t)a.x_rows : 1u;
+  const int stages = (K + KS - 1) / KS, mine = wv < stages ? (stages - wv + NW - 1) / NW : 0;
+  int8_t* ring = lds + wv * ST * STAGE;
+  float* sring = scales + wv * ST * 64;
+  auto load = [&](int i, int b) {  // this wave's i-th stage to buffer b
+    const int st = wv + NW * i, k = st * KS + 16 * chunk;
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+      const int8_t* p = src[j] + min(k, K - 16);  // past K: zeros times codes that are there
+      if (j < 2) load_to_lds(k < K ? p : kZeroCodes, ring + b * STAGE + 1024 * j);
+      else load_to_lds<true>(p, ring + b * STAGE + 1024 * j);
+    }
+    load_floats_to_lds(scale0 + (size_t)(uint32_t)st * scale_step, sring + 64 * b);
+  };
+#pragma unroll
+  for (int i = 0; i < ST; ++i)
+    if (i < mine) load(i, i);
+  f32x4 acc[NN];
+#pragma unroll
+  for (int j = 0; j < NN; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int b = 0;
+  Codes fw[NN], fx;
+  float sx, sw[NN];
+  auto read = [&]() {
+    const int8_t* buf = ring + b * STAGE;
+    fx = read_codes(buf, r, q);
+    sx = sring[64 * b + r];
+#pragma unroll
+    for (int j = 0; j < NN; ++j) {
+      fw[j] = read_codes(buf + 16 * KS * (1 + j), r, q);
+      // P 2: with one fragment rows 0 .. 7 are the gate's and 8 .. 15 the up matrix's, with two a fragment each
+      sw[j] = sring[64 * b + 16 + (P == 1 ? 0 : NN == 1 ? q / 2 : j)];
+    }
+    wait_lds();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto multiply = [&]() {
+    const Wide x = widen(fx);
+#pragma unroll
+    for (int j = 0; j < NN; ++j) add_scaled(acc[j], sx * sw[j], mfma_wide(widen(fw[j]), x));
+    b = b + 1 == ST ? 0 : b + 1;
+  };
+  // no branch in this loop; then what is left in the ring
+  for (int st = 0; st < mine - ST; ++st) {
+    wait_vm<(ST - 1) * L>();
+    asm volatile("" ::: "memory");
+    read();
+    load(st + ST, b);
+    multiply();
+  }
+  if (mine < ST) wait_vm<0>();
+#pragma unroll
+  for (int j = 0; j < ST; ++j) {
+    if (j >= mine) break;
+    wait_ring<ST, L>(ST - 1 - j);
+    asm volatile("" ::: "memory");
+    read();
+    multiply();
+  }
+  __syncthreads();
+  // register c of lane 16 q + r: matrix row 16 j + 4 q + c, row r of x
+  float* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int j = 0; j < NN; ++j) *reinterpret_cast<f32x4*>(red + (wv * 16 + r) * (16 * NN) + 16 * j + 4 * q) = acc[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < t.rows * COLS; i += T) {
+    const int m = i / COLS, c = i % COLS;
+    if (i0 + c >= a.n) continue;
+    float v[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      v[p] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v[p] += red[(w * 16 + m) * (16 * NN) + COLS * p + c];
+    }
+    store_y(a.y, a.y_dtype, (size_t)yr[m] * a.n + i0 + c, P == 2 ? swiglu_f(v[0], v[P - 1]) : v[0]);
+  }
+}
+
+// One float row of x, quantised on the way: each workgroup makes the row's codes and
+// scales itself while the first stages of its 16 matrix rows travel, which costs less than a
+// launch of its own.  Grouped: every slot reads this row.
+constexpr int kTokenK = 16384;  // the longest row, in whole blocks
+constexpr size_t kMaxGroups = ((size_t)1 << 31) / 512;  // workgroups of a launch: its threads, and numbers in int
+
+template <int DT, int P, int NW, int ST>
+__global__ __launch_bounds__(64 * NW, 2) void k_f8_token(F8Args a, const void* __restrict__ x, int tiles_n) {
+  constexpr int T = 64 * NW, STAGE = 16 * KS, L = 3, COLS = 16 / P, NC = kTokenK / 8 / T;
+  __shared__ __attribute__((aligned(1024))) int8_t lds[NW * ST * STAGE];
+  __shared__ __attribute__((aligned(256))) float scales[NW * ST * 64];
+  __shared__ __attribute__((aligned(16))) u32x2 row[kTokenK / 8];  // the codes of x
+  __shared__ float xs[kTokenK / kBlock];
+  __shared__ __attribute__((aligned(16))) float red[NW][16];
+  Tile t;
+  if (!find_tile<16>(a, blockIdx.x / tiles_n, t)) return;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i0 = blockIdx.x % tiles_n * COLS, K = a.k;
+  if (t.e >= a.num_experts) {
+    zero_rows(a, t, i0, COLS, T);
+    return;
+  }
+  float v[NC][8];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int at = 8 * ((int)threadIdx.x + T * i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    if (at < K) load8<DT, true>(x, at, K, v[i]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  const int lr = lane >> 3, chunk = (lane ^ lr) & 7;
+  const int8_t* src[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int m = 16 * (2 * wm + i) + r;
-    if (m >= t.rows) continue;
+    const int n = min(i0 + (P == 2 ? lr : 8 * i + lr), a.n - 1);  // P 2: 8 gate rows, 8 up rows
+    src[i] = a.w + (((size_t)t.e * P + (P == 2 ? i : 0)) * a.n + n) * K;
+  }
+  const float* scale0 = w_scales(a, t.e, P, P == 2 ? q / 2 : 0, i0 / kBlock);  // the lane's own matrix rows
+  const int stages = (K + KS - 1) / KS, mine = wv < stages ? (stages - wv + NW - 1) / NW : 0;
+  int8_t* ring = lds + wv * ST * STAGE;
+  float* sring = scales + wv * ST * 64;
+  auto load = [&](int i, int b) {  // this wave's i-th stage
+    const int st = wv + NW * i, k = min(st * KS + 16 * chunk, K - 16);
 #pragma unroll
-    for (int j = 0; j < 2 / P; ++j)
+    for (int j = 0; j < 2; ++j) load_to_lds<true>(src[j] + k, ring + b * STAGE + 1024 * j);
+    load_floats_to_lds(scale0 + st, sring + 64 * b);
+  };
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int n = i0 + (P == 2 ? 16 * wn : 16 * (2 * wn + j)) + 4 * q + c;
-        const float v = P == 2 ? swiglu_f(acc[i][0][c], acc[i][1][c]) : acc[i][j][c];
-        if (n < a.n) store_y(a.y, a.y_dtype, (size_t)yr[m] * a.n + n, v);
+  for (int i = 0; i < ST; ++i)
+    if (i < mine) load(i, i);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int at = threadIdx.x + T * i;  // elements past K, up to the end of its block, come out as zeros
+    if (at >= stages * kLanes) break;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+    const F8Scale s = f8_scale(block_max_bits(m));
+    if (at % kLanes == 0) xs[at / kLanes] = s.stored;
+    row[at] = f8_quant8(v[i], s);
+  }
+  wait_lds();
+  meet();
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  int b = 0;
+  Codes fw, fx;
+  float s;
+  auto read = [&](int i) {
+    const int st = wv + NW * i;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)  // the row in all 16 columns
+      fx.c[h] = *reinterpret_cast<const i32x4*>(reinterpret_cast<const int8_t*>(row) + st * KS + 64 * h + 16 * q);
+    fw = read_codes(ring + b * STAGE, r, q);
+    const float sx = xs[st], sw = sring[64 * b + lane];
+    wait_lds();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    s = sx * sw;
+  };
+  auto multiply = [&]() {
+    add_scaled(acc, s, mfma_wide(widen(fw), widen(fx)));
+    b = b + 1 == ST ? 0 : b + 1;
+  };
+  for (int st = 0; st < mine - ST; ++st) {
+    wait_vm<(ST - 1) * L>();
+    asm volatile("" ::: "memory");
+    read(st);
+    load(st + ST, b);
+    multiply();
+  }
+  if (mine < ST) wait_vm<0>();
+#pragma unroll
+  for (int j = 0; j < ST; ++j) {
+    if (j >= mine) break;
+    wait_ring<ST, L>(ST - 1 - j);
+    asm volatile("" ::: "memory");
+    read(max(mine - ST, 0) + j);
+    multiply();
+  }
+  if (r == 0) *reinterpret_cast<f32x4*>(&red[wv][4 * q]) = acc;
+  __syncthreads();
+  const int n = i0 + (int)threadIdx.x;
+  if ((int)threadIdx.x >= COLS || n >= a.n) return;
+  float y[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    y[p] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) y[p] += red[w][threadIdx.x + 8 * p];
+  }
+  const float out = P == 2 ? swiglu_f(y[0], y[P - 1]) : y[0];
+  for (int i = 0; i < t.rows; ++i) store_y(a.y, a.y_dtype, (size_t)y_row(a, t.p0 + i) * a.n + n, out);
+}
+
+bool f8_token_ok(const void* x, int k, int n, bool swiglu, int max_tiles) {
+  const size_t groups = ((size_t)n * (swiglu ? 2 : 1) + 15) / 16 * max_tiles;
+  return reinterpret_cast<uintptr_t>(x) % 16 == 0 && k <= kTokenK && groups < kMaxGroups;
+}
+
+template <int DT>
+static void token_dt(const F8Args& a, const void* x, int max_tiles, hipStream_t s) {
+  const int tiles_n = (a.n * (a.swiglu ? 2 : 1) + 15) / 16;
+  const dim3 grid(tiles_n * max_tiles), block(512);
+  if (a.swiglu) hipLaunchKernelGGL((k_f8_token<DT, 2, 8, 3>), grid, block, 0, s, a, x, tiles_n);
+  else hipLaunchKernelGGL((k_f8_token<DT, 1, 8, 3>), grid, block, 0, s, a, x, tiles_n);
+}
+
+hipError_t launch_f8_token(const F8Args& a, const void* x, int dtype, int max_tiles, hipStream_t s) {
+  if (dtype == MOE_DTYPE_BF16) token_dt<MOE_DTYPE_BF16>(a, x, max_tiles, s);
+  else if (dtype == MOE_DTYPE_F16) token_dt<MOE_DTYPE_F16>(a, x, max_tiles, s);
+  else token_dt<MOE_DTYPE_F32>(a, x, max_tiles, s);
+  return hipGetLastError();
+}
+
+// ---- many rows: tiles through LDS ----------------------------------------------
+//
+// A workgroup computes BM rows of x by BN rows of the matrix (with SwiGLU BN/2
+// gate rows and their BN/2 up rows, alternating by 16).  K runs in
+// stages kept in ST buffers: the loads of stage k + ST - 1 are issued, straight
+// into LDS, before stage k is computed.  Each wave also brings the scales of the rows of x
+// that it multiplies itself, and of its matrix rows, which lie in one block.
+
+// One tile configuration: BM rows of x by BN matrix rows (P matrices
+// interleaved), KG groups of WGM x WGN waves that take the stages in turn, ST
+// buffers of a stage.  WIDE: products in fp16, for outputs of fp32; else in codes.
+template <int BM_, int BN_, int WGM_, int WGN_, int KG_, int P_, int ST_, bool WIDE_>
+struct TileCfg {
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, KG = KG_, P = P_, ST = ST_;
+  static constexpr bool WIDE = WIDE_;
+  static constexpr int NW = WGM * WGN, T = 64 * NW * KG;                     // waves of a group, threads
+  static constexpr int MF = BM / WGM / 16, NF = BN / WGN / 16, MO = MF / KG;  // fragments of a wave, rows of them it stores
+  static constexpr bool SPLIT = BM == 64 && BN == 64;  // K may be split over workgroups
+  static constexpr int STAGE = (BM + BN) * KS, RING = ST * STAGE;
+  static constexpr int SL = MF == 4 ? 2 : 1;           // loads of a stage's scales, 64 floats each
+  static constexpr int SCALES = ST * NW * SL * 64;     // floats
+};
+
+// Stores a wave's sums: its fragment rows from `first` on.  Register
+// c of acc[i][j] of lane 16 q + r: matrix row 16 j + 4 q + c, row 16 i + r of x.
+template <int DT, class C>
+__device__ __forceinline__ void tile_store(const F8Args& a, const Tile& t, const int* yr, int i0, int wm, int wn,
+                                           int first, const f32x4 (&acc)[C::MO][C::NF]) {
+  constexpr int P = C::P, OB = Elem<DT>::bytes, V = 16 / OB;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const bool whole = a.n % V == 0;  // 16-byte stores stay aligned, and a chunk is inside the row or outside
+  const int c0 = i0 + wn * (C::BN / C::WGN / P);
+#pragma unroll
+  for (int i = 0; i < C::MO; ++i) {
+    const int m = 16 * (C::WGM * (first + i) + wm) + r;
+    if (m - r >= t.rows) break;
+    const size_t row = (size_t)yr[m] * a.n;
+    // Gates below -80 are rare: the row is stored as if there were none, and once more if
+    // there are.
+    float lowest = 0.0f;
+    auto values = [&](int j, auto low) {  // of output fragment j
+      f32x4 v = acc[i][j * P];
+      if constexpr (P == 2) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float u = acc[i][j * P + P - 1][c];
+          lowest = fminf(lowest, v[c]);
+          v[c] = decltype(low)::value ? swiglu_f(v[c], u) : swiglu_rest(v[c], u);
+        }
       }
+      return v;
+    };
+    auto put = [&](int c, const u32x4& d) {
+      if (m >= t.rows) return;
+      if (whole) {
+        if (c < a.n) *reinterpret_cast<u32x4*>(static_cast<char*>(a.y) + (row + c) * OB) = d;
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (c + k < a.n) {
+            if constexpr (OB == 4) static_cast<uint32_t*>(a.y)[row + c + k] = d[k];
+            else static_cast<uint16_t*>(a.y)[row + c + k] = (uint16_t)(d[k / 2] >> (k % 2 * 16));
+          }
+      }
+    };
+    auto store = [&](auto low) {
+      if constexpr (OB == 4) {
+#pragma unroll
+        for (int j = 0; j < C::NF / P; ++j) put(c0 + 16 * j + 4 * q, __builtin_bit_cast(u32x4, values(j, low)));
+      } else {
+#pragma unroll
+        for (int j = 0; j < C::NF / P; j += 2) {
+          if constexpr (C::NF / P > 1) {
+            const f32x4 v = values(j, low), w = values(j + 1, low);
+            put(c0 + 16 * j + 8 * q, join_fragments(u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])},
+                                                    u32x2{pack2<DT>(w[0], w[1]), pack2<DT>(w[2], w[3])}));
+          } else {  // one fragment only: 8 bytes a lane
+            const f32x4 v = values(j, low);
+            if (m >= t.rows) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (c0 + 4 * q + k < a.n) store_y(a.y, DT, row + c0 + 4 * q + k, v[k]);
+          }
+        }
+      }
+    };
+    store(std::false_type{});
+    if constexpr (P == 2)
+      if (__any(lowest < -80.0f)) store(std::true_type{});
   }
 }
 
-F8Plan f8_plan(int, int, bool, int, int, bool) { return F8Plan{0, 64}; }
-
-bool f8_launchable(const F8Plan&, int n, bool swiglu, int max_tiles) {
-  return ((size_t)n * (swiglu ? 2 : 1) + 63) / 64 * max_tiles < kMaxGroups;
+// With K split over workgroups: the sums of one part, by position, in rows of
+// all tiles' columns (the matrices interleaved as in the tile).
+template <class C>
+__device__ __forceinline__ void tile_store_part(const F8Args& a, const Tile& t, int tn, int tiles_n, int wm, int wn,
+                                                int part, int first, const f32x4 (&acc)[C::MO][C::NF]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const size_t width = (size_t)tiles_n * C::BN;
+  float* dst = a.parts + ((size_t)part * a.rows + t.p0) * width + tn * C::BN + wn * C::NF * 16 + 4 * q;
+#pragma unroll
+  for (int i = 0; i < C::MO; ++i) {
+    const int m = 16 * (C::WGM * (first + i) + wm) + r;
+    if (m >= t.rows) continue;
+#pragma unroll
+    for (int j = 0; j < C::NF; ++j) *reinterpret_cast<f32x4*>(dst + m * width + 16 * j) = acc[i][j];
+  }
 }
 
-hipError_t launch_gemm_f8(const F8Args& a, const F8Plan&, int max_tiles, hipStream_t s) {
-  const int tiles_n = (a.n * (a.swiglu ? 2 : 1) + 63) / 64;
-  if (a.swiglu) hipLaunchKernelGGL(k_f8_simple<2>, dim3(tiles_n * max_tiles), dim3(256), 0, s, a, tiles_n);
-  else hipLaunchKernelGGL(k_f8_simple<1>, dim3(tiles_n * max_tiles), dim3(256), 0, s, a, tiles_n);
+// The end of a tile: its outputs, or its part of the sums.
+template <class C>
+__device__ __forceinline__ void tile_end(const F8Args& a, const Tile& t, const int* yr, int i0, int tn, int tiles_n,
+                                         int wm, int wn, int parts, int part, int first,
+                                         const f32x4 (&acc)[C::MO][C::NF]) {
+  if constexpr (C::SPLIT) {
+    if (parts > 1) {
+      tile_store_part<C>(a, t, tn, tiles_n, wm, wn, part, first, acc);
+      return;
+    }
+  }
+  if constexpr (C::WIDE) tile_store<MOE_DTYPE_F32, C>(a, t, yr, i0, wm, wn, first, acc);
+  else if (a.y_dtype == MOE_DTYPE_BF16) tile_store<MOE_DTYPE_BF16, C>(a, t, yr, i0, wm, wn, first, acc);
+  else tile_store<MOE_DTYPE_F16, C>(a, t, yr, i0, wm, wn, first, acc);
+}
+
+template <class C>
+__global__ __launch_bounds__(C::T) void k_f8_tile(F8Args a, int tiles_n, int tiles_m, int parts, int band_rows) {
+  constexpr int BM = C::BM, BN = C::BN, WGM = C::WGM, WGN = C::WGN, P = C::P, ST = C::ST, NW = C::NW, MF = C::MF,
+                KG = C::KG, NF = C::NF, GX = BM / 8, L = (BM + BN) / 8 / NW, SL = C::SL;  // L: row loads of a wave and stage
+  constexpr int NH = NF / 2;  // matrix fragments of half a stage's work
+  static_assert(L * 8 * NW == BM + BN && NF % 2 == 0 && ST % KG == 0 && GX == NW * MF && (KG == 1 || NW == 4), "tile");
+  // the ring, then the scales of its stages, then the tile's output rows
+  __shared__ __attribute__((aligned(1024))) int8_t lds[C::RING + 4 * C::SCALES + 4 * BM];
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kg = wave / NW, wv = wave % NW;
+  const int wm = wv % WGM, wn = wv / WGM;
+  // a grouped product's grid is sized for the most tiles its slots can make: the
+  // XCDs share the ones there are
+  const TileAt at = tile_at(blockIdx.x, tiles_n, tiles_m, a.order ? a.num_tiles[0] : tiles_m, parts, band_rows);
+  if (!at.any) return;
+  const int tn = at.tn, tm = at.tm, part = at.part;
+  Tile t;
+  if (!find_tile<BM>(a, tm, t)) return;
+  const int K = a.k, i0 = tn * (BN / P);  // first output column
+  if (t.e >= a.num_experts) {
+    zero_rows(a, t, i0, BN / P, C::T);
+    return;
+  }
+  float* scales = reinterpret_cast<float*>(lds + C::RING);
+  int* yr = reinterpret_cast<int*>(scales + C::SCALES);
+  for (int i = threadIdx.x; i < BM; i += C::T) yr[i] = y_row(a, t.p0 + min(i, t.rows - 1));
+  __syncthreads();
+  // Loads: a wave copies 8 rows x 128 codes at a time; lane l brings chunk
+  // (l ^ row) & 7 of row l >> 3, so that the same 16-byte chunk of 8 consecutive
+  // rows lies in 8 different bank groups when a fragment reads it.
+  const int lr = lane >> 3, chunk = (lane ^ lr) & 7;
+  const int8_t* src[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int g = wv + NW * i;  // group of 8 rows: first those of x, then the matrix's
+    if (g < GX) {
+      src[i] = a.x + (size_t)x_row(a, yr[8 * g + lr]) * a.x_stride;
+    } else {
+      const int gw = 8 * (g - GX);  // first row of the tile's matrix part; P 2: 16 gate rows, 16 up rows, ...
+      const int n = min(i0 + (P == 2 ? gw / 32 * 16 + gw % 16 : gw) + lr, a.n - 1);
+      src[i] = a.w + (((size_t)t.e * P + (P == 2 ? gw / 16 % 2 : 0)) * a.n + n) * K;
+    }
+  }
+  // Scales: lane 16 i + r brings that of row r of the wave's fragment row i, the lanes behind
+  // them (or a load of their own) those of the wave's matrix rows.
+  const int nb = (i0 + wn * (BN / WGN / P)) / kBlock;
+  const bool of_x = lane < 16 * MF;
+  const float* w0 = w_scales(a, t.e, P, P == 2 ? lane & 1 : 0, nb);
+  const float* scale0 = of_x ? a.x_scale + x_row(a, yr[16 * (WGM * (lane >> 4) + wm) + r]) : w0;
+  const uint32_t scale_step = of_x ? (uint32_t)a.x_rows : 1u;
+  float* my_scales = scales + wv * SL * 64;
+  constexpr int SW = SL == 2 ? 64 : 16 * MF;  // where the matrix's scales lie, gate and up in turn
+
+  const int stages = (K + KS - 1) / KS;
+  const int s0 = (int)((size_t)stages * part / parts), S = (int)((size_t)stages * (part + 1) / parts);
+  f32x4 acc[MF][NF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // With U of the MF fragment rows: a tile whose last rows are missing (the end of an
+  // expert) neither loads nor multiplies them.
+  auto run = [&](auto used) {
+    constexpr int U = decltype(used)::value, LU = L - MF + U + SL;
+    auto load_scales = [&](int st, int b) {
+      float* dst = my_scales + b * (NW * SL * 64);
+      load_floats_to_lds(scale0 + (size_t)(uint32_t)st * scale_step, dst);
+      if constexpr (SL == 2) load_floats_to_lds(w0 + st, dst + 64);
+    };
+    auto load_whole = [&](int st, int b) {
+      int8_t* buf = lds + b * C::STAGE;
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        if (i < U || i >= MF) load_to_lds(src[i] + (st * KS + 16 * chunk), buf + 1024 * (wv + NW * i));
+      load_scales(st, b);
+    };
+    auto load = [&](int st, int b) {  // stage st to buffer b
+      if ((st + 1) * KS <= K) {
+        load_whole(st, b);
+      } else {  // the last stage of a K that is no multiple of 128: zeros past K on x's side, the matrix's own codes on the other
+        int8_t* buf = lds + b * C::STAGE;
+        const int k = st * KS + 16 * chunk;
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+          if (i < U || i >= MF)
+            load_to_lds(i < MF && k >= K ? kZeroCodes : src[i] + min(k, K - 16), buf + 1024 * (wv + NW * i));
+        load_scales(st, b);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < ST / KG - 1; ++i)
+      if (s0 + KG * i + kg < S) load(s0 + KG * i + kg, KG * i + kg);
+    Codes fw[NH], fx[U];
+    float sx[U], sw[P];
+    auto read = [&](int b, int half) {
+      const int8_t* bx = lds + b * C::STAGE + 16 * wm * KS;
+      const int8_t* bw = lds + b * C::STAGE + BM * KS + wn * (BN / WGN) * KS;
+      if (half == 0) {
+        const float* sc = my_scales + b * (NW * SL * 64);
+#pragma unroll
+        for (int p = 0; p < P; ++p) sw[p] = sc[SW + p];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          sx[i] = sc[16 * i + r];
+          fx[i] = read_codes(bx + 16 * WGM * KS * i, r, q);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NH; ++j) fw[j] = read_codes(bw + 16 * KS * (half * NH + j), r, q);
+    };
+    auto multiply = [&](int half) {
+      if constexpr (C::WIDE) {
+        Wide x[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) x[i] = widen(fx[i]);
+#pragma unroll
+        for (int j = 0; j < NH; ++j) {
+          const int jj = half * NH + j;
+          const Wide w = widen(fw[j]);
+#pragma unroll
+          for (int i = 0; i < U; ++i) add_scaled(acc[i][jj], sx[i] * sw[jj % P], mfma_wide(w, x[i]));
+        }
+      } else {
+        // the sums of a block are added two matrix instructions later, so that neither unit waits
+        constexpr int F = U * NH, LAG = F < 3 ? F - 1 : 2;
+        f32x4 v[LAG + 1];
+        auto add = [&](int f) {
+          const int jj = half * NH + f / U;
+          add_scaled(acc[f % U][jj], sx[f % U] * sw[jj % P], v[f % (LAG + 1)]);
+        };
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          v[f % (LAG + 1)] = mfma_codes(fw[f / U], fx[f % U]);
+          if (f >= LAG) add(f - LAG);
+        }
+#pragma unroll
+        for (int f = F - LAG; f < F; ++f) add(f);
+      }
+    };
+    // waits until all loads of this wave but those of the `later` newest stages have landed
+    auto landed = [&](int later) {
+      if (later >= 2) wait_vm<2 * LU>();
+      else if (later == 1) wait_vm<LU>();
+      else wait_vm<0>();
+    };
+    // Stages whose own load is a whole one go first, in a loop without a branch (each
+    // costs tens of clocks, and a stage of a small tile is a few hundred).
+    int i = 0;
+    const int n = S - s0;  // stage s0 + i is in buffer i
+    if constexpr (NW == 8) {
+      // Two waves a SIMD, of two groups one step apart: while the waves of one
+      // group multiply, those of the other read the fragments of half a stage from
+      // LDS and issue loads, then they change places at a barrier.  A stage has
+      // landed for every wave when a group reads it: each wave waited for its own
+      // loads of the next stage before the barrier that ends its reads of this one.
+      const bool second = wv >= 4;
+      landed(min(ST - 2, n - 1));
+      meet();
+      if (second) meet();
+      auto turn = [&](int half) {
+        meet();
+        __builtin_amdgcn_s_setprio(1);
+        multiply(half);
+        __builtin_amdgcn_s_setprio(0);
+        meet();
+      };
+      for (; i < n - ST; ++i) {
+        read(i & (ST - 1), 0);
+        load_whole(s0 + i + ST - 1, (i + ST - 1) & (ST - 1));  // both groups have read stage i - 1
+        wait_lds();
+        turn(0);
+        read(i & (ST - 1), 1);
+        wait_vm<(ST - 2) * LU>();
+        turn(1);
+      }
+      for (; i < n; ++i) {
+        read(i & (ST - 1), 0);
+        if (i + ST - 1 < n) load(s0 + i + ST - 1, (i + ST - 1) & (ST - 1));
+        wait_lds();
+        turn(0);
+        read(i & (ST - 1), 1);
+        landed(min(ST - 2, n - 2 - i));
+        turn(1);
+      }
+      if (!second) meet();
+    } else {
+      // One or two groups of four waves: while one reads fragments, the other multiplies.  Group kg
+      // has stages kg, kg + KG, ... and loads them itself; at the barrier of turn i every group has
+      // its stage of that turn, and has left the buffer of the turn before.  A ring is one body, so
+      // that its buffers are constants.
+      constexpr int R = ST / KG;
+      auto multiply_stage = [&](int b) {
+        read(b, 0);
+        multiply(0);
+        read(b, 1);
+        multiply(1);
+      };
+      const int mine = (n - kg + KG - 1) / KG, turns = (n + KG - 1) / KG;
+      for (; i <= turns - 2 * R; i += R) {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          wait_vm<(R - 2) * LU>();
+          meet();
+          load_whole(s0 + KG * (i + u + R - 1) + kg, KG * ((u + R - 1) % R) + kg);
+          multiply_stage(KG * u + kg);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2 * R - 1; ++u) {
+        if (i + u >= turns) break;
+        landed(min(R - 2, mine - 1 - i - u));
+        meet();
+        if (i + u + R - 1 < mine) load(s0 + KG * (i + u + R - 1) + kg, KG * ((u + R - 1) % R) + kg);
+        if (i + u < mine) multiply_stage(KG * (u % R) + kg);
+      }
+    }
+  };
+  const int need = (t.rows + 16 * WGM - 1) / (16 * WGM);
+  if (need >= MF) run(std::integral_constant<int, MF>{});
+  else if (MF == 4 && need == 3) run(std::integral_constant<int, MF == 4 ? 3 : 1>{});
+  else if (MF == 4 && need == 2) run(std::integral_constant<int, MF == 4 ? 2 : 1>{});
+  else run(std::integral_constant<int, 1>{});
+  if constexpr (KG == 1) {
+    tile_end<C>(a, t, yr, i0, tn, tiles_n, wm, wn, parts, part, 0, acc);
+  } else {
+    // each group gives the other half of its fragment rows away and adds what it gets
+    f32x4* swap = reinterpret_cast<f32x4*>(lds) + (wv * C::MO * NF) * 64 + lane;
+    constexpr int HALF = NW * C::MO * NF * 64;
+    static_assert(2 * HALF * 16 <= C::RING, "sums");
+    f32x4 sum[C::MO][NF];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < C::MO; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        sum[i][j] = kg ? acc[C::MO + i][j] : acc[i][j];
+        swap[kg * HALF + (i * NF + j) * 64] = kg ? acc[i][j] : acc[C::MO + i][j];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < C::MO; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) sum[i][j] += swap[(1 - kg) * HALF + (i * NF + j) * 64];
+    tile_end<C>(a, t, yr, i0, tn, tiles_n, wm, wn, parts, part, kg * C::MO, sum);
+  }
+}
+
+constexpr int kMaxParts = 8;
+
+// The parts of a split K (of a dense product) added up in their order and stored: a
+// workgroup takes 4 rows, a wave each, by 256 columns.
+template <int P>
+__global__ __launch_bounds__(256) void k_f8_parts(F8Args a, int parts, int tiles_n, int cols) {
+  constexpr int BN = 64, BO = BN / P;
+  const int m = blockIdx.x / cols * 4 + (threadIdx.x >> 6), n = blockIdx.x % cols * 256 + (threadIdx.x & 63) * 4;
+  if (m >= a.rows || n >= a.n) return;
+  const size_t width = (size_t)tiles_n * BN, step = (size_t)a.rows * width;
+  const float* src = a.parts + (size_t)m * width + n / BO * BN + n % BO / 16 * 16 * P + n % 16;
+  f32x4 v[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    f32x4 sum{0.f, 0.f, 0.f, 0.f}, part[kMaxParts];  // all parts requested before the first is added
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i)
+      part[i] = *reinterpret_cast<const f32x4*>(src + min(i, parts - 1) * step + 16 * p);
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sum[c] += i < parts ? part[i][c] : 0.0f;
+    v[p] = sum;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (n + k < a.n) store_y(a.y, a.y_dtype, (size_t)m * a.n + n + k, P == 2 ? swiglu_f(v[0][k], v[P - 1][k]) : v[0][k]);
+}
+
+template <class C>
+static void tile_launch(const F8Args& a, int max_tiles, int parts, hipStream_t s) {
+  const int tiles_n = (a.n * C::P + C::BN - 1) / C::BN;
+  const int per_xcd = (tiles_n * max_tiles * parts + 7) / 8;
+  int band = 8;
+  if (a.order) {
+    band = (a.rows / a.num_experts + C::BM / 2) / C::BM;
+    band = band < 1 ? 1 : band > 8 ? 8 : band;
+  }
+  hipLaunchKernelGGL(k_f8_tile<C>, dim3(8 * per_xcd), dim3(C::T), 0, s, a, tiles_n, max_tiles, parts, band);
+  if constexpr (C::SPLIT) {
+    if (parts == 1) return;
+    const int cols = (a.n + 255) / 256;
+    hipLaunchKernelGGL(k_f8_parts<C::P>, dim3(cols * ((a.rows + 3) / 4)), dim3(256), 0, s, a, parts, tiles_n, cols);
+  }
+}
+
+static void stream_launch(const F8Args& a, int max_tiles, hipStream_t s) {
+  const int rows = a.n * (a.swiglu ? 2 : 1), halves = (rows + 15) / 16;
+  const dim3 block(256);
+  if (halves * max_tiles <= 256) {
+    if (a.swiglu) hipLaunchKernelGGL((k_f8_stream<1, 2, 4, 3>), dim3(halves * max_tiles), block, 0, s, a, halves);
+    else hipLaunchKernelGGL((k_f8_stream<1, 1, 4, 3>), dim3(halves * max_tiles), block, 0, s, a, halves);
+    return;
+  }
+  const int tiles_n = (rows + 31) / 32;
+  if (a.swiglu) hipLaunchKernelGGL((k_f8_stream<2, 2, 4, 2>), dim3(tiles_n * max_tiles), block, 0, s, a, tiles_n);
+  else hipLaunchKernelGGL((k_f8_stream<2, 1, 4, 2>), dim3(tiles_n * max_tiles), block, 0, s, a, tiles_n);
+}
+
+// The kernels a product may run on, in the order of F8Plan::kind: 16 rows of x by 32
+// matrix rows as a stream, and the tiles.
+struct Tiling {
+  int bm, bn;
+  int resident;            // workgroups that the card holds at a time
+  bool rounds;             // dense: time goes by whole rounds of them
+  double d0, d1;           // dense: us a round, and a stage of a round
+  double g0, g1, g2, g3, g4;  // grouped, see f8_plan
+};
+constexpr Tiling kTilings[] = {{16, 32, 512, false, 3.3, 0.105, 3.9, 0.88, 0.257, 0.0, 0.06},
+                               {64, 64, 256, true, 3.0, 0.21, 0.4, 2.9, 0.118, 0.106, 0.422},
+                               {64, 128, 256, true, 4.0, 0.30, 0.0, 3.46, 0.173, 0.136, 0.549},
+                               {128, 128, 256, true, 4.5, 0.54, 0.0, 4.58, 0.118, 0.379, 0.354},
+                               {128, 128, 512, false, 6.1, 1.15, 0.0, 4.99, 0.569, 0.0, 0.49},
+                               {256, 256, 256, true, 7.0, 1.4, 0.0, 6.44, 0.869, 0.0, 0.453}};
+constexpr int kStream = 0, kSplit = 1, kTwoToACu = 4, kLargest = 5;
+
+F8Plan f8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu, bool wide) {
+  const int P = swiglu ? 2 : 1, stages = (k + KS - 1) / KS, used = !grouped ? 1 : rows < experts ? rows : experts;
+  const double per = (double)rows / used, read = (double)used * n * P * k / 6.6e6;
+  F8Plan best{-1, 0, 1, 0};
+  double least = 0.0;
+  for (int kind = 0; kind < (int)(sizeof(kTilings) / sizeof(kTilings[0])); ++kind) {
+    const Tiling& m = kTilings[kind];
+    if (wide && kind == kLargest) continue;
+    const int cols = (n * P + m.bn - 1) / m.bn;
+    double time;
+    int parts = 1;
+    if (grouped) {
+      const double down = per / m.bm + 0.5 < 1.0 ? 1.0 : per / m.bm + 0.5;
+      double load = down * used * cols / m.resident, work = (per / m.bm + 0.25) * used * cols / m.resident;
+      if (kind > kSplit) load = ceil(load);
+      if (load < 1.0) load = 1.0;
+      if (work < 1.0) work = 1.0;
+      time = m.g0 + (m.g1 + m.g2 * stages) * load + m.g3 * stages * work + m.g4 * read;
+      if (kind != kStream && time < 1.2 * read) time = 1.2 * read;
+    } else {
+      const double tiles = (double)((rows + m.bm - 1) / m.bm) * cols;
+      if (kind == kStream ? rows > 16 && tiles > 256.0 : kind == kTwoToACu && tiles <= 256.0) continue;
+      double load = m.rounds ? ceil(tiles / m.resident) : tiles / m.resident;
+      if (load < 1.0) load = 1.0;
+      time = kind == kStream && rows <= 16 ? 0.0 : (m.d0 + m.d1 * stages) * load;
+      if (kind == kSplit) {
+        parts = (int)(224.0 / tiles);
+        if (parts > kMaxParts) parts = kMaxParts;
+        if (parts > stages / 6) parts = stages / 6;
+        const double saved = parts > 1 ? m.d1 * (stages - stages / parts) - 8.0 : 0.0;
+        if (saved <= 0.0) parts = 1;
+        else time -= saved;
+      }
+    }
+    if (best.kind >= 0 && time >= least) continue;
+    least = time;
+    best = F8Plan{kind, m.bm, parts, parts > 1 ? (size_t)parts * rows * cols * m.bn * 4 : 0};
+  }
+  return best;
+}
+
+template <int P, bool WIDE>
+static void tiles_launch(const F8Args& a, const F8Plan& plan, int max_tiles, hipStream_t s) {
+  if (plan.kind == 1) tile_launch<TileCfg<64, 64, 2, 2, 2, P, 8, WIDE>>(a, max_tiles, plan.parts, s);
+  else if (plan.kind == 2) tile_launch<TileCfg<64, 128, 2, 2, 2, P, 6, WIDE>>(a, max_tiles, 1, s);
+  else if (plan.kind == 3) tile_launch<TileCfg<128, 128, 4, 2, 1, P, 4, WIDE>>(a, max_tiles, 1, s);
+  else if (plan.kind == 4) tile_launch<TileCfg<128, 128, 4, 2, 1, P, 2, WIDE>>(a, max_tiles, 1, s);
+  else if constexpr (!WIDE) tile_launch<TileCfg<256, 256, 4, 2, 1, P, 2, WIDE>>(a, max_tiles, 1, s);
+}
+
+bool f8_launchable(const F8Plan& plan, int n, bool swiglu, int max_tiles) {
+  const size_t bn = kTilings[plan.kind].bn, cols = ((size_t)n * (swiglu ? 2 : 1) + bn - 1) / bn;
+  return cols * max_tiles * plan.parts < kMaxGroups;
+}
+
+hipError_t launch_gemm_f8(const F8Args& a, const F8Plan& plan, int max_tiles, hipStream_t s) {
+  const bool wide = a.y_dtype == MOE_DTYPE_F32;
+  if (plan.kind == kStream) stream_launch(a, max_tiles, s);
+  else if (a.swiglu) wide ? tiles_launch<2, true>(a, plan, max_tiles, s) : tiles_launch<2, false>(a, plan, max_tiles, s);
+  else wide ? tiles_launch<1, true>(a, plan, max_tiles, s) : tiles_launch<1, false>(a, plan, max_tiles, s);
   return hipGetLastError();
 }
 

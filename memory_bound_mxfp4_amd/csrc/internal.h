@@ -200,11 +200,18 @@ struct F8Args {
   const int32_t *order, *num_tiles;
   const int2* tiles;
   int num_experts, x_div;
+  float* parts;  // sums of each part of a split K: [part][position][columns of all tiles]
 };
+// How a product runs, as I8Plan; wide: products in fp16 (outputs of fp32).
 struct F8Plan {
-  int kind, tile_rows;
+  int kind, tile_rows, parts;
+  size_t part_bytes;
 };
-F8Plan f8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu);
+F8Plan f8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu, bool wide);
+// A product of one float row that the kernel quantises itself, on the tiles of
+// 16 positions; f8_token_ok: the rows it takes.
+bool f8_token_ok(const void* x, int k, int n, bool swiglu, int max_tiles);
+hipError_t launch_f8_token(const F8Args& a, const void* x, int dtype, int max_tiles, hipStream_t s);
 bool f8_launchable(const F8Plan& plan, int n, bool swiglu, int max_tiles);
 hipError_t launch_gemm_f8(const F8Args& a, const F8Plan& plan, int max_tiles, hipStream_t s);
 

@@ -315,20 +315,71 @@ def test_gemm_longest_rows(m):
     _close(y, want, ref.product_bound(want, np.abs(want), 512, "f32"))
 
 
-@pytest.mark.parametrize("m", [1, 16, 60, 300])
-def test_gemm_scales_by_block(m):
-    """Scales that differ by powers of two from block to block, row to row: each block has its own, exactly."""
+# sizes that reach every kernel, beside SHAPES
+ALL_KERNELS = [(1, 300, 656), (12, 300, 656), (12, 5000, 400), (24, 300, 656), (60, 200, 7184), (60, 1000, 1040), (60, 5000, 272),
+               (200, 1100, 656), (300, 5000, 272), (1000, 2050, 272), (1500, 7000, 144), (2100, 7200, 272)]
+
+
+def _exact_inputs(m, n, k, lead, seed):
+    """Codes and scales of few bits: every sum in fp32, in any order and however products are aligned, is exact."""
+    rng = np.random.default_rng(seed)
+    kb = ref.blocks(k)
+    x = rng.choice([0.0, 1.0, -1.0, 2.0], (m, k))
+    w = rng.choice([0.0, 1.0, -1.0, 0.5], lead + (n, k))
+    xs, ws = 2.0 ** rng.integers(-2, 3, (kb, m)), 2.0 ** rng.integers(-2, 3, lead + (ref.blocks(n), kb))
+    return x, w, xs, ws
+
+
+def _e4m3(v):
     import torch
-    n, k = 400, 128 * 5 + 16
-    rng = np.random.default_rng(m)
-    codes = rng.integers(0, 2, (m, k)) * 0.5            # sums of a few bits: exact in fp32
-    xs = 2.0 ** rng.integers(-3, 4, (6, m))
-    wv = rng.integers(0, 2, (n, k)) * 1.0
-    ws = 2.0 ** rng.integers(-3, 4, (4, 6))
-    y = moe.gemm_f8(torch.from_numpy(codes).float().to(torch.float8_e4m3fn).cuda(), torch.from_numpy(wv).float().to(torch.float8_e4m3fn).cuda(),
-                    _dev(ws.astype(np.float32)), x_scale=_dev(xs.astype(np.float32)), out_dtype=torch.float32)
-    want, _ = ref.product(codes, xs, wv, ws)
-    assert np.array_equal(y.double().cpu().numpy(), want)
+    return torch.from_numpy(np.ascontiguousarray(v)).float().to(torch.float8_e4m3fn).cuda()
+
+
+def _rounded(y, out):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(y)).float().to(ref.torch_dtype(out)).cuda()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("m,n,k", ALL_KERNELS)
+def test_gemm_exact(m, n, k, swiglu, out):
+    """Each row, column and block of K with its own scale, to the last bit. With SwiGLU the gates lie above 32, where
+    silu(g) is g in fp32."""
+    import torch
+    x, w, xs, ws = _exact_inputs(m, n, k, (2,) if swiglu else (), m + n)
+    if swiglu:
+        x[:, 32:] = 0.0                                     # short sums, whose product fits
+        x[:, :32], w[0, :, :32], xs[0], ws[0, :, 0] = 1.0, 1.0, np.maximum(xs[0], 1.0), 2.0
+        w[0, :, 32:] = 0.0
+    y = moe.gemm_f8(_e4m3(x), _e4m3(w), _dev(ws.astype(np.float32)), x_scale=_dev(xs.astype(np.float32)), swiglu=swiglu,
+                    out_dtype=ref.torch_dtype(out))
+    if swiglu:
+        want = ref.product(x, xs, w[0], ws[0])[0] * ref.product(x, xs, w[1], ws[1])[0]
+    else:
+        want = ref.product(x, xs, w, ws)[0]
+    assert torch.equal(y, _rounded(want, out))
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("by_slot", [False, True])
+@pytest.mark.parametrize("tokens,top_k,E,n,k", [(1, 4, 8, 300, 272), (9, 3, 16, 600, 400), (60, 4, 3, 300, 656), (300, 4, 8, 520, 272),
+                                                (700, 4, 4, 1100, 400), (2000, 2, 2, 2100, 272)])
+def test_experts_exact(tokens, top_k, E, n, k, by_slot, out):
+    import torch
+    idx = _idx(tokens, top_k, E, tokens)
+    rows = tokens * top_k if by_slot else tokens
+    x, w, xs, ws = _exact_inputs(rows, n, k, (E,), tokens)
+    groups = moe.moe_group_slots(_dev(idx), E)
+    y = moe.experts_gemm_f8(_e4m3(x), groups, _e4m3(w), _dev(ws.astype(np.float32)), x_scale=_dev(xs.astype(np.float32)),
+                            out_dtype=ref.torch_dtype(out))
+    flat = idx.reshape(-1)
+    want = np.zeros((tokens * top_k, n))
+    for e in range(E):
+        mine = np.flatnonzero(flat == e)
+        from_rows = mine if by_slot else mine // top_k
+        want[mine] = ref.product(x[from_rows], xs[:, from_rows], w[e], ws[e])[0]
+    assert torch.equal(y, _rounded(want, out))
 
 
 @pytest.mark.parametrize("m", [1, 3, 90, 300])
