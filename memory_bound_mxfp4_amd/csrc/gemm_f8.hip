@@ -472,10 +472,9 @@ __device__ __forceinline__ void tile_end(const F8Args& a, const Tile& t, const i
 }
 
 template <class C>
-__global__ __launch_bounds__(C::T) void k_f8_tile(F8Args a, int tiles_n, int tiles_m, int parts, int band_rows) {
+__global__ __launch_bounds__(C::T, C::RING <= 65536 ? 4 : 2) void k_f8_tile(F8Args a, int tiles_n, int tiles_m, int parts, int band_rows) {
   constexpr int BM = C::BM, BN = C::BN, WGM = C::WGM, WGN = C::WGN, P = C::P, ST = C::ST, NW = C::NW, MF = C::MF,
                 KG = C::KG, NF = C::NF, GX = BM / 8, L = (BM + BN) / 8 / NW, SL = C::SL;  // L: row loads of a wave and stage
-  constexpr int NH = NF / 2;  // matrix fragments of half a stage's work
   static_assert(L * 8 * NW == BM + BN && NF % 2 == 0 && ST % KG == 0 && GX == NW * MF && (KG == 1 || NW == 4), "tile");
   // the ring, then the scales of its stages, then the tile's output rows
   __shared__ __attribute__((aligned(1024))) int8_t lds[C::RING + 4 * C::SCALES + 4 * BM];
@@ -507,11 +506,11 @@ __global__ __launch_bounds__(C::T) void k_f8_tile(F8Args a, int tiles_n, int til
   for (int i = 0; i < L; ++i) {
     const int g = wv + NW * i;  // group of 8 rows: first those of x, then the matrix's
     if (g < GX) {
-      src[i] = a.x + (size_t)x_row(a, yr[8 * g + lr]) * a.x_stride;
+      src[i] = a.x + (size_t)x_row(a, yr[8 * g + lr]) * a.x_stride + 16 * chunk;
     } else {
       const int gw = 8 * (g - GX);  // first row of the tile's matrix part; P 2: 16 gate rows, 16 up rows, ...
       const int n = min(i0 + (P == 2 ? gw / 32 * 16 + gw % 16 : gw) + lr, a.n - 1);
-      src[i] = a.w + (((size_t)t.e * P + (P == 2 ? gw / 16 % 2 : 0)) * a.n + n) * K;
+      src[i] = a.w + (((size_t)t.e * P + (P == 2 ? gw / 16 % 2 : 0)) * a.n + n) * K + 16 * chunk;
     }
   }
   // Scales: lane 16 i + r brings that of row r of the wave's fragment row i, the lanes behind
@@ -523,6 +522,18 @@ __global__ __launch_bounds__(C::T) void k_f8_tile(F8Args a, int tiles_n, int til
   const uint32_t scale_step = of_x ? (uint32_t)a.x_rows : 1u;
   float* my_scales = scales + wv * SL * 64;
   constexpr int SW = SL == 2 ? 64 : 16 * MF;  // where the matrix's scales lie, gate and up in turn
+  // Where this lane's chunks of the wave's first fragments and its scales lie in the buffer that is read: moved on from
+  // stage to stage, so that all else are constants in the instructions and no address takes a register of its own.
+  int x_at[2], w_at[2], sx_at, sw_at;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int at = kg * C::STAGE + r * KS + 16 * ((4 * h + q) ^ (r & 7));
+    x_at[h] = at + 16 * wm * KS;
+    w_at[h] = at + (BM + wn * (BN / WGN)) * KS;
+  }
+  constexpr int SCALE_STAGE = 4 * NW * SL * 64;  // bytes
+  sw_at = C::RING + kg * SCALE_STAGE + 4 * wv * SL * 64;
+  sx_at = sw_at + 4 * r;
 
   const int stages = (K + KS - 1) / KS;
   const int s0 = (int)((size_t)stages * part / parts), S = (int)((size_t)stages * (part + 1) / parts);
@@ -534,157 +545,192 @@ __global__ __launch_bounds__(C::T) void k_f8_tile(F8Args a, int tiles_n, int til
   // With U of the MF fragment rows: a tile whose last rows are missing (the end of an
   // expert) neither loads nor multiplies them.
   auto run = [&](auto used) {
-    constexpr int U = decltype(used)::value, LU = L - MF + U + SL;
-    auto load_scales = [&](int st, int b) {
-      float* dst = my_scales + b * (NW * SL * 64);
-      load_floats_to_lds(scale0 + (size_t)(uint32_t)st * scale_step, dst);
-      if constexpr (SL == 2) load_floats_to_lds(w0 + st, dst + 64);
-    };
-    auto load_whole = [&](int st, int b) {
+    constexpr int U = decltype(used)::value, LU = L - MF + U + SL;  // loads of a stage
+    // load number i of stage st to buffer b; WHOLE: the stage has 128 codes
+    auto load_one = [&](int st, int b, int i, auto whole) {
       int8_t* buf = lds + b * C::STAGE;
-#pragma unroll
-      for (int i = 0; i < L; ++i)
-        if (i < U || i >= MF) load_to_lds(src[i] + (st * KS + 16 * chunk), buf + 1024 * (wv + NW * i));
-      load_scales(st, b);
-    };
-    auto load = [&](int st, int b) {  // stage st to buffer b
-      if ((st + 1) * KS <= K) {
-        load_whole(st, b);
-      } else {  // the last stage of a K that is no multiple of 128: zeros past K on x's side, the matrix's own codes on the other
-        int8_t* buf = lds + b * C::STAGE;
-        const int k = st * KS + 16 * chunk;
-#pragma unroll
-        for (int i = 0; i < L; ++i)
-          if (i < U || i >= MF)
-            load_to_lds(i < MF && k >= K ? kZeroCodes : src[i] + min(k, K - 16), buf + 1024 * (wv + NW * i));
-        load_scales(st, b);
+      if (i >= LU - SL) {
+        float* dst = my_scales + b * (NW * SL * 64);
+        if (i == LU - SL) load_floats_to_lds(scale0 + (size_t)(uint32_t)st * scale_step, dst);
+        else load_floats_to_lds(w0 + st, dst + 64);
+        return;
       }
-    };
-#pragma unroll
-    for (int i = 0; i < ST / KG - 1; ++i)
-      if (s0 + KG * i + kg < S) load(s0 + KG * i + kg, KG * i + kg);
-    Codes fw[NH], fx[U];
-    float sx[U], sw[P];
-    auto read = [&](int b, int half) {
-      const int8_t* bx = lds + b * C::STAGE + 16 * wm * KS;
-      const int8_t* bw = lds + b * C::STAGE + BM * KS + wn * (BN / WGN) * KS;
-      if (half == 0) {
-        const float* sc = my_scales + b * (NW * SL * 64);
-#pragma unroll
-        for (int p = 0; p < P; ++p) sw[p] = sc[SW + p];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          sx[i] = sc[16 * i + r];
-          fx[i] = read_codes(bx + 16 * WGM * KS * i, r, q);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < NH; ++j) fw[j] = read_codes(bw + 16 * KS * (half * NH + j), r, q);
-    };
-    auto multiply = [&](int half) {
-      if constexpr (C::WIDE) {
-        Wide x[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) x[i] = widen(fx[i]);
-#pragma unroll
-        for (int j = 0; j < NH; ++j) {
-          const int jj = half * NH + j;
-          const Wide w = widen(fw[j]);
-#pragma unroll
-          for (int i = 0; i < U; ++i) add_scaled(acc[i][jj], sx[i] * sw[jj % P], mfma_wide(w, x[i]));
-        }
+      const int g = i < U ? i : i - U + MF;
+      int8_t* dst = buf + 1024 * (wv + NW * g);
+      // past K: zeros on x's side, times codes of the matrix that are there
+      if constexpr (decltype(whole)::value) {
+        load_to_lds(src[g] + st * KS, dst);
       } else {
-        // the sums of a block are added two matrix instructions later, so that neither unit waits
-        constexpr int F = U * NH, LAG = F < 3 ? F - 1 : 2;
-        f32x4 v[LAG + 1];
-        auto add = [&](int f) {
-          const int jj = half * NH + f / U;
-          add_scaled(acc[f % U][jj], sx[f % U] * sw[jj % P], v[f % (LAG + 1)]);
-        };
-#pragma unroll
-        for (int f = 0; f < F; ++f) {
-          v[f % (LAG + 1)] = mfma_codes(fw[f / U], fx[f % U]);
-          if (f >= LAG) add(f - LAG);
-        }
-#pragma unroll
-        for (int f = F - LAG; f < F; ++f) add(f);
+        const int k = st * KS + 16 * chunk;
+        load_to_lds(g < MF && k >= K ? kZeroCodes : src[g] + (min(k, K - 16) - 16 * chunk), dst);
       }
     };
+    auto load = [&](int st, int b) {
+#pragma unroll
+      for (int i = 0; i < LU; ++i) load_one(st, b, i, std::false_type{});
+    };
+
+    // The work of a stage: NF * U products in this order, column by column but for the last two
+    // columns, which go row by row, so that the rows of x of the next stage can be read meanwhile.
+    constexpr int F = NF * U, F0 = (NF - 2) * U;
+    constexpr int LAG = C::WIDE ? 0 : F < 4 ? F - 1 : 3;
+    Codes fw[4], fx[U];
+    float sx[U], sw[P], scale[U][P];
+    f32x4 v[LAG + 1];
+    auto column = [](int f) { return f < F0 ? f / U : NF - 2 + (f - F0) % 2; };
+    auto row = [](int f) { return f < F0 ? f % U : (f - F0) / 2; };
+    auto read_x = [&](int i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) fx[i].c[h] = *reinterpret_cast<const i32x4*>(lds + x_at[h] + 16 * WGM * i * KS);
+      sx[i] = *reinterpret_cast<const float*>(lds + sx_at + 64 * i);
+    };
+    auto read_w = [&](int j) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) fw[j % 4].c[h] = *reinterpret_cast<const i32x4*>(lds + w_at[h] + 16 * j * KS);
+    };
+    auto read_sw = [&]() {
+#pragma unroll
+      for (int p = 0; p < P; ++p) sw[p] = *reinterpret_cast<const float*>(lds + sw_at + 4 * (SW + p));
+    };
+    auto advance = [&](int buffers) {  // to the buffer that many further
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        x_at[h] += buffers * C::STAGE;
+        w_at[h] += buffers * C::STAGE;
+        asm volatile("" : "+v"(x_at[h]), "+v"(w_at[h]));
+      }
+      sx_at += buffers * SCALE_STAGE;
+      sw_at += buffers * SCALE_STAGE;
+      asm volatile("" : "+v"(sx_at), "+v"(sw_at));
+    };
+    auto scales_of_stage = [&]() {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int p = 0; p < P; ++p) scale[i][p] = sx[i] * sw[p];
+    };
+    auto add = [&](int f) {
+      f32x4& sum = acc[row(f)][column(f)];
+      add_scaled(sum, scale[row(f)][column(f) % P], v[f % (LAG + 1)]);
+      asm volatile("" : "+v"(sum));  // here, and not where the compiler would gather the additions of a whole stage
+    };
+    // Product f, and the addition of the one LAG before it: its sum has left the matrix unit by
+    // then.  (With LAG 2 a matrix instruction and its additions took 44 clocks, with 4 38, alone 35.)
+    auto slot = [&](int f) {
+      if constexpr (C::WIDE) {
+        if (f == 0) scales_of_stage();
+        add_scaled(acc[row(f)][column(f)], scale[row(f)][column(f) % P], mfma_wide(widen(fw[column(f) % 4]), widen(fx[row(f)])));
+      } else {
+        v[f % (LAG + 1)] = mfma_codes(fw[column(f) % 4], fx[row(f)]);
+        if (f == LAG) scales_of_stage();  // those before belong to the stage before
+        add(f >= LAG ? f - LAG : f - LAG + F);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    if constexpr (!C::WIDE) {
+#pragma unroll
+      for (int i = 0; i <= LAG; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int p = 0; p < P; ++p) scale[i][p] = 0.0f;
+    }
+
+    // Group kg has stages kg, kg + KG, ... of the workgroup's n, its t-th in buffer KG (t % R) + kg.
+    constexpr int R = ST / KG;
+    const int n = S - s0, mine = (n - kg + KG - 1) / KG, turns = (n + KG - 1) / KG;
+    auto stage_of = [&](int t) { return s0 + KG * t + kg; };
     // waits until all loads of this wave but those of the `later` newest stages have landed
     auto landed = [&](int later) {
-      if (later >= 2) wait_vm<2 * LU>();
+      if (later >= 3) wait_vm<3 * LU>();
+      else if (later == 2) wait_vm<2 * LU>();
       else if (later == 1) wait_vm<LU>();
       else wait_vm<0>();
     };
-    // Stages whose own load is a whole one go first, in a loop without a branch (each
-    // costs tens of clocks, and a stage of a small tile is a few hundred).
-    int i = 0;
-    const int n = S - s0;  // stage s0 + i is in buffer i
-    if constexpr (NW == 8) {
-      // Two waves a SIMD, of two groups one step apart: while the waves of one
-      // group multiply, those of the other read the fragments of half a stage from
-      // LDS and issue loads, then they change places at a barrier.  A stage has
-      // landed for every wave when a group reads it: each wave waited for its own
-      // loads of the next stage before the barrier that ends its reads of this one.
-      const bool second = wv >= 4;
-      landed(min(ST - 2, n - 1));
-      meet();
-      if (second) meet();
-      auto turn = [&](int half) {
-        meet();
-        __builtin_amdgcn_s_setprio(1);
-        multiply(half);
-        __builtin_amdgcn_s_setprio(0);
-        meet();
-      };
-      for (; i < n - ST; ++i) {
-        read(i & (ST - 1), 0);
-        load_whole(s0 + i + ST - 1, (i + ST - 1) & (ST - 1));  // both groups have read stage i - 1
-        wait_lds();
-        turn(0);
-        read(i & (ST - 1), 1);
-        wait_vm<(ST - 2) * LU>();
-        turn(1);
-      }
-      for (; i < n; ++i) {
-        read(i & (ST - 1), 0);
-        if (i + ST - 1 < n) load(s0 + i + ST - 1, (i + ST - 1) & (ST - 1));
-        wait_lds();
-        turn(0);
-        read(i & (ST - 1), 1);
-        landed(min(ST - 2, n - 2 - i));
-        turn(1);
-      }
-      if (!second) meet();
-    } else {
-      // One or two groups of four waves: while one reads fragments, the other multiplies.  Group kg
-      // has stages kg, kg + KG, ... and loads them itself; at the barrier of turn i every group has
-      // its stage of that turn, and has left the buffer of the turn before.  A ring is one body, so
-      // that its buffers are constants.
-      constexpr int R = ST / KG;
-      auto multiply_stage = [&](int b) {
-        read(b, 0);
-        multiply(0);
-        read(b, 1);
-        multiply(1);
-      };
-      const int mine = (n - kg + KG - 1) / KG, turns = (n + KG - 1) / KG;
-      for (; i <= turns - 2 * R; i += R) {
+    auto first_columns = [&]() {
 #pragma unroll
-        for (int u = 0; u < R; ++u) {
-          wait_vm<(R - 2) * LU>();
-          meet();
-          load_whole(s0 + KG * (i + u + R - 1) + kg, KG * ((u + R - 1) % R) + kg);
-          multiply_stage(KG * u + kg);
+      for (int j = 0; j < NF - 2; ++j) {
+        read_w(j + 2);
+#pragma unroll
+        for (int i = 0; i < U; ++i) slot(j * U + i);
+      }
+    };
+    static_assert(NF == 2 || NF % 4 == 0, "buffers of the columns");
+    // The last two columns; `next`: and the next stage's first fragments, `loads`: of stage st to buffer b.
+    auto last_columns = [&](int st, int b, auto next, auto loads) {
+      if constexpr (decltype(next)::value) {
+        if constexpr (NF > 2) {
+          read_w(0);
+          read_w(1);
+        }
+        read_sw();
+      }
+#pragma unroll
+      for (int g = 0; g < 2 * U; ++g) {
+        slot(F0 + g);
+        if constexpr (decltype(next)::value)
+          if (g % 2) read_x(g / 2);
+        if constexpr (decltype(loads)::value) {
+#pragma unroll
+          for (int i = g * LU / (2 * U); i < (g + 1) * LU / (2 * U); ++i) load_one(st, b, i, std::true_type{});
         }
       }
+      if constexpr (decltype(next)::value && NF == 2) {
+        read_w(0);
+        read_w(1);
+      }
+    };
+    auto first_reads = [&]() {
+      read_sw();
 #pragma unroll
-      for (int u = 0; u < 2 * R - 1; ++u) {
-        if (i + u >= turns) break;
-        landed(min(R - 2, mine - 1 - i - u));
-        meet();
-        if (i + u + R - 1 < mine) load(s0 + KG * (i + u + R - 1) + kg, KG * ((u + R - 1) % R) + kg);
-        if (i + u < mine) multiply_stage(KG * (u % R) + kg);
+      for (int i = 0; i < U; ++i) read_x(i);
+      read_w(0);
+      read_w(1);
+    };
+    auto pass = [&]() {  // a barrier behind which what every wave waited for has landed, and what it read is no longer needed
+      wait_lds();
+      meet();
+    };
+
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+      if (t < mine) load(stage_of(t), KG * t + kg);
+    landed(min(R - 1, mine - 1));
+    pass();
+    if (mine > 0) first_reads();
+    // Stages that are followed by another and whose loads are whole ones go first, without a branch.
+    const int loads_whole = (K / KS - s0 - kg + KG - 1) / KG;  // of this group's stages, those of 128 codes come first
+    const int ahead = min(mine, loads_whole) - (2 * R - 1);     // the pass at t loads up to stage t + 2 R - 1
+    int t = 0;
+    for (; t < ahead; t += R) {
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        first_columns();
+        wait_vm<(R - 2) * LU>();
+        pass();
+        advance(u + 1 == R ? -KG * (R - 1) : KG);
+        last_columns(stage_of(t + u + R), KG * u + kg, std::true_type{}, std::true_type{});
+      }
+    }
+    // The rest, a stage at a time.
+    for (int at = 0; t < turns; ++t, at = at + 1 == R ? 0 : at + 1) {
+      const bool there = KG == 1 || t < mine;
+      if (there) first_columns();
+      if (t + 1 < turns) {
+        landed(min(R - 2, mine - 2 - t));
+        pass();
+        if (t + R < mine) load(stage_of(t + R), KG * at + kg);
+      }
+      if (there) last_columns(0, 0, std::false_type{}, std::false_type{});
+      if (t + 1 < mine) {
+        advance(at + 1 == R ? -KG * (R - 1) : KG);
+        first_reads();
+      }
+    }
+    if constexpr (!C::WIDE) {
+      if (mine > 0) {
+#pragma unroll
+        for (int f = F - LAG; f < F; ++f) add(f);
       }
     }
   };
@@ -706,8 +752,14 @@ __global__ __launch_bounds__(C::T) void k_f8_tile(F8Args a, int tiles_n, int til
     for (int i = 0; i < C::MO; ++i)
 #pragma unroll
       for (int j = 0; j < NF; ++j) {
-        sum[i][j] = kg ? acc[C::MO + i][j] : acc[i][j];
-        swap[kg * HALF + (i * NF + j) * 64] = kg ? acc[i][j] : acc[C::MO + i][j];
+        const f32x4 lower = acc[i][j], upper = acc[C::MO + i][j];  // values: a choice between places would keep acc in memory
+        f32x4 away;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          sum[i][j][c] = kg ? upper[c] : lower[c];
+          away[c] = kg ? lower[c] : upper[c];
+        }
+        swap[kg * HALF + (i * NF + j) * 64] = away;
       }
     __syncthreads();
 #pragma unroll
