@@ -603,11 +603,22 @@ __global__ __launch_bounds__(C::T, C::RING <= 65536 ? 4 : 2) void k_f8_tile(F8Ar
       sw_at += buffers * SCALE_STAGE;
       asm volatile("" : "+v"(sx_at), "+v"(sw_at));
     };
-    auto scales_of_stage = [&]() {
+    // The scales that products of the stage are added with, set when the last ones of the stage before have
+    // been.  With few products the next stage's are read before that: `fresh` keeps this one's.
+    constexpr bool EARLY = F0 <= LAG;
+    float fresh[U][P];
+    auto multiply_scales = [&]() {
 #pragma unroll
       for (int i = 0; i < U; ++i)
 #pragma unroll
-        for (int p = 0; p < P; ++p) scale[i][p] = sx[i] * sw[p];
+        for (int p = 0; p < P; ++p) fresh[i][p] = sx[i] * sw[p];
+    };
+    auto scales_of_stage = [&]() {
+      if constexpr (!EARLY) multiply_scales();
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int p = 0; p < P; ++p) scale[i][p] = fresh[i][p];
     };
     auto add = [&](int f) {
       f32x4& sum = acc[row(f)][column(f)];
@@ -658,6 +669,7 @@ __global__ __launch_bounds__(C::T, C::RING <= 65536 ? 4 : 2) void k_f8_tile(F8Ar
     static_assert(NF == 2 || NF % 4 == 0, "buffers of the columns");
     // The last two columns; `next`: and the next stage's first fragments, `loads`: of stage st to buffer b.
     auto last_columns = [&](int st, int b, auto next, auto loads) {
+      if constexpr (EARLY) multiply_scales();
       if constexpr (decltype(next)::value) {
         if constexpr (NF > 2) {
           read_w(0);
