@@ -52,42 +52,53 @@ __device__ __forceinline__ u32x2 f8_pack(const float* t) {
   return o;
 }
 
-// A block's scale, from the bits of its largest magnitude.
+// A block's scale, from the bits of its largest magnitude: fp32(amax / 448).  The quotient by
+// the constant takes one correction (the same as the division for every significand, as long as
+// nothing leaves the normal numbers); its reciprocal only has to be near.
 struct F8Scale {
   float stored, inv;
   bool zero;  // all codes 0
   bool tiny;  // a scale whose fp32 reciprocal would overflow, or that is far from amax / 448
 };
 __device__ __forceinline__ F8Scale f8_scale(uint32_t amax_bits) {
+  constexpr float C = 1.0f / kF8Max;
   F8Scale r;
   const bool bad = amax_bits >= 0x7F800000u;
-  const float s = __uint_as_float(amax_bits) / kF8Max;
+  const float amax = __uint_as_float(amax_bits), near = amax * C;
+  float s = fmaf(fmaf(-near, kF8Max, amax), C, near);
+  r.tiny = amax < 0x1p-90f;
+  if (r.tiny) {
+    s = amax / kF8Max;
+    asm volatile("" : "+v"(s));  // rare: a branch, and not a division for every block
+  }
   r.stored = bad ? __uint_as_float(0x7FC00000u) : s;
   r.zero = bad || s == 0.0f;
-  r.tiny = s < 0x1p-100f;
-  r.inv = 1.0f / s;
+  r.inv = __builtin_amdgcn_rcpf(s);
   return r;
 }
 
 // 8 elements of a block to codes, each the nearest to the exact quotient x / scale.  x * inv
-// is within two of its last places of the quotient (half of one for the reciprocal, half
-// for the product, twice that where the leading bits differ); where that leaves
-// it in doubt, the sign of x - middle * scale decides, which 64 bits hold exactly
-// (24 + 5 bits).
+// is within three of its last places of the quotient (two for the reciprocal, one for the product);
+// where that leaves it in doubt, the sign of x - middle * scale decides, which 64 bits hold exactly
+// (24 + 5 bits).  The test for doubt takes numbers of 2^-6 and more one way, and sends a block
+// with smaller ones but 0 (some 4% of the waves, of normal values) to the other part too.
 __device__ __forceinline__ u32x2 f8_quant8(const float* v, const F8Scale& r) {
+  constexpr int TOL = 6;
   float t[8];
-  bool near = false;
+  uint32_t doubt = ~0u, least = ~0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     t[i] = v[i] * r.inv;
-    near |= f8_near<4>(t[i]);
+    const uint32_t b = __float_as_uint(t[i]);
+    doubt = min(doubt, (b << 12) - ((F8_HALF - TOL) << 12));  // the bits rounded away, from just below the middle on
+    least = min(least, (b << 1) - 1u);
   }
-  if (near || r.tiny) {
+  if (doubt <= (2u * TOL) << 12 || least < 0x79000000u - 1u || r.tiny) {  // 0x3C800000 is 2^-6
     const double s = (double)r.stored;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (r.tiny) t[i] = f8_clamp((float)((double)v[i] / s));
-      if (f8_near<4>(t[i])) {
+      if (f8_near<TOL>(t[i])) {
         const float m = f8_middle(t[i]);
         t[i] = f8_side(t[i], m, fma(-(double)m, s, (double)fabsf(v[i])));
       }
@@ -105,28 +116,40 @@ __device__ __forceinline__ uint32_t block_max_bits(uint32_t m) {
   return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x121, 0xF, 0xF, false));
 }
 
-// 8 elements of a row from `at` on, fp32; VEC: aligned to 16 bytes and inside the row,
-// else element by element, zeros from `end` on.
+// The 8 elements of a row that chunk c stands for; a block is 16 chunks.  VEC: those from 8 c on,
+// for rows aligned to 16 bytes whose length is a multiple of 8, in wide accesses; else 16 apart within
+// the block, so that the 16 lanes of a block touch neighbours (4096 rows of 4999 fp32: see the quantiser).
+template <bool VEC>
+__device__ __forceinline__ int element(int c, int i) {
+  return VEC ? 8 * c + i : c / kLanes * kBlock + c % kLanes + kLanes * i;
+}
+
+// They in fp32, zeros from `end` on.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const void* row, int at, int end, float* v) {
+__device__ __forceinline__ void load8(const void* row, int c, int end, float* v) {
   if constexpr (VEC) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(row) + (size_t)at * Elem<DT>::bytes);
-    Chunk<DT>::widen(p[0], v);
-    if constexpr (Chunk<DT>::N == 4) Chunk<DT>::widen(p[1], v + 4);
+    u32x4 d[2] = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+    if (8 * c < end) {
+      const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(row) + (size_t)c * 8 * Elem<DT>::bytes);
+      d[0] = p[0];
+      if constexpr (Chunk<DT>::N == 4) d[1] = p[1];
+    }
+    Chunk<DT>::widen(d[0], v);
+    if constexpr (Chunk<DT>::N == 4) Chunk<DT>::widen(d[1], v + 4);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = at + i < end ? load_f32<DT>(row, at + i) : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = element<VEC>(c, i) < end ? load_f32<DT>(row, element<VEC>(c, i)) : 0.0f;
   }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8_codes(void* row, int at, int end, const u32x2& o) {
+__device__ __forceinline__ void store8_codes(void* row, int c, int end, const u32x2& o) {
   if constexpr (VEC) {
-    *reinterpret_cast<u32x2*>(static_cast<char*>(row) + at) = o;
+    if (8 * c < end) reinterpret_cast<u32x2*>(row)[c] = o;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (at + i < end) static_cast<uint8_t*>(row)[at + i] = (uint8_t)(o[i / 4] >> (i % 4 * 8));
+      if (element<VEC>(c, i) < end) static_cast<uint8_t*>(row)[element<VEC>(c, i)] = (uint8_t)(o[i / 4] >> (i % 4 * 8));
   }
 }
 

@@ -234,12 +234,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_f8_token(F8Args a, const void* _
   }
   float v[NC][8];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int at = 8 * ((int)threadIdx.x + T * i);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    if (at < K) load8<DT, true>(x, at, K, v[i]);
-  }
+  for (int i = 0; i < NC; ++i) load8<DT, true>(x, threadIdx.x + T * i, K, v[i]);
   __builtin_amdgcn_sched_barrier(0);
   const int lr = lane >> 3, chunk = (lane ^ lr) & 7;
   const int8_t* src[2];
@@ -828,17 +823,18 @@ static void tile_launch(const F8Args& a, int max_tiles, int parts, hipStream_t s
   }
 }
 
+template <int NN, int NW, int ST>
+static void stream_launch_as(const F8Args& a, int max_tiles, hipStream_t s) {
+  const int tiles_n = (a.n * (a.swiglu ? 2 : 1) + 16 * NN - 1) / (16 * NN);
+  const dim3 grid(tiles_n * max_tiles), block(64 * NW);
+  if (a.swiglu) hipLaunchKernelGGL((k_f8_stream<NN, 2, NW, ST>), grid, block, 0, s, a, tiles_n);
+  else hipLaunchKernelGGL((k_f8_stream<NN, 1, NW, ST>), grid, block, 0, s, a, tiles_n);
+}
+
 static void stream_launch(const F8Args& a, int max_tiles, hipStream_t s) {
   const int rows = a.n * (a.swiglu ? 2 : 1), halves = (rows + 15) / 16;
-  const dim3 block(256);
-  if (halves * max_tiles <= 256) {
-    if (a.swiglu) hipLaunchKernelGGL((k_f8_stream<1, 2, 4, 3>), dim3(halves * max_tiles), block, 0, s, a, halves);
-    else hipLaunchKernelGGL((k_f8_stream<1, 1, 4, 3>), dim3(halves * max_tiles), block, 0, s, a, halves);
-    return;
-  }
-  const int tiles_n = (rows + 31) / 32;
-  if (a.swiglu) hipLaunchKernelGGL((k_f8_stream<2, 2, 4, 2>), dim3(tiles_n * max_tiles), block, 0, s, a, tiles_n);
-  else hipLaunchKernelGGL((k_f8_stream<2, 1, 4, 2>), dim3(tiles_n * max_tiles), block, 0, s, a, tiles_n);
+  if (halves * max_tiles <= 256) stream_launch_as<1, 4, 3>(a, max_tiles, s);
+  else stream_launch_as<2, 4, 2>(a, max_tiles, s);
 }
 
 // The kernels a product may run on, in the order of F8Plan::kind: 16 rows of x by 32

@@ -63,37 +63,33 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_q(NormArgs a) {
   const int tid = threadIdx.x % T, lane = threadIdx.x & 63, wv = tid >> 6;
   const size_t row = a.row0 + (size_t)blockIdx.x * (B / T) + threadIdx.x / T;
   if (B != T && row >= (size_t)a.rows) return;
-  const int H = a.hidden, blocks = (H + kBlock - 1) / kBlock, chunks = F8 ? blocks * kLanes : (H + 7) / 8;
+  const int H = a.hidden, blocks = (H + kBlock - 1) / kBlock, chunks = blocks * kLanes;
   const float* hrow = a.h + row * a.h_stride;
   const char* trow = static_cast<const char*>(a.t) + row * a.t_stride * Elem<DT>::bytes;
   float* orow = a.h_out + row * H;
   float g[R][8];
 
-  auto sum = [&](int c, float* v) {  // the chunk's h + t, stored
-    const int at = 8 * c;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (at >= H) return;
-    load8<MOE_DTYPE_F32, VEC>(hrow, at, H, v);
+  // A chunk of h and t; then their sum, stored.  (Apart: h_out may be h, so no load moves over a store.)
+  auto fetch = [&](int c, float* v, float* u) {
+    load8<MOE_DTYPE_F32, VEC>(hrow, c, H, v);
+    if (a.t) load8<DT, VEC>(trow, c, H, u);
+  };
+  auto sum = [&](int c, float* v, const float* u) {
     if (!a.t) return;
-    float u[8];
-    load8<DT, VEC>(trow, at, H, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += u[i];
     if constexpr (VEC) {
+      if (8 * c >= H) return;
 #pragma unroll
-      for (int i = 0; i < 8; i += 4) *reinterpret_cast<f32x4*>(orow + at + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+      for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<f32x4*>(orow + 8 * c + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (at + i < H) orow[at + i] = v[i];
+        if (element<VEC>(c, i) < H) orow[element<VEC>(c, i)] = v[i];
     }
   };
-  auto again = [&](int c, float* v) {  // the same chunk in a later pass
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (8 * c < H) load8<MOE_DTYPE_F32, VEC>(a.t ? orow : hrow, 8 * c, H, v);
-  };
+  auto again = [&](int c, float* v) { load8<MOE_DTYPE_F32, VEC>(a.t ? orow : hrow, c, H, v); };  // in a later pass
   auto squares = [&](const float* v, double s) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fma((double)v[i], (double)v[i], s);
@@ -113,13 +109,19 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_q(NormArgs a) {
 
   double ss = 0.0;
   if constexpr (NC > 0) {
+    float u[NC][8];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) sum(tid + T * i, g[i]);
+    for (int i = 0; i < NC; ++i) fetch(tid + T * i, g[i], u[i]);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) ss = squares(g[i], ss);
+    for (int i = 0; i < NC; ++i) {
+      sum(tid + T * i, g[i], u[i]);
+      ss = squares(g[i], ss);
+    }
   } else {
     for (int c = tid; c < chunks; c += T) {
-      sum(c, g[0]);
+      float u[8];
+      fetch(c, g[0], u);
+      sum(c, g[0], u);
       ss = squares(g[0], ss);
     }
   }
@@ -129,8 +131,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_q(NormArgs a) {
   // g * gain of a chunk, and the largest of them
   auto gained = [&](int c, const float* v, double* p) {
     float w[8];
-    if (a.gain && 8 * c < H) {
-      load8<MOE_DTYPE_F32, VEC>(a.gain, 8 * c, H, w);
+    if (a.gain) {
+      load8<MOE_DTYPE_F32, VEC>(a.gain, c, H, w);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = 1.0f;
@@ -149,16 +151,17 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_q(NormArgs a) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = (float)(p[i] * inv);
-    uint16_t* o = a.out + row * H + 8 * c;
+    uint16_t* o = a.out + row * H;
     if constexpr (VEC) {
+      if (8 * c >= H) return;
       u32x4 d;
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[i] = pack2<MOE_DTYPE_BF16>(v[2 * i], v[2 * i + 1]);
-      *reinterpret_cast<u32x4*>(o) = d;
+      reinterpret_cast<u32x4*>(o)[c] = d;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (8 * c + i < H) o[i] = f32_to_bf16(v[i]);
+        if (element<VEC>(c, i) < H) o[element<VEC>(c, i)] = f32_to_bf16(v[i]);
     }
   };
 
@@ -168,11 +171,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_q(NormArgs a) {
       const double m = lanes_max64<kLanes>(gained(c, v, p));
       const NormScale s = norm_scale(m, inv, 448.0);
       if (tid % kLanes == 0) a.scale[(size_t)(c / kLanes) * a.rows + row] = s.stored;
-      if (8 * c >= H) return;
       float t[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] = f8_quotient(p[i] * s.mul);
-      store8_codes<VEC>(static_cast<uint8_t*>(a.q) + row * H, 8 * c, H, s.zero ? u32x2{0u, 0u} : f8_pack(t));
+      store8_codes<VEC>(static_cast<uint8_t*>(a.q) + row * H, c, H, s.zero ? u32x2{0u, 0u} : f8_pack(t));
       if (a.out) put_out(c, p);
     };
     // a block's 16 lanes take the same turn: T is a multiple of them
@@ -217,7 +219,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_norm_q(NormArgs a) {
         const int k = s.zero ? 0 : (int)fmin(fmax(rint(p[i] * s.mul), -127.0), 127.0);
         o[i / 4] |= ((uint32_t)k & 0xFFu) << (i % 4 * 8);
       }
-      store8_codes<VEC>(static_cast<uint8_t*>(a.q) + row * H, 8 * c, H, o);
+      store8_codes<VEC>(static_cast<uint8_t*>(a.q) + row * H, c, H, o);
       if (a.out) put_out(c, p);
     };
     if constexpr (NC > 0) {
@@ -246,9 +248,17 @@ static void norm_dt(NormArgs a, hipStream_t s) {
   for (a.row0 = 0; a.row0 < a.rows; a.row0 += kRows) {
     const int n = a.rows - a.row0 < kRows ? a.rows - a.row0 : kRows;
 #define NORM(VEC, T, NC, grid) \
-  hipLaunchKernelGGL((k_norm_q<DT, F8, VEC, T, NC>), dim3(grid), dim3(T < 256 ? 256 : T), 0, s, a)
-    if (vec && chunks <= 1024) NORM(true, 256, 4, n);
-    else NORM(false, 256, 0, n);
+  hipLaunchKernelGGL((k_norm_q<DT, F8, VEC, T, NC>), dim3(grid), dim3((T) < 256 ? 256 : (T)), 0, s, a)
+    // A row a wave up to 1024 elements (65536 rows of 1024: 140 us, with 4 waves 164, 8 waves 261; of
+    // 256: 50, 105, 206); above, 8 waves, or 16 where rows are few and time is latency (7168 elements, 1
+    // row: 5.6 and 5.2 us, 2048 rows: 34.9 and 35.7, 16384 rows: 241 and 248; 4 waves 7.5, 39.8, 257).
+    if (vec && chunks <= 128) NORM(true, 64, 2, (n + 3) / 4);
+    else if (vec && chunks <= 1024 && n > 256) NORM(true, 512, 2, n);
+    else if (vec && chunks <= 1024) NORM(true, 1024, 1, n);
+    else if (vec) NORM(true, 1024, 0, n);
+    else if (chunks <= 128) NORM(false, 64, 2, (n + 3) / 4);
+    else if (chunks <= 1024) NORM(false, 512, 2, n);
+    else NORM(false, 1024, 0, n);
 #undef NORM
   }
 }

@@ -4,40 +4,55 @@
 
 namespace moe {
 
-// 16 lanes take a block; a workgroup takes one block of each of 16 rows, so that the
-// 16 scales it writes lie side by side.
-template <int DT, bool VEC>
+// 16 lanes take a block, and U blocks one after another with all their loads in flight; a
+// workgroup takes them of 16 rows, so that the scales it writes lie 16 side by side.
+template <int DT, bool VEC, int U>
 __global__ __launch_bounds__(256) void k_quant_f8(const void* __restrict__ x, size_t x_stride, int row0, int rows,
-                                                  int K, unsigned blocks, uint8_t* __restrict__ q,
+                                                  int K, unsigned blocks, unsigned groups, uint8_t* __restrict__ q,
                                                   float* __restrict__ scale) {
-  const unsigned b = blockIdx.x % blocks;
-  const size_t row = row0 + (size_t)(blockIdx.x / blocks) * 16 + threadIdx.x / kLanes;
+  const unsigned b = blockIdx.x % groups * U;
+  const size_t row = row0 + (size_t)(blockIdx.x / groups) * 16 + threadIdx.x / kLanes;
   if (row >= (size_t)rows) return;
-  const int lane = threadIdx.x % kLanes, at = (int)b * kBlock + 8 * lane;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const bool any = at < K;
-  if (any) load8<DT, VEC>(static_cast<const char*>(x) + row * x_stride * Elem<DT>::bytes, at, K, v);
-  uint32_t m = 0;
+  const int lane = threadIdx.x % kLanes, c = (int)b * kLanes + lane;
+  const char* src = static_cast<const char*>(x) + row * x_stride * Elem<DT>::bytes;
+  float v[U][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
-  const F8Scale s = f8_scale(block_max_bits(m));
-  if (lane == 0) scale[(size_t)b * rows + row] = s.stored;
-  if (any) store8_codes<VEC>(q + row * K, at, K, f8_quant8(v, s));
+  for (int u = 0; u < U; ++u) load8<DT, VEC>(src, c + u * kLanes, K, v[u]);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (b + u >= blocks) return;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[u][i]));
+    const F8Scale s = f8_scale(block_max_bits(m));
+    if (lane == 0) scale[(size_t)(b + u) * rows + row] = s.stored;
+    store8_codes<VEC>(q + row * K, c + u * kLanes, K, f8_quant8(v[u], s));
+  }
+}
+
+template <int DT, bool VEC, int U>
+static void quant_launch(const void* x, size_t x_stride, int rows, int K, uint8_t* q, float* scale, hipStream_t s) {
+  const unsigned blocks = (K + kBlock - 1) / kBlock, groups = (blocks + U - 1) / U;
+  // a launch holds at most 2^31 threads: long calls go in pieces of whole rows
+  const size_t most = ((size_t)1 << 31) / 256 / groups * 16, step = most < (size_t)rows ? most : rows;
+  for (size_t r0 = 0; r0 < (size_t)rows; r0 += step) {
+    const size_t n = rows - r0 < step ? rows - r0 : step;
+    hipLaunchKernelGGL((k_quant_f8<DT, VEC, U>), dim3((unsigned)((n + 15) / 16 * groups)), dim3(256), 0, s, x, x_stride,
+                       (int)r0, rows, K, blocks, groups, q, scale);
+  }
 }
 
 template <int DT>
 static void quant_dt(const void* x, size_t x_stride, int rows, int K, uint8_t* q, float* scale, hipStream_t s) {
   const bool vec = K % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
                    (rows == 1 || x_stride * Elem<DT>::bytes % 16 == 0) && reinterpret_cast<uintptr_t>(q) % 8 == 0;
-  const unsigned blocks = (K + kBlock - 1) / kBlock;
-  // a launch holds at most 2^31 threads: long calls go in pieces of whole rows
-  const int step = (int)((((size_t)1 << 31) / 256 / blocks) * 16 < (size_t)rows ? (((size_t)1 << 31) / 256 / blocks) * 16 : rows);
-  for (size_t r0 = 0; r0 < (size_t)rows; r0 += step) {
-    const size_t n = rows - r0 < (size_t)step ? rows - r0 : step;
-    const dim3 grid((unsigned)((n + 15) / 16 * blocks)), block(256);
-    if (vec) hipLaunchKernelGGL((k_quant_f8<DT, true>), grid, block, 0, s, x, x_stride, (int)r0, rows, K, blocks, q, scale);
-    else hipLaunchKernelGGL((k_quant_f8<DT, false>), grid, block, 0, s, x, x_stride, (int)r0, rows, K, blocks, q, scale);
-  }
+  // Two blocks a lane where there is work for all CUs (32768 rows of 1536 bf16: 33.0 us for 36.5, four 33.8;
+  // 509 rows of 7056 fp16: 5.7 for 5.3).
+  const bool two = ((size_t)rows + 15) / 16 * ((K + kBlock - 1) / kBlock) >= 4096;
+#define QUANT(VEC, U) quant_launch<DT, VEC, U>(x, x_stride, rows, K, q, scale, s)
+  if (vec) two ? QUANT(true, 2) : QUANT(true, 1);
+  else two ? QUANT(false, 2) : QUANT(false, 1);
+#undef QUANT
 }
 
 hipError_t launch_quant_f8(const void* x, int dtype, size_t x_stride, int rows, int K, uint8_t* q, float* scale,
