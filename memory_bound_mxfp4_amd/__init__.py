@@ -707,7 +707,7 @@ def quant_rows_f8(x, q=None, scale=None, stream=None):
 
 
 def _codes_out(q, scale, rows: int, k: int, f8: bool, device, stream):
-    torch = _torch()
+    torch = _module or _torch()
     dtype = torch.float8_e4m3fn if f8 else torch.int8
     shape = (_blocks(k), rows) if f8 else (rows,)
     q = _empty((rows, k), dtype, device, stream) if q is None else _want(q, (rows, k), dtype, device, "q")
@@ -717,27 +717,29 @@ def _codes_out(q, scale, rows: int, k: int, f8: bool, device, stream):
 
 
 def _norm_q(what: str, f8: bool, h, t, gain, eps, h_out, out, q, scale, stream):
-    torch = _torch()
+    torch = _module or _torch()
     rows, hidden, stride = _rows(h, "h")
-    dev = h.device
-    if h.dtype != torch.float32:
+    dev, shape, f32 = h.device, h.shape, torch.float32
+    if h.dtype != f32:
         raise ValueError(f"h must be float32, not {h.dtype}")
+    at = h.data_ptr()
+    t_at = out_at = gain_at = None
     code = t_stride = 0
     if t is not None:
-        t_rows, t_cols, t_stride = _rows(t, "t")
-        if (t_rows, t_cols) != (rows, hidden) or t.device != dev:
-            raise ValueError(f"t must have the shape of h on its device, not {(t_rows, t_cols)} on {t.device}")
-        code = _dtype_code(t.dtype, "t")
-        h_out = _want(h if h_out is None else h_out, (rows, hidden), torch.float32, dev, "h_out")
+        if t.shape != shape or t.device != dev:
+            raise ValueError(f"t must have the shape of h on its device, not {tuple(t.shape)} on {t.device}")
+        t_stride = hidden if t.is_contiguous() else _rows(t, "t")[2]
+        code, t_at = _dtype_code(t.dtype, "t"), t.data_ptr()
+        h_out = _want(h if h_out is None else h_out, shape, f32, dev, "h_out").data_ptr()
     elif h_out is not None:
         raise ValueError("h_out goes with t, and only with it")
     if gain is not None:
-        _want(gain, (hidden,), torch.float32, dev, "gain")
+        gain_at = _want(gain, (hidden,), f32, dev, "gain").data_ptr()
     if out is not None:
-        _want(out, (rows, hidden), torch.bfloat16, dev, "out")
+        out_at = _want(out, shape, torch.bfloat16, dev, "out").data_ptr()
     q, scale = _codes_out(q, scale, rows, hidden, f8, dev, stream)
-    _launch(what, dev, stream, _addr(h), stride, _addr(t), code, t_stride, _addr(gain), rows, hidden, float(eps),
-            _addr(h_out), _addr(out), _addr(q), _addr(scale))
+    _launch(what, dev, stream, at, stride, t_at, code, t_stride, gain_at, rows, hidden, float(eps), h_out, out_at,
+            q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
