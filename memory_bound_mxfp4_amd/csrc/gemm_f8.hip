@@ -79,6 +79,14 @@ __device__ __forceinline__ void load_floats_to_lds(const float* src, float* dst)
   __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)dst, 4, 0, 0);
 }
 
+// The lane's number, as something the compiler knows nothing about: what is computed from it inside a
+// loop is not kept in registers throughout.
+__device__ __forceinline__ int lane_here() {
+  int l = threadIdx.x & 63;
+  asm volatile("" : "+v"(l));
+  return l;
+}
+
 // Where the scales of a matrix lie: of expert e, part p (gate, up), block `nb` of its rows.
 __device__ __forceinline__ const float* w_scales(const F8Args& a, int e, int P, int p, int nb) {
   const int kb = (a.k + kBlock - 1) / kBlock, blocks = (a.n + kBlock - 1) / kBlock;
@@ -360,24 +368,26 @@ struct TileCfg {
   static constexpr int MF = BM / WGM / 16, NF = BN / WGN / 16, MO = MF / KG;  // fragments of a wave, rows of them it stores
   static constexpr bool SPLIT = BM == 64 && BN == 64;  // K may be split over workgroups
   static constexpr int STAGE = (BM + BN) * KS, RING = ST * STAGE;
+  static constexpr bool TWO = RING <= 65536;             // two workgroups to a CU
+  static constexpr bool ON = KG == 1 && !WIDE && !TWO;  // a workgroup goes on from tile to tile
   static constexpr int SL = MF == 4 ? 2 : 1;           // loads of a stage's scales, 64 floats each
   static constexpr int SCALES = ST * NW * SL * 64;     // floats
 };
 
 // Stores a wave's sums: its fragment rows from `first` on.  Register
 // c of acc[i][j] of lane 16 q + r: matrix row 16 j + 4 q + c, row 16 i + r of x.
-template <int DT, class C>
-__device__ __forceinline__ void tile_store(const F8Args& a, const Tile& t, const int* yr, int i0, int wm, int wn,
+template <int DT, class C, class R>
+__device__ __forceinline__ void tile_store(const F8Args& a, const Tile& t, const R& row_of, int i0, int wm, int wn,
                                            int first, const f32x4 (&acc)[C::MO][C::NF]) {
   constexpr int P = C::P, OB = Elem<DT>::bytes, V = 16 / OB;
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int lane = lane_here(), r = lane & 15, q = lane >> 4;
   const bool whole = a.n % V == 0;  // 16-byte stores stay aligned, and a chunk is inside the row or outside
   const int c0 = i0 + wn * (C::BN / C::WGN / P);
 #pragma unroll
   for (int i = 0; i < C::MO; ++i) {
     const int m = 16 * (C::WGM * (first + i) + wm) + r;
     if (m - r >= t.rows) break;
-    const size_t row = (size_t)yr[m] * a.n;
+    const size_t row = (size_t)row_of(m) * a.n;
     // Gates below -80 are rare: the row is stored as if there were none, and once more if
     // there are.
     float lowest = 0.0f;
@@ -451,8 +461,8 @@ __device__ __forceinline__ void tile_store_part(const F8Args& a, const Tile& t, 
 }
 
 // The end of a tile: its outputs, or its part of the sums.
-template <class C>
-__device__ __forceinline__ void tile_end(const F8Args& a, const Tile& t, const int* yr, int i0, int tn, int tiles_n,
+template <class C, class R>
+__device__ __forceinline__ void tile_end(const F8Args& a, const Tile& t, const R& row_of, int i0, int tn, int tiles_n,
                                          int wm, int wn, int parts, int part, int first,
                                          const f32x4 (&acc)[C::MO][C::NF]) {
   if constexpr (C::SPLIT) {
@@ -461,104 +471,176 @@ __device__ __forceinline__ void tile_end(const F8Args& a, const Tile& t, const i
       return;
     }
   }
-  if constexpr (C::WIDE) tile_store<MOE_DTYPE_F32, C>(a, t, yr, i0, wm, wn, first, acc);
-  else if (a.y_dtype == MOE_DTYPE_BF16) tile_store<MOE_DTYPE_BF16, C>(a, t, yr, i0, wm, wn, first, acc);
-  else tile_store<MOE_DTYPE_F16, C>(a, t, yr, i0, wm, wn, first, acc);
+  if constexpr (C::WIDE) tile_store<MOE_DTYPE_F32, C>(a, t, row_of, i0, wm, wn, first, acc);
+  else if (a.y_dtype == MOE_DTYPE_BF16) tile_store<MOE_DTYPE_BF16, C>(a, t, row_of, i0, wm, wn, first, acc);
+  else tile_store<MOE_DTYPE_F16, C>(a, t, row_of, i0, wm, wn, first, acc);
 }
 
 template <class C>
-__global__ __launch_bounds__(C::T, C::RING <= 65536 ? 4 : 2) void k_f8_tile(F8Args a, int tiles_n, int tiles_m, int parts, int band_rows) {
+__global__ __launch_bounds__(C::T, C::TWO ? 4 : 2) void k_f8_tile(F8Args a, int tiles_n, int tiles_m, int parts, int band_rows) {
   constexpr int BM = C::BM, BN = C::BN, WGM = C::WGM, WGN = C::WGN, P = C::P, ST = C::ST, NW = C::NW, MF = C::MF,
                 KG = C::KG, NF = C::NF, GX = BM / 8, L = (BM + BN) / 8 / NW, SL = C::SL;  // L: row loads of a wave and stage
   static_assert(L * 8 * NW == BM + BN && NF % 2 == 0 && ST % KG == 0 && GX == NW * MF && (KG == 1 || NW == 4), "tile");
-  // the ring, then the scales of its stages, then the tile's output rows
-  __shared__ __attribute__((aligned(1024))) int8_t lds[C::RING + 4 * C::SCALES + 4 * BM];
+  constexpr bool ON = C::ON;
+  // the ring, then the scales of its stages, then the rows of this tile, the next and the one before
+  __shared__ __attribute__((aligned(1024))) int8_t lds[C::RING + 4 * C::SCALES + 4 * BM * (ON ? 3 : 1)];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kg = wave / NW, wv = wave % NW;
-  const int wm = wv % WGM, wn = wv / WGM;
+  const int wm = wv % WGM, wn = wv / WGM, K = a.k;
+  float* scales = reinterpret_cast<float*>(lds + C::RING);
+  int* order = reinterpret_cast<int*>(scales + C::SCALES);
   // a grouped product's grid is sized for the most tiles its slots can make: the
   // XCDs share the ones there are
-  const TileAt at = tile_at(blockIdx.x, tiles_n, tiles_m, a.order ? a.num_tiles[0] : tiles_m, parts, band_rows);
-  if (!at.any) return;
-  const int tn = at.tn, tm = at.tm, part = at.part;
-  Tile t;
-  if (!find_tile<BM>(a, tm, t)) return;
-  const int K = a.k, i0 = tn * (BN / P);  // first output column
-  if (t.e >= a.num_experts) {
-    zero_rows(a, t, i0, BN / P, C::T);
-    return;
+  const int count = a.order ? a.num_tiles[0] : tiles_m;
+  struct Place {
+    Tile t;
+    int i0, tn, part;  // first output column, its tile, part of a split K
+    bool any;
+  };
+  // The first tile from workgroup number `block` on, in steps of the grid; those of slots without
+  // an expert are dealt with here.
+  auto locate = [&](unsigned block) {
+    Place o{};
+    for (;; block += gridDim.x) {
+      const TileAt at = tile_at(block, tiles_n, tiles_m, count, parts, band_rows);
+      if (!at.any) return o;
+      o.tn = at.tn;
+      o.part = at.part;
+      o.i0 = at.tn * (BN / P);
+      if (!a.order) {
+        o.t = Tile{0, at.tm * BM, min(BM, a.rows - at.tm * BM)};
+      } else {
+        // a scalar load, which waits for no vector load or store
+        uint64_t d;
+        asm volatile("s_load_dwordx2 %0, %1, 0x0\n\ts_waitcnt lgkmcnt(0)" : "=s"(d) : "s"(a.tiles + at.tm) : "memory");
+        o.t.e = (int)d & 0xFFFF;
+        o.t.p0 = (int)(d >> 32);
+        o.t.rows = min(min((int)d >> 16, BM), a.rows - o.t.p0);
+        if (o.t.e > a.num_experts || o.t.p0 < 0 || o.t.rows <= 0) continue;
+        if (o.t.e == a.num_experts) {
+          zero_rows(a, o.t, o.i0, BN / P, C::T);
+          continue;
+        }
+      }
+      o.any = true;
+      return o;
+    }
+  };
+  // The rows of y that a tile writes, by position in it: straight into place `at` of LDS.
+  auto bring_rows = [&](const Tile& t, int at) {
+    if (64 * wave < BM)
+      load_floats_to_lds(reinterpret_cast<const float*>(a.order + min(t.p0 + 64 * wave + lane_here(), a.rows - 1)),
+                         reinterpret_cast<float*>(order + at * BM + 64 * wave));
+  };
+  auto y_row_at = [&](const Tile& t, int at, int m) {
+    m = min(m, t.rows - 1);
+    return a.order ? (int)min((unsigned)order[at * BM + m], (unsigned)(a.rows - 1)) : t.p0 + m;
+  };
+  unsigned block = blockIdx.x;
+  Place cur = locate(block);
+  if (!cur.any) return;
+  int place = 0;
+  if (a.order) {
+    bring_rows(cur.t, 0);
+    wait_vm<0>();
+    meet();
   }
-  float* scales = reinterpret_cast<float*>(lds + C::RING);
-  int* yr = reinterpret_cast<int*>(scales + C::SCALES);
-  for (int i = threadIdx.x; i < BM; i += C::T) yr[i] = y_row(a, t.p0 + min(i, t.rows - 1));
-  __syncthreads();
   // Loads: a wave copies 8 rows x 128 codes at a time; lane l brings chunk
   // (l ^ row) & 7 of row l >> 3, so that the same 16-byte chunk of 8 consecutive
   // rows lies in 8 different bank groups when a fragment reads it.
   const int lr = lane >> 3, chunk = (lane ^ lr) & 7;
-  const int8_t* src[L];
-#pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const int g = wv + NW * i;  // group of 8 rows: first those of x, then the matrix's
-    if (g < GX) {
-      src[i] = a.x + (size_t)x_row(a, yr[8 * g + lr]) * a.x_stride + 16 * chunk;
-    } else {
-      const int gw = 8 * (g - GX);  // first row of the tile's matrix part; P 2: 16 gate rows, 16 up rows, ...
-      const int n = min(i0 + (P == 2 ? gw / 32 * 16 + gw % 16 : gw) + lr, a.n - 1);
-      src[i] = a.w + (((size_t)t.e * P + (P == 2 ? gw / 16 % 2 : 0)) * a.n + n) * K + 16 * chunk;
-    }
-  }
   // Scales: lane 16 i + r brings that of row r of the wave's fragment row i, the lanes behind
   // them (or a load of their own) those of the wave's matrix rows.
-  const int nb = (i0 + wn * (BN / WGN / P)) / kBlock;
+  const int8_t* src[MF];     // rows of x
+  uint32_t w_off[L - MF];    // rows of the matrix, from the tile's first one: at most 255 * 65536 bytes on
+  const int8_t* w_base[P];   // those first rows, the same for all lanes
+  const float *scale0, *w0;
   const bool of_x = lane < 16 * MF;
-  const float* w0 = w_scales(a, t.e, P, P == 2 ? lane & 1 : 0, nb);
-  const float* scale0 = of_x ? a.x_scale + x_row(a, yr[16 * (WGM * (lane >> 4) + wm) + r]) : w0;
   const uint32_t scale_step = of_x ? (uint32_t)a.x_rows : 1u;
   float* my_scales = scales + wv * SL * 64;
   constexpr int SW = SL == 2 ? 64 : 16 * MF;  // where the matrix's scales lie, gate and up in turn
+  auto aim = [&](const Place& c, int at) {  // at a tile
+    const int lane = lane_here(), lr = lane >> 3, chunk = (lane ^ lr) & 7, r = lane & 15;
+#pragma unroll
+    for (int i = 0; i < MF; ++i)  // a load is of 8 rows: those of x first, then the matrix's
+      src[i] = a.x + (size_t)x_row(a, y_row_at(c.t, at, 8 * (wv + NW * i) + lr)) * a.x_stride + 16 * chunk;
+#pragma unroll
+    for (int i = 0; i < L - MF; ++i) {
+      const int gw = 8 * (wv + NW * (MF + i) - GX);  // first row of the tile's matrix part; P 2: 16 gate rows, 16 up rows, ...
+      const int n = min((P == 2 ? gw / 32 * 16 + gw % 16 : gw) + lr, a.n - 1 - c.i0);
+      w_off[i] = (uint32_t)(n * K + 16 * chunk);
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) w_base[p] = a.w + (((size_t)c.t.e * P + p) * a.n + c.i0) * K;
+    w0 = w_scales(a, c.t.e, P, P == 2 ? lane & 1 : 0, (c.i0 + wn * (BN / WGN / P)) / kBlock);
+    scale0 = of_x ? a.x_scale + x_row(a, y_row_at(c.t, at, 16 * (WGM * (lane >> 4) + wm) + r)) : w0;
+  };
   // Where this lane's chunks of the wave's first fragments and its scales lie in the buffer that is read: moved on from
   // stage to stage, so that all else are constants in the instructions and no address takes a register of its own.
   int x_at[2], w_at[2], sx_at, sw_at;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int at = kg * C::STAGE + r * KS + 16 * ((4 * h + q) ^ (r & 7));
-    x_at[h] = at + 16 * wm * KS;
-    w_at[h] = at + (BM + wn * (BN / WGN)) * KS;
-  }
   constexpr int SCALE_STAGE = 4 * NW * SL * 64;  // bytes
-  sw_at = C::RING + kg * SCALE_STAGE + 4 * wv * SL * 64;
-  sx_at = sw_at + 4 * r;
+  auto first_buffer = [&]() {
+    const int lane = lane_here(), r = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = kg * C::STAGE + r * KS + 16 * ((4 * h + q) ^ (r & 7));
+      x_at[h] = at + 16 * wm * KS;
+      w_at[h] = at + (BM + wn * (BN / WGN)) * KS;
+    }
+    sw_at = C::RING + kg * SCALE_STAGE + 4 * wv * SL * 64;
+    sx_at = sw_at + 4 * r;
+  };
 
+  // Group kg has stages kg, kg + KG, ... of the workgroup's n, its t-th in buffer KG (t % R) + kg.
+  constexpr int R = ST / KG;
   const int stages = (K + KS - 1) / KS;
-  const int s0 = (int)((size_t)stages * part / parts), S = (int)((size_t)stages * (part + 1) / parts);
+  const int s0 = (int)((size_t)stages * cur.part / parts), S = (int)((size_t)stages * (cur.part + 1) / parts);
+  const int n = S - s0, mine = (n - kg + KG - 1) / KG, turns = (n + KG - 1) / KG;
+  auto stage_of = [&](int t) { return s0 + KG * t + kg; };
+  // load number i, of a row group or of scales, of stage st to buffer b; WHOLE: the stage has 128 codes
+  auto load_rows = [&](int st, int b, int i, auto whole) {
+    int8_t* dst = lds + b * C::STAGE + 1024 * (wv + NW * i);
+    const int k = st * KS + 16 * chunk;
+    constexpr bool W = decltype(whole)::value;
+    if (i < MF) {  // past K: zeros on this side, times codes of the matrix that are there
+      if constexpr (W) load_to_lds(src[i] + st * KS, dst);
+      else load_to_lds(k >= K ? kZeroCodes : src[i] + st * KS, dst);
+    } else {
+      const int8_t* base = w_base[P == 2 ? (wv + NW * i - GX) / 2 % 2 : 0] + (size_t)st * KS;
+      if constexpr (W) load_to_lds(base + w_off[i - MF], dst);
+      else load_to_lds(base + (int)(w_off[i - MF] - (k > K - 16 ? k - (K - 16) : 0)), dst);
+    }
+  };
+  auto load_scales = [&](int st, int b, int i) {
+    float* dst = my_scales + b * (NW * SL * 64);
+    if (i == 0) load_floats_to_lds(scale0 + (size_t)(uint32_t)st * scale_step, dst);
+    else load_floats_to_lds(w0 + st, dst + 64);
+  };
+  auto first_loads = [&]() {  // of a tile: R stages
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      if (t >= mine) break;
+#pragma unroll
+      for (int i = 0; i < L; ++i) load_rows(stage_of(t), KG * t + kg, i, std::false_type{});
+#pragma unroll
+      for (int i = 0; i < SL; ++i) load_scales(stage_of(t), KG * t + kg, i);
+    }
+  };
+  aim(cur, 0);
+  first_loads();
+  // Loads and stores complete in their order.  The first R waits of a tile are for loads that were issued
+  // before the NST stores of the tile before (if it was a whole one), and leave them out: `slack` of them to come.
+  constexpr int NST = ON ? C::MO * (NF / P) / 2 : 0;
+  int slack = 0;
+  Place next{};
   f32x4 acc[MF][NF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   // With U of the MF fragment rows: a tile whose last rows are missing (the end of an
   // expert) neither loads nor multiplies them.
   auto run = [&](auto used) {
     constexpr int U = decltype(used)::value, LU = L - MF + U + SL;  // loads of a stage
-    // load number i of stage st to buffer b; WHOLE: the stage has 128 codes
     auto load_one = [&](int st, int b, int i, auto whole) {
-      int8_t* buf = lds + b * C::STAGE;
-      if (i >= LU - SL) {
-        float* dst = my_scales + b * (NW * SL * 64);
-        if (i == LU - SL) load_floats_to_lds(scale0 + (size_t)(uint32_t)st * scale_step, dst);
-        else load_floats_to_lds(w0 + st, dst + 64);
-        return;
-      }
-      const int g = i < U ? i : i - U + MF;
-      int8_t* dst = buf + 1024 * (wv + NW * g);
-      // past K: zeros on x's side, times codes of the matrix that are there
-      if constexpr (decltype(whole)::value) {
-        load_to_lds(src[g] + st * KS, dst);
-      } else {
-        const int k = st * KS + 16 * chunk;
-        load_to_lds(g < MF && k >= K ? kZeroCodes : src[g] + (min(k, K - 16) - 16 * chunk), dst);
-      }
+      if (i >= LU - SL) load_scales(st, b, i - (LU - SL));
+      else load_rows(st, b, i < U ? i : i - U + MF, whole);
     };
     auto load = [&](int st, int b) {
 #pragma unroll
@@ -642,23 +724,40 @@ __global__ __launch_bounds__(C::T, C::RING <= 65536 ? 4 : 2) void k_f8_tile(F8Ar
         for (int p = 0; p < P; ++p) scale[i][p] = 0.0f;
     }
 
-    // Group kg has stages kg, kg + KG, ... of the workgroup's n, its t-th in buffer KG (t % R) + kg.
-    constexpr int R = ST / KG;
-    const int n = S - s0, mine = (n - kg + KG - 1) / KG, turns = (n + KG - 1) / KG;
-    auto stage_of = [&](int t) { return s0 + KG * t + kg; };
     // waits until all loads of this wave but those of the `later` newest stages have landed
     auto landed = [&](int later) {
-      if (later >= 3) wait_vm<3 * LU>();
-      else if (later == 2) wait_vm<2 * LU>();
-      else if (later == 1) wait_vm<LU>();
-      else wait_vm<0>();
+      if (NST && slack > 0) {
+        --slack;
+        if (later >= 3) wait_vm<3 * LU + NST>();
+        else if (later == 2) wait_vm<2 * LU + NST>();
+        else if (later == 1) wait_vm<LU + NST>();
+        else wait_vm<NST>();
+      } else {
+        if (later >= 3) wait_vm<3 * LU>();
+        else if (later == 2) wait_vm<2 * LU>();
+        else if (later == 1) wait_vm<LU>();
+        else wait_vm<0>();
+      }
     };
-    auto first_columns = [&]() {
+    // Of a stage's loads, FA are issued with the last columns of the stage whose buffer they take, the other FB
+    // with the first columns of the next: a wave that waits to issue a load multiplies nothing.
+    // (8192 x 8192 x 7168 404.5 us with all of them there, 403.4 with a third here, 411 with half; 2 x 1536, K 7168,
+    // 16384 rows: 314, 307, 310.)
+    constexpr int FB = F0 > 0 ? LU / 3 : 0, FA = LU - FB;
+    // The first columns; `loads`: with the rest of stage st's to buffer b.
+    auto first_columns = [&](int st, int b, auto loads) {
 #pragma unroll
       for (int j = 0; j < NF - 2; ++j) {
         read_w(j + 2);
 #pragma unroll
-        for (int i = 0; i < U; ++i) slot(j * U + i);
+        for (int i = 0; i < U; ++i) {
+          const int f = j * U + i;
+          slot(f);
+          if constexpr (decltype(loads)::value && FB > 0) {
+#pragma unroll
+            for (int l = 2 * f * FB / F0; l < 2 * (f + 1) * FB / F0 && l < FB; ++l) load_one(st, b, FA + l, std::true_type{});
+          }
+        }
       }
     };
     static_assert(NF == 2 || NF % 4 == 0, "buffers of the columns");
@@ -679,7 +778,7 @@ __global__ __launch_bounds__(C::T, C::RING <= 65536 ? 4 : 2) void k_f8_tile(F8Ar
           if (g % 2) read_x(g / 2);
         if constexpr (decltype(loads)::value) {
 #pragma unroll
-          for (int i = g * LU / (2 * U); i < (g + 1) * LU / (2 * U); ++i) load_one(st, b, i, std::true_type{});
+          for (int i = g * FA / (2 * U); i < (g + 1) * FA / (2 * U); ++i) load_one(st, b, i, std::true_type{});
         }
       }
       if constexpr (decltype(next)::value && NF == 2) {
@@ -699,34 +798,39 @@ __global__ __launch_bounds__(C::T, C::RING <= 65536 ? 4 : 2) void k_f8_tile(F8Ar
       meet();
     };
 
-#pragma unroll
-    for (int t = 0; t < R; ++t)
-      if (t < mine) load(stage_of(t), KG * t + kg);
+    first_buffer();
     landed(min(R - 1, mine - 1));
     pass();
     if (mine > 0) first_reads();
-    // Stages that are followed by another and whose loads are whole ones go first, without a branch.
+    // Stages that are followed by another and whose loads are whole ones go first.
     const int loads_whole = (K / KS - s0 - kg + KG - 1) / KG;  // of this group's stages, those of 128 codes come first
     const int ahead = min(mine, loads_whole) - (2 * R - 1);     // the pass at t loads up to stage t + 2 R - 1
     int t = 0;
     for (; t < ahead; t += R) {
 #pragma unroll
       for (int u = 0; u < R; ++u) {
-        first_columns();
-        wait_vm<(R - 2) * LU>();
+        first_columns(stage_of(t + u + R - 1), KG * ((u + R - 1) % R) + kg, std::true_type{});
+        landed(R - 2);
         pass();
         advance(u + 1 == R ? -KG * (R - 1) : KG);
         last_columns(stage_of(t + u + R), KG * u + kg, std::true_type{}, std::true_type{});
       }
     }
+    if (FB > 0 && t > 0) {
+#pragma unroll
+      for (int l = FA; l < LU; ++l) load_one(stage_of(t + R - 1), KG * (R - 1) + kg, l, std::true_type{});
+    }
     // The rest, a stage at a time.
     for (int at = 0; t < turns; ++t, at = at + 1 == R ? 0 : at + 1) {
       const bool there = KG == 1 || t < mine;
-      if (there) first_columns();
+      if (there) first_columns(0, 0, std::false_type{});
       if (t + 1 < turns) {
         landed(min(R - 2, mine - 2 - t));
         pass();
         if (t + R < mine) load(stage_of(t + R), KG * at + kg);
+      } else if (ON && next.any) {  // the last stage has been read, and the next tile's rows are there
+        wait_vm<0>();
+        pass();
       }
       if (there) last_columns(0, 0, std::false_type{}, std::false_type{});
       if (t + 1 < mine) {
@@ -741,39 +845,61 @@ __global__ __launch_bounds__(C::T, C::RING <= 65536 ? 4 : 2) void k_f8_tile(F8Ar
       }
     }
   };
-  const int need = (t.rows + 16 * WGM - 1) / (16 * WGM);
-  if (need >= MF) run(std::integral_constant<int, MF>{});
-  else if (MF == 4 && need == 3) run(std::integral_constant<int, MF == 4 ? 3 : 1>{});
-  else if (MF == 4 && need == 2) run(std::integral_constant<int, MF == 4 ? 2 : 1>{});
-  else run(std::integral_constant<int, 1>{});
-  if constexpr (KG == 1) {
-    tile_end<C>(a, t, yr, i0, tn, tiles_n, wm, wn, parts, part, 0, acc);
-  } else {
-    // each group gives the other half of its fragment rows away and adds what it gets
-    f32x4* swap = reinterpret_cast<f32x4*>(lds) + (wv * C::MO * NF) * 64 + lane;
-    constexpr int HALF = NW * C::MO * NF * 64;
-    static_assert(2 * HALF * 16 <= C::RING, "sums");
-    f32x4 sum[C::MO][NF];
-    __syncthreads();
+  for (;;) {
+    if constexpr (ON) {
+      next = locate(block += gridDim.x);
+      if (next.any && a.order) bring_rows(next.t, place == 2 ? 0 : place + 1);
+    }
 #pragma unroll
-    for (int i = 0; i < C::MO; ++i)
+    for (int i = 0; i < MF; ++i)
 #pragma unroll
-      for (int j = 0; j < NF; ++j) {
-        const f32x4 lower = acc[i][j], upper = acc[C::MO + i][j];  // values: a choice between places would keep acc in memory
-        f32x4 away;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          sum[i][j][c] = kg ? upper[c] : lower[c];
-          away[c] = kg ? lower[c] : upper[c];
-        }
-        swap[kg * HALF + (i * NF + j) * 64] = away;
+      for (int j = 0; j < NF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int need = (cur.t.rows + 16 * WGM - 1) / (16 * WGM);
+    if (need >= MF) run(std::integral_constant<int, MF>{});
+    else if (MF == 4 && need == 3) run(std::integral_constant<int, MF == 4 ? 3 : 1>{});
+    else if (MF == 4 && need == 2) run(std::integral_constant<int, MF == 4 ? 2 : 1>{});
+    else run(std::integral_constant<int, 1>{});
+    if constexpr (ON) {
+      if (next.any) {  // its first stages travel while this tile's outputs are stored
+        aim(next, place == 2 ? 0 : place + 1);
+        first_loads();
       }
-    __syncthreads();
+    }
+    auto row_of = [&](int m) { return y_row_at(cur.t, place, m); };
+    if constexpr (KG == 1) {
+      tile_end<C>(a, cur.t, row_of, cur.i0, cur.tn, tiles_n, wm, wn, parts, cur.part, 0, acc);
+    } else {
+      // each group gives the other half of its fragment rows away and adds what it gets
+      f32x4* swap = reinterpret_cast<f32x4*>(lds) + (wv * C::MO * NF) * 64 + lane;
+      constexpr int HALF = NW * C::MO * NF * 64;
+      static_assert(2 * HALF * 16 <= C::RING, "sums");
+      f32x4 sum[C::MO][NF];
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < C::MO; ++i)
+      for (int i = 0; i < C::MO; ++i)
 #pragma unroll
-      for (int j = 0; j < NF; ++j) sum[i][j] += swap[(1 - kg) * HALF + (i * NF + j) * 64];
-    tile_end<C>(a, t, yr, i0, tn, tiles_n, wm, wn, parts, part, kg * C::MO, sum);
+        for (int j = 0; j < NF; ++j) {
+          const f32x4 lower = acc[i][j], upper = acc[C::MO + i][j];  // values: a choice between places would keep acc in memory
+          f32x4 away;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            sum[i][j][c] = kg ? upper[c] : lower[c];
+            away[c] = kg ? lower[c] : upper[c];
+          }
+          swap[kg * HALF + (i * NF + j) * 64] = away;
+        }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < C::MO; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) sum[i][j] += swap[(1 - kg) * HALF + (i * NF + j) * 64];
+      tile_end<C>(a, cur.t, row_of, cur.i0, cur.tn, tiles_n, wm, wn, parts, cur.part, kg * C::MO, sum);
+    }
+    if (!ON || !next.any) break;
+    const bool all_stores = cur.t.rows == BM && cur.i0 + BN / P <= a.n && a.n % 8 == 0;
+    slack = all_stores ? R : 0;
+    cur = next;
+    place = place == 2 ? 0 : place + 1;
   }
 }
 
@@ -815,7 +941,12 @@ static void tile_launch(const F8Args& a, int max_tiles, int parts, hipStream_t s
     band = (a.rows / a.num_experts + C::BM / 2) / C::BM;
     band = band < 1 ? 1 : band > 8 ? 8 : band;
   }
-  hipLaunchKernelGGL(k_f8_tile<C>, dim3(8 * per_xcd), dim3(C::T), 0, s, a, tiles_n, max_tiles, parts, band);
+  int grid = 8 * per_xcd;
+  if (C::ON) {
+    const int resident = (num_cus() + 7) / 8 * 8;
+    grid = grid < resident ? grid : resident;
+  }
+  hipLaunchKernelGGL(k_f8_tile<C>, dim3(grid), dim3(C::T), 0, s, a, tiles_n, max_tiles, parts, band);
   if constexpr (C::SPLIT) {
     if (parts == 1) return;
     const int cols = (a.n + 255) / 256;
@@ -846,22 +977,45 @@ struct Tiling {
   double d0, d1;           // dense: us a round, and a stage of a round
   double g0, g1, g2, g3, g4;  // grouped, see f8_plan
 };
-constexpr Tiling kTilings[] = {{16, 32, 512, false, 3.3, 0.105, 3.9, 0.88, 0.257, 0.0, 0.06},
-                               {64, 64, 256, true, 3.0, 0.21, 0.4, 2.9, 0.118, 0.106, 0.422},
-                               {64, 128, 256, true, 4.0, 0.30, 0.0, 3.46, 0.173, 0.136, 0.549},
-                               {128, 128, 256, true, 4.5, 0.54, 0.0, 4.58, 0.118, 0.379, 0.354},
-                               {128, 128, 512, false, 6.1, 1.15, 0.0, 4.99, 0.569, 0.0, 0.49},
-                               {256, 256, 256, true, 7.0, 1.4, 0.0, 6.44, 0.869, 0.0, 0.453}};
-constexpr int kStream = 0, kSplit = 1, kTwoToACu = 4, kLargest = 5;
+// With the products of codes, and with those in fp16 (the last two tiles: not for these).
+constexpr Tiling kTilings[2][6] = {{{16, 32, 512, false, 3.5, 0.157, 1.2, 1.25, 0.226, 0.0, 0.075},
+                                    {64, 64, 256, true, 3.55, 0.205, 0.5, 2.9, 0.109, 0.146, 0.422},
+                                    {64, 128, 256, true, 3.7, 0.3, 0.0, 3.55, 0.173, 0.103, 0.374},
+                                    {128, 128, 256, true, 4.2, 0.49, 0.0, 5.43, 0.118, 0.379, 0.389},
+                                    {128, 128, 512, false, 4.5, 1.15, 0.0, 3.59, 0.665, 0.0, 0.418},
+                                    {256, 256, 256, true, 7.0, 1.17, 0.0, 8.42, 0.784, 0.0, 0.314}},
+                                   {{16, 32, 512, false, 3.3, 0.084, 3.46, 0.457, 0.246, 0.0, 0.067},
+                                    {64, 64, 256, true, 3.55, 0.21, 0.4, 3.69, 0.118, 0.164, 0.458},
+                                    {64, 128, 256, true, 4.0, 0.3, 0.0, 3.97, 0.153, 0.182, 0.905},
+                                    {128, 128, 256, true, 3.73, 0.456, 0.0, 4.33, 0.118, 0.535, 0.646}}};
+constexpr int kStream = 0, kSplit = 1, kTwoToACu = 4, kKinds[2] = {6, 4};
 
+// Which kernel a product runs on: the one with the least estimated time.
+// Dense: T workgroups in rounds of those that the card holds, each d0 + d1 * stages.  Up
+// to 16 rows always the stream; with more rows it reads the matrix again for every 16, and is
+// taken where the card holds all its workgroups.  Two 128 x 128 tiles to a CU (two
+// buffers of a stage each) are for more than one round of single ones (four buffers).
+// Measured at N 7168, K 7168: 8 rows 10.6 us (64 x 64 tiles 15.3), 24 rows 19.6; 128 rows:
+// 64 x 64 21.1 us, 64 x 128 28.2, 128 x 128 37.5; 2048 rows: 234, 172, 136 (two to a CU 124),
+// 256 x 256 94; 8192 rows: 864, 642, 489, 451, 366.
+// Grouped: each expert's matrix comes from HBM, an expert's rows end anywhere in a tile
+// (half a tile more on average, of which only the rows that there are cost anything).
+// g0 + rounds * (g1 + g2 * stages) + g3 * stages * rounds' worth of rows + g4 * the time to read
+// the matrices at 6.6 TB/s.  106 experts of 9 rows, 2 x 4172, K 256: the stream 99 us, 64 x 64 93,
+// 128 x 128 40 (two to a CU 35), 256 x 256 41; 12 rows of 84 experts, N 92, K 6112: 6.6, 11.9, 20, 22, 32.
+// Fitted to 1153 products of the sizes in 1 to 8192 rows, N 64 to 8192, K 64 to 8192, 2 to 128
+// experts; on 500 others the choice costs 1.6% over the best kernel on average where it is dense
+// (2.1% in fp16), 5.0% (3.9%) where it is grouped.
+// K is split over parts where 64 x 64 tiles leave most CUs without work and the stages saved
+// are worth adding the parts up (64 rows of N 7168, K 7168: 18.3 us in 2 parts, 21.1 in one;
+// 37 rows of N 1536, K 7168 to fp32: 10.9 in 8 parts, 20.7 in one, 8.9 as a stream).
 F8Plan f8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu, bool wide) {
   const int P = swiglu ? 2 : 1, stages = (k + KS - 1) / KS, used = !grouped ? 1 : rows < experts ? rows : experts;
   const double per = (double)rows / used, read = (double)used * n * P * k / 6.6e6;
   F8Plan best{-1, 0, 1, 0};
   double least = 0.0;
-  for (int kind = 0; kind < (int)(sizeof(kTilings) / sizeof(kTilings[0])); ++kind) {
-    const Tiling& m = kTilings[kind];
-    if (wide && kind == kLargest) continue;
+  for (int kind = 0; kind < kKinds[wide]; ++kind) {
+    const Tiling& m = kTilings[wide][kind];
     const int cols = (n * P + m.bn - 1) / m.bn;
     double time;
     int parts = 1;
@@ -875,7 +1029,7 @@ F8Plan f8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu, b
       if (kind != kStream && time < 1.2 * read) time = 1.2 * read;
     } else {
       const double tiles = (double)((rows + m.bm - 1) / m.bm) * cols;
-      if (kind == kStream ? rows > 16 && tiles > 256.0 : kind == kTwoToACu && tiles <= 256.0) continue;
+      if (kind == kStream ? rows > 16 && tiles > m.resident : kind == kTwoToACu && tiles <= 256.0) continue;
       double load = m.rounds ? ceil(tiles / m.resident) : tiles / m.resident;
       if (load < 1.0) load = 1.0;
       time = kind == kStream && rows <= 16 ? 0.0 : (m.d0 + m.d1 * stages) * load;
@@ -883,7 +1037,7 @@ F8Plan f8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu, b
         parts = (int)(224.0 / tiles);
         if (parts > kMaxParts) parts = kMaxParts;
         if (parts > stages / 6) parts = stages / 6;
-        const double saved = parts > 1 ? m.d1 * (stages - stages / parts) - 8.0 : 0.0;
+        const double saved = parts > 1 ? m.d1 * (stages - stages / parts) - 4.0 : 0.0;
         if (saved <= 0.0) parts = 1;
         else time -= saved;
       }
@@ -900,12 +1054,14 @@ static void tiles_launch(const F8Args& a, const F8Plan& plan, int max_tiles, hip
   if (plan.kind == 1) tile_launch<TileCfg<64, 64, 2, 2, 2, P, 8, WIDE>>(a, max_tiles, plan.parts, s);
   else if (plan.kind == 2) tile_launch<TileCfg<64, 128, 2, 2, 2, P, 6, WIDE>>(a, max_tiles, 1, s);
   else if (plan.kind == 3) tile_launch<TileCfg<128, 128, 4, 2, 1, P, 4, WIDE>>(a, max_tiles, 1, s);
-  else if (plan.kind == 4) tile_launch<TileCfg<128, 128, 4, 2, 1, P, 2, WIDE>>(a, max_tiles, 1, s);
-  else if constexpr (!WIDE) tile_launch<TileCfg<256, 256, 4, 2, 1, P, 2, WIDE>>(a, max_tiles, 1, s);
+  else if constexpr (!WIDE) {
+    if (plan.kind == kTwoToACu) tile_launch<TileCfg<128, 128, 4, 2, 1, P, 2, WIDE>>(a, max_tiles, 1, s);
+    else tile_launch<TileCfg<256, 256, 4, 2, 1, P, 2, WIDE>>(a, max_tiles, 1, s);
+  }
 }
 
 bool f8_launchable(const F8Plan& plan, int n, bool swiglu, int max_tiles) {
-  const size_t bn = kTilings[plan.kind].bn, cols = ((size_t)n * (swiglu ? 2 : 1) + bn - 1) / bn;
+  const size_t bn = kTilings[0][plan.kind].bn, cols = ((size_t)n * (swiglu ? 2 : 1) + bn - 1) / bn;
   return cols * max_tiles * plan.parts < kMaxGroups;
 }
 

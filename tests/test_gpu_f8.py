@@ -317,7 +317,8 @@ def test_gemm_longest_rows(m):
 
 # sizes that reach every kernel, beside SHAPES
 ALL_KERNELS = [(1, 300, 656), (12, 300, 656), (12, 5000, 400), (24, 300, 656), (60, 200, 7184), (60, 1000, 1040), (60, 5000, 272),
-               (200, 1100, 656), (300, 5000, 272), (1000, 2050, 272), (1500, 7000, 144), (2100, 7200, 272)]
+               (500, 400, 7184), (500, 800, 7184), (300, 2500, 272), (300, 5000, 272), (1000, 2050, 272), (1500, 7000, 144),
+               (2040, 8100, 272), (2100, 3600, 400)]
 
 
 def _exact_inputs(m, n, k, lead, seed):
@@ -364,7 +365,8 @@ def test_gemm_exact(m, n, k, swiglu, out):
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("by_slot", [False, True])
 @pytest.mark.parametrize("tokens,top_k,E,n,k", [(1, 4, 8, 300, 272), (9, 3, 16, 600, 400), (60, 4, 3, 300, 656), (300, 4, 8, 520, 272),
-                                                (700, 4, 4, 1100, 400), (2000, 2, 2, 2100, 272)])
+                                                (300, 4, 8, 1200, 272), (130, 4, 16, 1947, 1216), (700, 4, 4, 1100, 400),
+                                                (2000, 2, 2, 2100, 272)])
 def test_experts_exact(tokens, top_k, E, n, k, by_slot, out):
     import torch
     idx = _idx(tokens, top_k, E, tokens)
@@ -458,6 +460,17 @@ def test_experts(tokens, top_k, E, n, k, by_slot, swiglu):
     kinds = ["bf16", "f16", "f32"]
     _experts_case(tokens, top_k, E, n, k, swiglu, by_slot, kinds[(tokens + n) % 3], kinds[(n + k // 16) % 3],
                   codes_in=(tokens + top_k) % 2 == 0)
+
+
+# with SwiGLU, to every kernel: tokens, top_k, experts, n, k, rows by slot
+SWIGLU_EXPERTS = [(9, 3, 16, 300, 400, False), (60, 4, 3, 500, 656, True), (100, 4, 8, 550, 656, False), (300, 4, 8, 600, 272, True),
+                  (258, 2, 16, 985, 1168, False), (700, 4, 4, 550, 400, True), (2000, 2, 2, 1050, 272, False), (1000, 4, 8, 1500, 272, False)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("tokens,top_k,E,n,k,by_slot", SWIGLU_EXPERTS)
+def test_experts_swiglu(tokens, top_k, E, n, k, by_slot, out):
+    _experts_case(tokens, top_k, E, n, k, True, by_slot, "bf16", out, codes_in=tokens % 200 == 0)
 
 
 @pytest.mark.parametrize("swiglu", [False, True])
