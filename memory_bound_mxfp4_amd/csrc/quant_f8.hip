@@ -5,7 +5,9 @@
 namespace moe {
 
 // 16 lanes take a block, and U blocks one after another with all their loads in flight; a
-// workgroup takes them of 16 rows, so that the scales it writes lie 16 side by side.
+// workgroup takes them of 16 rows, so that the scales it writes lie 16 side by side.  Bound by
+// memory: 32768 rows of 1536 bf16 33 to 35 us (4.3 to 4.6 TB/s; a large copy has 5.0), of fp32 46 (5.5); 4096 rows
+// of 4999 fp32, which no wide load fits, 33 (3.1).
 template <int DT, bool VEC, int U>
 __global__ __launch_bounds__(256) void k_quant_f8(const void* __restrict__ x, size_t x_stride, int row0, int rows,
                                                   int K, unsigned blocks, unsigned groups, uint8_t* __restrict__ q,

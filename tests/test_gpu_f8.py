@@ -617,6 +617,88 @@ def test_two_streams_at_once():
     assert all(torch.equal(a, b) for a, b in zip(alone, outs))
 
 
+def test_memory_of_a_call_on_another_stream():
+    """A call given a stream makes its outputs and workspace there: what the current stream allocates and writes while
+    that stream still works never lands in them."""
+    import torch
+    m, n, k, top_k, E = 48, 512, 1024, 2, 4
+    x, _ = _x(m, k, "f32", 1)
+    t, _ = _x(m, k, "bf16", 2)
+    w, ws = _w((E, n, k), 3)
+    w, ws = ref.tensor_of(w), _dev(ws)
+    groups = moe.moe_group_slots(_dev(_idx(m, top_k, E, 4)), E)
+
+    kept = []  # a buffer of the caller's is the caller's to keep while the stream works
+
+    def run(stream):
+        q, qs = moe.quant_rows_f8(x, stream=stream)
+        h = torch.empty_like(x)
+        kept.append(h)
+        nq, ns = moe.residual_add_rmsnorm_f8(x, t, h_out=h, stream=stream)
+        iq, s = moe.residual_add_rmsnorm_i8(x, t, h_out=h, stream=stream)
+        return (q, qs, nq, ns, iq, s, moe.gemm_f8(x, w[0], ws[0], stream=stream),
+                moe.experts_gemm_f8(x, groups, w, ws, stream=stream),
+                moe.gemm_f8(nq, w[0], ws[0], x_scale=ns, out_dtype=torch.bfloat16, stream=stream))
+
+    want = [v.clone() for v in run(None)]
+    need = moe.gemm_f8_workspace_size(m, n, k, False, torch.float32)
+    torch.cuda.synchronize()
+    for as_int in (False, True):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # the calls below wait behind this
+        got = run(side.cuda_stream if as_int else side)
+        trash = [torch.full((size,), 0x55, dtype=torch.uint8, device="cuda")
+                 for size in (need, m * k, 4 * m, 1 << 16, 1 << 12) for _ in range(4)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert all(bool((v == 0x55).all()) for v in trash)
+
+
+@pytest.mark.parametrize("f8", [True, False])
+def test_norm_of_more_rows_than_a_launch_takes(f8):
+    """2^21 + 37 rows go in two launches: the last rows and those around the border are those of a call of their own."""
+    import torch
+    rows, hidden = (1 << 21) + 37, 8
+    call = moe.residual_add_rmsnorm_f8 if f8 else moe.residual_add_rmsnorm_i8
+    h = torch.randn(rows, hidden, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    q, s = call(h)
+    for lo, hi in [(0, 100), ((1 << 21) - 50, (1 << 21) + 10), (rows - 60, rows)]:
+        want, ws = call(h[lo:hi].clone())
+        assert torch.equal(q[lo:hi].view(torch.uint8), want.view(torch.uint8))
+        assert torch.equal((s[:, lo:hi] if f8 else s[lo:hi]), ws)
+
+
+@pytest.mark.parametrize("m,n,k,out", [(40, 300, 272, "bf16"), (600, 520, 272, "bf16"), (600, 520, 272, "f32")])
+def test_experts_of_a_groups_buffer_that_holds_anything(m, n, k, out):
+    """Whatever a groups buffer holds, nothing outside the output is written, and a right one then gives right bits."""
+    import torch
+    top_k, E = 4, 8
+    x, _ = _x(m, k, "bf16", 1)
+    w, ws = _w((E, n, k), 2)
+    w, ws = ref.tensor_of(w), _dev(ws)
+    groups = moe.moe_group_slots(_dev(_idx(m, top_k, E, 3)), E)
+    dtype = getattr(torch, {"bf16": "bfloat16", "f32": "float32"}[out])
+    want = moe.experts_gemm_f8(x, groups, w, ws, out_dtype=dtype)
+    right = groups.buffer.clone()
+    block = torch.empty(64 + m * top_k + 64, n, dtype=dtype, device="cuda")
+    y = block[64:-64]
+    gen = torch.Generator("cuda").manual_seed(4)
+    for fill in (0, 0xFF, 0x7F, 0x01, None):
+        if fill is None:
+            groups.buffer.view(torch.uint8).random_(0, 256, generator=gen)
+        else:
+            groups.buffer.view(torch.uint8).fill_(fill)
+        block.fill_(7)
+        moe.experts_gemm_f8(x, groups, w, ws, out=y)
+        torch.cuda.synchronize()
+        assert bool((block[:64] == 7).all()) and bool((block[-64:] == 7).all())
+    groups.buffer.copy_(right)
+    moe.experts_gemm_f8(x, groups, w, ws, out=y)
+    assert torch.equal(y, want)
+
+
 def test_norm_feeds_the_integer_product():
     """residual_add_rmsnorm_i8 leaves what gemm_i8 takes."""
     import torch
