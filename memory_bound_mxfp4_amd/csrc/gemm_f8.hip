@@ -107,7 +107,7 @@ __device__ __forceinline__ void zero_rows(const A& a, const Tile& t, int i0, int
 // widened to fp16: the vector units have the time.  A stage's scales come in one load: lane
 // r brings that of row r of x, lane 16 + p that of part p of the matrix.
 // 8 rows of N 7168, K 7168 10.8 us (4.8 TB/s), 16 of N 65536 88 us (5.4); 8 tokens with 16 of 128 experts
-// each, SwiGLU of 2 x 1024, K 7168 92 us (6.5; reading alone has 6.7).
+// each, SwiGLU of 2 x 1024, K 7168 92 us (0.63 GB: 6.8, which is what reading alone has).
 template <int NN, int P, int NW, int ST>
 __global__ __launch_bounds__(64 * NW, 2) void k_f8_stream(F8Args a, int tiles_n) {
   constexpr int STAGE = (1 + NN) * 16 * KS, D = 2 * (1 + NN), L = D + 1, COLS = 16 * NN / P, T = 64 * NW;
