@@ -510,12 +510,12 @@ __global__ __launch_bounds__(C::T, C::TWO ? 4 : 2) void k_f8_tile(F8Args a, int 
     int i0, tn, part;  // first output column, its tile, part of a split K
     bool any;
   };
-  // The first tile from workgroup number `block` on, in steps of the grid; those of slots without
-  // an expert are dealt with here.
-  auto locate = [&](unsigned block) {
+  unsigned block = blockIdx.x;
+  // The workgroup's next tile; those of slots without an expert are dealt with here.
+  auto locate = [&]() {
     Place o{};
-    for (;; block += gridDim.x) {
-      const TileAt at = tile_at(block, tiles_n, tiles_m, count, parts, band_rows);
+    for (;;) {
+      const TileAt at = next_tile(block, gridDim.x, tiles_n, tiles_m, count, parts, band_rows);
       if (!at.any) return o;
       o.tn = at.tn;
       o.part = at.part;
@@ -549,8 +549,7 @@ __global__ __launch_bounds__(C::T, C::TWO ? 4 : 2) void k_f8_tile(F8Args a, int 
     m = min(m, t.rows - 1);
     return a.order ? (int)min((unsigned)order[at * BM + m], (unsigned)(a.rows - 1)) : t.p0 + m;
   };
-  unsigned block = blockIdx.x;
-  Place cur = locate(block);
+  Place cur = locate();
   if (!cur.any) return;
   int place = 0;
   if (a.order) {
@@ -860,7 +859,7 @@ __global__ __launch_bounds__(C::T, C::TWO ? 4 : 2) void k_f8_tile(F8Args a, int 
   };
   for (;;) {
     if constexpr (ON) {
-      next = locate(block += gridDim.x);
+      next = locate();
       if (next.any && a.order) bring_rows(next.t, place == 2 ? 0 : place + 1);
     }
 #pragma unroll

@@ -36,4 +36,13 @@ __host__ __device__ __forceinline__ TileAt tile_at(unsigned block, int tiles_n, 
   return o;
 }
 
+// The same for a workgroup that goes on from tile to tile in steps of the grid (a multiple of 8, so it stays on its
+// XCD's run): `block` is the number it looks at next, and moves on with every tile it is given, taken or passed.
+__host__ __device__ __forceinline__ TileAt next_tile(unsigned& block, unsigned grid, int tiles_n, int tiles_m, int count,
+                                                     int parts, int band_rows) {
+  const TileAt at = tile_at(block, tiles_n, tiles_m, count, parts, band_rows);
+  block += grid;
+  return at;
+}
+
 }  // namespace moe
