@@ -857,6 +857,12 @@ __global__ __launch_bounds__(C::T, C::TWO ? 4 : 2) void k_f8_tile(F8Args a, int 
       }
     }
   };
+  // The counts of `slack` hold for loads and stores in the order written here: none may move over these places.
+  auto in_order = [&]() {
+    if constexpr (!ON) return;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
   for (;;) {
     if constexpr (ON) {
       next = locate();
@@ -877,9 +883,11 @@ __global__ __launch_bounds__(C::T, C::TWO ? 4 : 2) void k_f8_tile(F8Args a, int 
         first_loads();
       }
     }
+    in_order();
     auto row_of = [&](int m) { return y_row_at(cur.t, place, m); };
     if constexpr (KG == 1) {
       tile_end<C>(a, cur.t, row_of, cur.i0, cur.tn, tiles_n, wm, wn, parts, cur.part, 0, acc);
+      in_order();
     } else {
       // each group gives the other half of its fragment rows away and adds what it gets
       f32x4* swap = reinterpret_cast<f32x4*>(lds) + (wv * C::MO * NF) * 64 + lane;
