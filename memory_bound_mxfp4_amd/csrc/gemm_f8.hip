@@ -814,7 +814,11 @@ __global__ __launch_bounds__(C::T, C::TWO ? 4 : 2) void k_f8_tile(F8Args a, int 
     landed(min(R - 1, mine - 1));
     pass();
     if (mine > 0) first_reads();
-    // Stages that are followed by another and whose loads are whole ones go first.
+    // Stages that are followed by another and whose loads are whole ones go first.  The FB loads of the very first turn
+    // bring what first_loads() has asked for already, the same bytes to the same places of stage R - 1: a copy that
+    // lands while another wave reads that buffer changes nothing, since every dword it writes holds the value it
+    // has, and it lands before the next stage of that buffer does, as a wave's loads do in their order.  (Leaving
+    // them out by a branch spilled registers: 4096 tokens, 8 of 64 experts, SwiGLU of 2 x 1536, K 7168 1280 us for 775.)
     const int loads_whole = (K / KS - s0 - kg + KG - 1) / KG;  // of this group's stages, those of 128 codes come first
     const int ahead = min(mine, loads_whole) - (2 * R - 1);     // the pass at t loads up to stage t + 2 R - 1
     int t = 0;
