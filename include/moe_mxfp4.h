@@ -509,8 +509,8 @@ moe_status quant_rows_f8(const void* x, moe_dtype dtype, size_t x_stride, int ro
  * types.  A block's two scales should have a product among fp32's normal
  * numbers (that of two scales above 2^-63 has); below that it loses bits.
  * 1 <= m <= MOE_MAX_ROWS, 1 <= n <= 2^20, k a multiple of 16 in 16 .. 65536;
- * MOE_ERR_UNSUPPORTED also where its tiles make 2^22 workgroups or more (an
- * output of some 10^10 elements, fewer with few rows an expert).  16-byte aligned x
+ * MOE_ERR_UNSUPPORTED also where the tiles of every kernel make 2^22 workgroups or
+ * more (an output of some 10^10 elements, fewer with few rows an expert).  16-byte aligned x
  * (x_stride a multiple of 16) if it is E4M3, else aligned to its element; w
  * and y 16-byte aligned.
  */

@@ -1041,6 +1041,7 @@ F8Plan f8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu, b
   const double per = (double)rows / used, read = (double)used * n * P * k / 6.6e6;
   F8Plan best{-1, 0, 1, 0};
   double least = 0.0;
+  bool launchable = false;
   for (int kind = 0; kind < kKinds[wide]; ++kind) {
     const Tiling& m = kTilings[wide][kind];
     const int cols = (n * P + m.bn - 1) / m.bn;
@@ -1069,8 +1070,11 @@ F8Plan f8_plan(int rows, int experts, bool grouped, int n, int k, bool swiglu, b
         else time -= saved;
       }
     }
-    if (best.kind >= 0 && time >= least) continue;
+    // a kernel whose workgroups a launch does not hold only where no other one's fit either
+    const bool fits = (size_t)cols * parts * (grouped ? max_tiles(rows, experts, m.bm) : (rows + m.bm - 1) / m.bm) < kMaxGroups;
+    if (best.kind >= 0 && (fits == launchable ? time >= least : launchable)) continue;
     least = time;
+    launchable = fits;
     best = F8Plan{kind, m.bm, parts, parts > 1 ? (size_t)parts * rows * cols * m.bn * 4 : 0};
   }
   return best;

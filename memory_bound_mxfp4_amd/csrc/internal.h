@@ -117,6 +117,11 @@ hipError_t launch_route(const void* logits, int dtype, size_t row_stride, int ro
 // of its positions: {expert | positions << 16, first position}.
 constexpr int kTileMaps = 4;
 constexpr int kTileRows[kTileMaps] = {16, 64, 128, 256};
+// The most tiles of that many rows that slots of so many experts make: whole ones, and an end of each expert.
+inline int max_tiles(size_t slots, int num_experts, int tile_rows) {
+  const size_t ends = (size_t)num_experts + 1;
+  return (int)(slots / tile_rows + (slots < ends ? slots : ends));
+}
 struct TileMaps {
   int2* t[kTileMaps];
 };

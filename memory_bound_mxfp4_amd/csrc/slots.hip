@@ -19,8 +19,7 @@ GroupsLayout groups_layout(int tokens, int top_k, int E) {
   o += 256;
   for (int i = 0; i < kTileMaps; ++i) {
     g.tiles[i] = o;
-    const size_t partial = slots < (size_t)E + 1 ? slots : (size_t)E + 1;
-    g.max_tiles[i] = (int)(slots / kTileRows[i] + partial);
+    g.max_tiles[i] = max_tiles(slots, E, kTileRows[i]);
     o += align256(8 * (size_t)g.max_tiles[i]);
   }
   // workgroups of the sort: one up to kOneBlock slots, then one for that many, at most 64
