@@ -503,11 +503,19 @@ moe_status quant_rows_f8(const void* x, moe_dtype dtype, size_t x_stride, int ro
  *             initialisation and holds nothing between calls.
  * Neither y nor the workspace's gemm_f8_workspace_size(...) bytes overlap the
  * rows of x, w, either scale or each other.
- * The products of a block are summed in fp32 by the matrix units, each block's
- * sum is multiplied by fp32(x_scale * w_scale) and added in fp32; SwiGLU runs in
- * fp32 on the two sums.  The order of the blocks is fixed for given sizes and
- * types.  A block's two scales should have a product among fp32's normal
- * numbers (that of two scales above 2^-63 has); below that it loses bits.
+ * The products of a block are summed by the matrix units, each block's sum is
+ * multiplied by fp32(x_scale * w_scale) and added in fp32; SwiGLU runs in fp32 on
+ * the two sums.  The order of the blocks is fixed for given sizes and types.
+ * With y_dtype fp32, and in gemm_f8 of up to 16 rows, the products are summed in
+ * fp32.  Other bf16 and fp16 outputs may come from the matrix units' 8-bit
+ * products: of the products of each 8 consecutive k (0..7, 8..15, ...) these lose
+ * what lies below 2^-13 of the power of two at or under the largest of them.  Of
+ * normal values that is 1.2e-5 of a sum (the output's own rounding is 1.7e-3 of it
+ * in bf16, 2e-4 in fp16), at the most 7 * 2^-13 of the sum of the terms'
+ * magnitudes, which shows where large terms cancel: ask for fp32 outputs there.
+ * So the last bits of a row go by how many rows share its call.
+ * A block's two scales should have a product among fp32's normal numbers (that of
+ * two scales above 2^-63 has); below that it loses bits.
  * 1 <= m <= MOE_MAX_ROWS, 1 <= n <= 2^20, k a multiple of 16 in 16 .. 65536;
  * MOE_ERR_UNSUPPORTED also where the tiles of every kernel make 2^22 workgroups or
  * more (an output of some 10^10 elements, fewer with few rows an expert).  16-byte aligned x

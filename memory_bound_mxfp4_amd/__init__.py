@@ -786,7 +786,9 @@ def _f8_operands(x, x_scale, w, w_scale, swiglu: bool, lead: tuple):
 def gemm_f8(x, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dtype=None, ws=None, stream=None):
     """y = x w^T in 8-bit floating point (gemm_f8): x [m][k] float rows, quantised on the way, or float8_e4m3fn codes
     with x_scale [ceil(k / 128)][m]; w float8_e4m3fn [n][k] with w_scale [ceil(n / 128)][ceil(k / 128)], or [2][..][..]
-    both with swiglu. Returns y [m][n] in out's type, out_dtype or bfloat16; neither out nor ws overlaps an input."""
+    both with swiglu. Returns y [m][n] in out's type, out_dtype or bfloat16; neither out nor ws overlaps an input. The
+    products are summed in fp32 where y is float32 or has up to 16 rows; other 16-bit outputs may lose what lies below
+    2^-13 of the largest of 8 neighbouring products, which matters where large ones cancel."""
     m, k, stride, n, code = _f8_operands(x, x_scale, w, w_scale, swiglu, ())
     dev = x.device
     y = _out(out, (m, n), out_dtype, dev, stream)
@@ -806,7 +808,8 @@ def experts_gemm_f8_workspace_size(groups: SlotGroups, x_rows: int, n: int, k: i
 def experts_gemm_f8(x, groups: SlotGroups, w, w_scale, x_scale=None, swiglu: bool = False, out=None, out_dtype=None,
                     ws=None, stream=None):
     """gemm_f8 of every slot with its expert's matrix (experts_gemm_f8): x has a row per token or per slot, w is
-    float8_e4m3fn [num_experts][n][k] (or [num_experts][2][n][k] with swiglu). Returns y [tokens * top_k][n]."""
+    float8_e4m3fn [num_experts][n][k] (or [num_experts][2][n][k] with swiglu). Returns y [tokens * top_k][n]; its sums are
+    those of gemm_f8, in fp32 where y is float32."""
     E = groups.num_experts
     rows, k, stride, n, code = _f8_operands(x, x_scale, w, w_scale, swiglu, (E,))
     dev = x.device
