@@ -368,9 +368,11 @@ hipError_t launch_f8_token(const F8Args& a, const void* x, int dtype, int max_ti
 // stages kept in ST buffers: the loads of stage k + ST - 1 are issued, straight
 // into LDS, before stage k is computed.  Each wave also brings the scales of the rows of x
 // that it multiplies itself, and of its matrix rows, which lie in one block.
-// Bound by the matrix units under the power limit where there are tiles for all CUs: 8192 x 8192 x 7168 396 us
-// (2430 TFLOP/s; of zeros 338, 2850), by the latency of a stage where there are few: 509 rows, SwiGLU of
-// 2 x 1536, K 7056 28 us in 192 tiles of 64 x 128.
+// Bound by the matrix units under the power limit where there are tiles for all CUs: 8192 x 8192 x 7168 375 to 396 us
+// on different cards (2430 to 2570 TFLOP/s; of zeros 291 to 338), by the latency of a stage where there are few: 509
+// rows, SwiGLU of 2 x 1536, K 7056 28 us in 192 tiles of 64 x 128.  Products in fp16 keep the matrix units busy for 44% of
+// the time instead of 68: every wave widens the codes it reads, with nearly four times the vector instructions, and adds a
+// sum as soon as its products end (8192 rows of 7168 x 7168 to fp32 840 us, of zeros 770).
 
 // One tile configuration: BM rows of x by BN matrix rows (P matrices
 // interleaved), KG groups of WGM x WGN waves that take the stages in turn, ST
@@ -755,8 +757,8 @@ __global__ __launch_bounds__(C::T, C::TWO ? 4 : 2) void k_f8_tile(F8Args a, int 
     };
     // Of a stage's loads, FA are issued with the last columns of the stage whose buffer they take, the other FB
     // with the first columns of the next: a wave that waits to issue a load multiplies nothing.
-    // (8192 x 8192 x 7168 404.5 us with all of them there, 403.4 with a third here, 411 with half; 2 x 1536, K 7168,
-    // 16384 rows: 314, 307, 310.)
+    // (8192 x 8192 x 7168, in turn on one card: 383 us with all of them there, 375 with a third here, 368 with half; 2 x
+    // 1536, K 7168, 16384 rows: 300, 296, 290.  On another card half was the slowest: 404.5, 403.4, 411; 314, 307, 310.)
     constexpr int FB = F0 > 0 ? LU / 3 : 0, FA = LU - FB;
     // The first columns; `loads`: with the rest of stage st's to buffer b.
     auto first_columns = [&](int st, int b, auto loads) {
