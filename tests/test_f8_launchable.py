@@ -56,7 +56,7 @@ def test_no_product_is_refused_that_some_kernel_takes():
         assert plan.tile_rows == ROWS[plan.kind]
         if not fits:
             refused += 1
-            few = 3 if not grouped and rows > 16 else 0  # a dense product of many rows is never a stream
+            few = 1 if not grouped and rows > 16 else 0  # a dense product of many rows is never a stream
             assert not any(_fits(kind, rows, experts, grouped, n, swiglu) for kind in range(few, 4 if wide else 6)), \
                 (rows, experts, grouped, n, k, swiglu, wide, plan.kind)
     assert refused
